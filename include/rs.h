@@ -17,6 +17,11 @@
  *   rs_compact_positive_f32 keep x > 0 in order, zero-fill the rest, count
  *   rs_compact_positive_f32_noalloc  the same with static scratch (no temp)
  *   rs_bitonic_tile         sort each run of at most 1024 keys in LDS
+ *   rs_route_topk           best experts of each row of router scores, weights
+ *   rs_route_topk_grad      gradient of those weights for the scores
+ *   rs_group_choices        choices ordered by expert, stably, padded segments
+ *   rs_token_logprobs       log probability, entropy, rank, top alternatives
+ *   rs_token_logprobs_grad  gradient of those for the logits
  *   rs_status_string        text of a status code
  *
  * Common rules.
@@ -74,10 +79,11 @@ extern "C" {
 typedef enum rs_status {
     RS_OK = 0,
     RS_ERR_INVALID_VALUE = 1,    /* null pointer with n > 0, bad bit range, bad tile */
-    RS_ERR_UNSUPPORTED_SIZE = 2, /* n >= 2^30 (2^29 for 8-byte and two-key sorts) */
+    RS_ERR_UNSUPPORTED_SIZE = 2, /* n >= 2^30 (2^29 for 8-byte and two-key sorts), or a count of
+                                    the calls on rows of scores over its limit */
     RS_ERR_TEMP_TOO_SMALL = 3,   /* *temp_bytes below the queried size */
     RS_ERR_OVERLAP = 4,          /* two of the buffers overlap */
-    RS_ERR_MISALIGNED = 5,       /* a pointer is not 16-byte aligned */
+    RS_ERR_MISALIGNED = 5,       /* a pointer is not aligned (to 16 bytes unless the call says less) */
     RS_ERR_HIP = 6               /* a HIP launch or runtime call failed */
 } rs_status;
 
@@ -310,6 +316,155 @@ rs_status rs_compact_positive_f32_noalloc(const float *in, float *out, uint32_t 
 rs_status rs_bitonic_tile(const uint32_t *keys_in, uint32_t *keys_out, uint64_t n,
                           uint32_t tile, int begin_bit, int end_bit, hipStream_t stream);
 
+/*
+ * Rows of scores: the select of the best k of each row, with the
+ * probabilities that a language model's router or output layer gives them.
+ *
+ * A matrix of rows is a device pointer, a row stride in elements and an
+ * element type; its rows hold `experts` or `vocab` elements next to each
+ * other.  Matrices need only the alignment of their elements, and other
+ * arrays of these calls that of theirs (4 bytes); rows that start on 16-byte
+ * boundaries are read fastest.  An input's row stride may be any number (0
+ * repeats one row); a written matrix's must be at least its row length, and
+ * elements between its rows are left as they are.  Scores, logits and
+ * gradients are converted to f32 when read; gradients are rounded to their
+ * matrix's type once, when stored (to nearest, ties to even).
+ *
+ * Order within a row: by value, larger first; equal values (and -0.0 and
+ * +0.0 are equal) by index, lower first; a NaN comes after -inf.
+ */
+typedef enum rs_elem_type {
+    RS_ELEM_F32 = 0,
+    RS_ELEM_F16 = 1,
+    RS_ELEM_BF16 = 2
+} rs_elem_type;
+
+typedef enum rs_score_fn {
+    RS_SCORE_SOFTMAX = 0,   /* p = exp(x) / sum of exp over the row */
+    RS_SCORE_SIGMOID = 1    /* p = 1 / (1 + exp(-x)) */
+} rs_score_fn;
+
+#define RS_MAX_EXPERTS 1024   /* experts of a router, segments of a grouping */
+#define RS_MAX_GROUPS 64      /* expert groups of a router */
+#define RS_MAX_TOP_K 64       /* experts a row chooses, alternatives of a row */
+
+/*
+ * Routing: the top_k experts of every row of scores [rows, experts] and their
+ * weights.  p = the score function of the row (softmax over all its experts).
+ * An expert is chosen by s = p + bias[e], computed in 64 bits, or without a
+ * bias (NULL) by its score; an expert whose score is -inf or NaN, or whose s
+ * is -inf or NaN, is masked: it comes after every other.
+ *   groups > 1: expert e is in group e / (experts / groups); a group's score
+ *   is the sum of the group_best (1 or 2) largest s of its experts that are
+ *   not masked (s = p there without a bias; with group_best 1 the largest
+ *   score), and -inf if all are; the top_groups groups with the largest
+ *   scores (ties to the lower group) are kept, and the experts of the others
+ *   cannot be chosen.
+ *   ids [rows, top_k]: the chosen experts, in decreasing s, ties to the lower
+ *   expert.  They are always distinct and below `experts`.
+ *   weights [rows, top_k] f32: scale * p, or with renormalize != 0
+ *   scale * p / (sum of the row's chosen p), 0 where that sum is 0.  A masked
+ *   expert's p is 0 if its score is -inf, and a softmax row of nothing but
+ *   -inf has p = 0.  A NaN or +inf in a softmax row makes its weights NaN.
+ * 1 <= experts <= RS_MAX_EXPERTS, 1 <= groups <= RS_MAX_GROUPS and a divisor
+ * of experts, 1 <= top_groups <= groups, group_best 1 or 2 and at most
+ * experts / groups, 1 <= top_k <= min(RS_MAX_TOP_K, top_groups * experts /
+ * groups), scale finite and above 0, rows < 2^30.  No temp.
+ */
+rs_status rs_route_topk(rs_elem_type elem_type, const void *scores, uint64_t row_stride,
+                        const float *bias, uint64_t rows, uint32_t experts, uint32_t top_k,
+                        rs_score_fn score_fn, uint32_t groups, uint32_t top_groups,
+                        uint32_t group_best, int renormalize, float scale, uint32_t *ids,
+                        float *weights, hipStream_t stream);
+
+/*
+ * Gradient of the routing weights for the scores.  dweights [rows, top_k] f32
+ * is the gradient of the weights that rs_route_topk gave with ids, weights
+ * and the same scores, score function, renormalize and scale.  With
+ * D = sum over the row's choices of dweights * weights, and
+ * g_j = dweights_j - D / scale (renormalised) or dweights_j (otherwise):
+ *   softmax: dscores_e = weights_j g_j summed over the choices j of e, less
+ *            p_e D if not renormalised (then it reaches every expert);
+ *   sigmoid: dscores_e = weights_j (1 - p_e) g_j summed likewise.
+ * The choice itself and the bias have no gradient.  Every element of dscores
+ * [rows, experts] (of elem_type, as the scores) is written.  A choice of
+ * `experts` or above is passed over; an expert chosen twice gets both terms.
+ */
+rs_status rs_route_topk_grad(rs_elem_type elem_type, const void *scores, uint64_t row_stride,
+                             const uint32_t *ids, const float *weights, const float *dweights,
+                             uint64_t rows, uint32_t experts, uint32_t top_k, rs_score_fn score_fn,
+                             int renormalize, float scale, void *dscores, uint64_t dscores_stride,
+                             hipStream_t stream);
+
+/*
+ * Grouping: the n choices ids [n] (a router's ids, row by row) ordered by
+ * expert, equal ones in input order: the stable partition with one side for
+ * each expert.  Each expert's segment is padded to a multiple of `align`, so
+ * that a matrix product over tiles of `align` rows has one expert a tile.
+ *   counts [experts]       choices of each expert
+ *   starts [experts + 1]   first position of each expert's segment; the last
+ *                          is the length of all segments
+ *   order  [n + experts * (align - 1)]  the choice (index into ids) at each
+ *                          position, 0xFFFFFFFF in the padding and behind the
+ *                          last segment; every element is written
+ *   place  [n]             each choice's position in order, 0xFFFFFFFF for a
+ *                          choice whose id is `experts` or above (it belongs
+ *                          to no segment)
+ * 1 <= experts <= RS_MAX_EXPERTS, align >= 1, n + experts * (align - 1) <
+ * 2^30.  ids, order and place need 16-byte alignment as the sorts' arrays.
+ * Temp with the query idiom (d_temp == NULL writes the size, which depends
+ * only on n and experts).
+ */
+rs_status rs_group_choices(const uint32_t *ids, uint64_t n, uint32_t experts, uint32_t align,
+                           uint32_t *order, uint32_t *place, uint32_t *starts, uint32_t *counts,
+                           void *d_temp, size_t *temp_bytes, hipStream_t stream);
+
+/*
+ * Log probabilities.  For every row x of logits [rows, vocab], with
+ * c = scale (an inverse temperature):
+ *   stats [rows, 2] f32: m = the largest logit, s = sum of exp(c (x - m));
+ *   lse      [rows] f32: c m + ln s
+ *   entropy  [rows] f32: of p = exp(c (x - m)) / s, in nats
+ *   logprob  [rows] f32: ln p of the row's target, 0 for a row without one
+ *   rank     [rows] u32: logits before the target's in the row's order (0: it
+ *            is the first), 0xFFFFFFFF for a row without target or whose
+ *            target's logit is NaN
+ *   top_ids [rows, top_k] u32, top_logprobs [rows, top_k] f32: the first
+ *            top_k logits in the row's order and their ln p.
+ * targets [rows]: a target of `vocab` or above means none.  A row of nothing
+ * but -inf has m = -inf, s = 0, lse = -inf, entropy 0, and -inf for every ln
+ * p; a NaN or +inf in a row makes its lse, entropy, s and ln p NaN.
+ * stats must be given; targets may be NULL (then logprob and rank too), and
+ * any of lse, entropy, logprob and rank; top_ids and top_logprobs are both
+ * NULL with top_k == 0 and both given otherwise.  1 <= vocab < 2^30, rows <
+ * 2^30, top_k <= min(vocab, RS_MAX_TOP_K), 2^-60 <= scale <= 2^60.
+ * Temp with the query idiom; the size depends on rows, vocab and top_k.
+ */
+rs_status rs_token_logprobs(rs_elem_type elem_type, const void *logits, uint64_t row_stride,
+                            const uint32_t *targets, uint64_t rows, uint32_t vocab, float scale,
+                            uint32_t top_k, float *stats, float *lse, float *entropy,
+                            float *logprob, uint32_t *rank, uint32_t *top_ids, float *top_logprobs,
+                            void *d_temp, size_t *temp_bytes, hipStream_t stream);
+
+/*
+ * Gradient for the logits of a sum over rows of dlogprob * logprob + dentropy
+ * * entropy + dlse * lse (each f32 [rows], or NULL for none):
+ *   dlogits_i = c ( dlogprob ([i = target] - p_i) + dlse p_i
+ *                   - dentropy p_i (ln p_i + entropy) )
+ * with the stats (and, with dentropy, the entropy) that rs_token_logprobs
+ * gave for the same logits and scale.  A row without target has no gradient
+ * through logprob, a row of nothing but -inf none at all, and a logit of
+ * -inf none.  Every element of dlogits [rows, vocab] (of elem_type, as the
+ * logits) is written; dlogits may be the logits themselves (with the same
+ * stride), otherwise the two must not overlap.  targets must be given with
+ * dlogprob.  At least one of the three gradients must be given.
+ */
+rs_status rs_token_logprobs_grad(rs_elem_type elem_type, const void *logits, uint64_t row_stride,
+                                 const uint32_t *targets, const float *stats, const float *entropy,
+                                 uint64_t rows, uint32_t vocab, float scale, const float *dlogprob,
+                                 const float *dentropy, const float *dlse, void *dlogits,
+                                 uint64_t dlogits_stride, hipStream_t stream);
+
 /* Static text for a status code (never NULL). */
 const char *rs_status_string(rs_status status);
 
@@ -341,7 +496,15 @@ typedef enum rs_kernel_id {
     RS_KERNEL_SCAN = 10,        /* single-pass prefix sum */
     RS_KERNEL_SELECT_INIT = 11, /* clears select/partition counters and states */
     RS_KERNEL_SELECT_COUNT = 12,/* partition: kept elements of the whole input */
-    RS_KERNEL_SELECT = 13       /* single-pass select / partition */
+    RS_KERNEL_SELECT = 13,      /* single-pass select / partition */
+    RS_KERNEL_ROUTE = 14,       /* a router's choices and weights */
+    RS_KERNEL_ROUTE_GRAD = 15,  /* their gradient */
+    RS_KERNEL_GROUP_COUNT = 16, /* grouping: each tile's choices by expert */
+    RS_KERNEL_GROUP_SCAN = 17,  /* grouping: segments, tiles' offsets in them */
+    RS_KERNEL_GROUP_PLACE = 18, /* grouping: choices to their places */
+    RS_KERNEL_LOGPROBS = 19,    /* one read of the logits: sums, rank, top alternatives */
+    RS_KERNEL_LOGPROBS_JOIN = 20, /* joins the parts of rows that were split */
+    RS_KERNEL_LOGPROBS_GRAD = 21  /* the logits' gradient */
 } rs_kernel_id;
 
 rs_status rs_timing_enable(int enable);

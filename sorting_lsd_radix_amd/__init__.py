@@ -13,6 +13,7 @@ fallback implementation.  ``use_library(path)`` binds the functions to another
 build of the same sources (the tests use it for the build with the ballot rank
 forced on every path, ``librs_ballot.so``).
 """
+import collections
 import ctypes
 import os
 
@@ -24,7 +25,10 @@ __all__ = [
     "rs_sort_two_keys_u32", "rs_digit_counts", "rs_compact_positive_f32",
     "rs_compact_positive_f32_noalloc", "rs_exclusive_scan_u32", "rs_inclusive_scan_u32",
     "rs_select", "rs_partition", "RS_OP_LT", "RS_OP_LE", "RS_OP_GT", "RS_OP_GE", "RS_OP_EQ",
-    "RS_OP_NE", "rs_bitonic_tile", "rs_status_string", "rs_timing_enable", "rs_timing_collect",
+    "RS_OP_NE", "RS_ELEM_F32", "RS_ELEM_F16", "RS_ELEM_BF16", "RS_SCORE_SOFTMAX",
+    "RS_SCORE_SIGMOID", "rs_route_topk", "rs_route_topk_grad", "rs_group_choices",
+    "rs_token_logprobs", "rs_token_logprobs_grad", "route_topk", "route_topk_grad",
+    "group_choices", "token_logprobs", "token_logprobs_grad", "TokenLogprobs", "rs_bitonic_tile", "rs_status_string", "rs_timing_enable", "rs_timing_collect",
     "exclusive_scan_u32", "inclusive_scan_u32", "select", "partition",
     "sort_keys_u32", "sort_pairs_u32", "sort_pairs_f32", "sort_keys", "sort_pairs",
     "sort_two_keys_u32", "digit_counts", "compact_positive_f32", "bitonic_tile",
@@ -60,7 +64,13 @@ RS_KERNEL_TILE_SORT = 7
 RS_KERNEL_BUCKET_SORT = 8
 KERNEL_NAMES = {0: "upsweep", 1: "onesweep", 2: "sort_init", 3: "compact_init",
                 4: "compact", 5: "bitonic", 6: "copy", 7: "tile_sort", 8: "bucket_sort",
-                9: "scan_init", 10: "scan", 11: "select_init", 12: "select_count", 13: "select"}
+                9: "scan_init", 10: "scan", 11: "select_init", 12: "select_count", 13: "select",
+                14: "route", 15: "route_grad", 16: "group_count", 17: "group_scan",
+                18: "group_place", 19: "logprobs", 20: "logprobs_join", 21: "logprobs_grad"}
+
+RS_ELEM_F32, RS_ELEM_F16, RS_ELEM_BF16 = range(3)
+RS_SCORE_SOFTMAX, RS_SCORE_SIGMOID = range(2)
+_SCORES = {"softmax": RS_SCORE_SOFTMAX, "sigmoid": RS_SCORE_SIGMOID}
 
 RS_OP_LT, RS_OP_LE, RS_OP_GT, RS_OP_GE, RS_OP_EQ, RS_OP_NE = range(6)
 _OPS = {"<": RS_OP_LT, "<=": RS_OP_LE, ">": RS_OP_GT, ">=": RS_OP_GE, "==": RS_OP_EQ,
@@ -70,7 +80,8 @@ EXPORTED_SYMBOLS = ["rs_sort_keys_u32", "rs_sort_pairs_u32", "rs_sort_pairs_f32"
                     "rs_sort_keys", "rs_sort_pairs", "rs_sort_two_keys_u32", "rs_digit_counts",
                     "rs_compact_positive_f32", "rs_compact_positive_f32_noalloc",
                     "rs_exclusive_scan_u32", "rs_inclusive_scan_u32", "rs_select", "rs_partition",
-                    "rs_bitonic_tile", "rs_status_string",
+                    "rs_bitonic_tile", "rs_route_topk", "rs_route_topk_grad", "rs_group_choices",
+                    "rs_token_logprobs", "rs_token_logprobs_grad", "rs_status_string",
                     "rs_timing_enable", "rs_timing_collect"]
 
 _lib = None
@@ -128,6 +139,19 @@ def _load():
     for f in (lib.rs_sort_keys_u32, lib.rs_sort_pairs_u32, lib.rs_sort_pairs_f32, lib.rs_sort_keys,
               lib.rs_sort_pairs, lib.rs_sort_two_keys_u32, lib.rs_digit_counts,
               lib.rs_compact_positive_f32, lib.rs_bitonic_tile):
+        f.restype = i32
+    f32 = ctypes.c_float
+    lib.rs_route_topk.argtypes = [i32, vp, u64, vp, u64, u32, u32, i32, u32, u32, u32, i32, f32,
+                                  vp, vp, vp]
+    lib.rs_route_topk_grad.argtypes = [i32, vp, u64, vp, vp, vp, u64, u32, u32, i32, i32, f32, vp,
+                                       u64, vp]
+    lib.rs_group_choices.argtypes = [vp, u64, u32, u32, vp, vp, vp, vp, vp, szp, vp]
+    lib.rs_token_logprobs.argtypes = [i32, vp, u64, vp, u64, u32, f32, u32, vp, vp, vp, vp, vp, vp,
+                                      vp, vp, szp, vp]
+    lib.rs_token_logprobs_grad.argtypes = [i32, vp, u64, vp, vp, vp, u64, u32, f32, vp, vp, vp, vp,
+                                           u64, vp]
+    for f in (lib.rs_route_topk, lib.rs_route_topk_grad, lib.rs_group_choices,
+              lib.rs_token_logprobs, lib.rs_token_logprobs_grad):
         f.restype = i32
     lib.rs_status_string.argtypes = [i32]
     lib.rs_status_string.restype = ctypes.c_char_p
@@ -307,6 +331,65 @@ def rs_bitonic_tile(keys_in, keys_out, n, tile, begin_bit, end_bit, stream=None)
     st = _load().rs_bitonic_tile(_ptr(keys_in), _ptr(keys_out), int(n), int(tile),
                                  int(begin_bit), int(end_bit), _stream(stream))
     _call("rs_bitonic_tile", st)
+
+
+def rs_route_topk(elem_type, scores, row_stride, bias, rows, experts, top_k, score_fn, groups,
+                  top_groups, group_best, renormalize, scale, ids, weights, stream=None):
+    """C: rs_route_topk."""
+    st = _load().rs_route_topk(int(elem_type), _ptr(scores), int(row_stride), _ptr(bias), int(rows),
+                               int(experts), int(top_k), int(score_fn), int(groups),
+                               int(top_groups), int(group_best), int(bool(renormalize)),
+                               float(scale), _ptr(ids), _ptr(weights), _stream(stream))
+    _call("rs_route_topk", st)
+
+
+def rs_route_topk_grad(elem_type, scores, row_stride, ids, weights, dweights, rows, experts, top_k,
+                       score_fn, renormalize, scale, dscores, dscores_stride, stream=None):
+    """C: rs_route_topk_grad."""
+    st = _load().rs_route_topk_grad(int(elem_type), _ptr(scores), int(row_stride), _ptr(ids),
+                                    _ptr(weights), _ptr(dweights), int(rows), int(experts),
+                                    int(top_k), int(score_fn), int(bool(renormalize)),
+                                    float(scale), _ptr(dscores), int(dscores_stride),
+                                    _stream(stream))
+    _call("rs_route_topk_grad", st)
+
+
+def rs_group_choices(ids, n, experts, align, order, place, starts, counts, d_temp, temp_bytes,
+                     stream=None):
+    """C: rs_group_choices.  With d_temp None, returns the temp size."""
+    size = ctypes.c_size_t(0 if temp_bytes is None else int(temp_bytes))
+    st = _load().rs_group_choices(_ptr(ids), int(n), int(experts), int(align), _ptr(order),
+                                  _ptr(place), _ptr(starts), _ptr(counts), _ptr(d_temp),
+                                  ctypes.byref(size),
+                                  _stream(stream) if d_temp is not None else None)
+    _call("rs_group_choices", st)
+    return size.value if d_temp is None else None
+
+
+def rs_token_logprobs(elem_type, logits, row_stride, targets, rows, vocab, scale, top_k, stats, lse,
+                      entropy, logprob, rank, top_ids, top_logprobs, d_temp, temp_bytes,
+                      stream=None):
+    """C: rs_token_logprobs.  With d_temp None, returns the temp size."""
+    size = ctypes.c_size_t(0 if temp_bytes is None else int(temp_bytes))
+    st = _load().rs_token_logprobs(int(elem_type), _ptr(logits), int(row_stride), _ptr(targets),
+                                   int(rows), int(vocab), float(scale), int(top_k), _ptr(stats),
+                                   _ptr(lse), _ptr(entropy), _ptr(logprob), _ptr(rank),
+                                   _ptr(top_ids), _ptr(top_logprobs), _ptr(d_temp),
+                                   ctypes.byref(size),
+                                   _stream(stream) if d_temp is not None else None)
+    _call("rs_token_logprobs", st)
+    return size.value if d_temp is None else None
+
+
+def rs_token_logprobs_grad(elem_type, logits, row_stride, targets, stats, entropy, rows, vocab,
+                           scale, dlogprob, dentropy, dlse, dlogits, dlogits_stride, stream=None):
+    """C: rs_token_logprobs_grad."""
+    st = _load().rs_token_logprobs_grad(int(elem_type), _ptr(logits), int(row_stride),
+                                        _ptr(targets), _ptr(stats), _ptr(entropy), int(rows),
+                                        int(vocab), float(scale), _ptr(dlogprob), _ptr(dentropy),
+                                        _ptr(dlse), _ptr(dlogits), int(dlogits_stride),
+                                        _stream(stream))
+    _call("rs_token_logprobs_grad", st)
 
 
 def rs_timing_enable(enable):
@@ -524,4 +607,188 @@ def bitonic_tile(keys, tile, begin_bit=0, end_bit=32, out=None, stream=None):
     _check_tensor(keys, torch.uint32, "keys")
     out = torch.empty_like(keys) if out is None else out
     rs_bitonic_tile(keys, out, keys.numel(), tile, begin_bit, end_bit, stream)
+    return out
+
+
+# --- rows of scores -------------------------------------------------------------------
+
+def _rows(t, name, dtype=None):
+    """(elem_type, rows, columns, row stride) of a matrix whose rows are dense."""
+    import torch
+    table = {torch.float32: RS_ELEM_F32, torch.float16: RS_ELEM_F16, torch.bfloat16: RS_ELEM_BF16}
+    if not t.is_cuda or t.dim() != 2 or t.dtype not in table or \
+            (t.stride(1) != 1 and t.shape[1] > 1):
+        raise TypeError("%s must be a 2-D CUDA tensor of float32, float16 or bfloat16 whose rows "
+                        "are contiguous" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be of %s" % (name, dtype))
+    return table[t.dtype], t.shape[0], t.shape[1], t.stride(0)
+
+
+def _check_like(t, name, shape, dtypes, device):
+    """A contiguous tensor of `shape`, one of `dtypes`, on `device`."""
+    if t.device != device or t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or \
+            not t.is_contiguous():
+        raise TypeError("%s must be a contiguous tensor of shape %s and %s on %s"
+                        % (name, tuple(shape), " or ".join(str(d) for d in dtypes), device))
+
+
+class _On:
+    """The device of a call's tensors as the current one, and the stream it runs on as torch's
+    current one, so that what the call allocates belongs to that stream."""
+
+    def __init__(self, device, stream):
+        import torch
+        self._contexts = []
+        if device.index != torch.cuda.current_device():
+            self._contexts.append(torch.cuda.device(device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self._contexts.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self._contexts:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self._contexts):
+            c.__exit__(*exc)
+
+
+def _ints():
+    import torch
+    return torch.int32, torch.uint32
+
+
+def route_topk(scores, top_k, bias=None, score="softmax", groups=1, top_groups=1, group_best=1,
+               renormalize=True, scale=1.0, stream=None):
+    """The `top_k` experts of each row of router scores [rows, experts] (float32, float16 or
+    bfloat16) and their weights: (ids int32 [rows, top_k], weights float32 [rows, top_k]).
+
+    score: "softmax" (over all experts) or "sigmoid".  bias (float32 [experts]) is added to the
+    probabilities for the choice only.  With groups > 1 the choice is among the experts of the
+    top_groups groups whose group_best largest biased probabilities have the largest sum.
+    Ties go to the lower expert.  The weights are scale * p, divided by the sum of the row's
+    chosen p if renormalize."""
+    import torch
+    et, rows, experts, stride = _rows(scores, "scores")
+    if bias is not None:
+        _check_like(bias, "bias", (experts,), (torch.float32,), scores.device)
+    with _On(scores.device, stream):
+        ids = torch.empty((rows, top_k), dtype=torch.int32, device=scores.device)
+        weights = torch.empty((rows, top_k), dtype=torch.float32, device=scores.device)
+        rs_route_topk(et, scores, stride, bias, rows, experts, top_k, _SCORES[score], groups,
+                      top_groups, group_best, renormalize, scale, ids, weights)
+    return ids, weights
+
+
+def route_topk_grad(scores, ids, weights, dweights, score="softmax", renormalize=True, scale=1.0,
+                    out=None, stream=None):
+    """Gradient for the scores of the weights that route_topk gave with these ids, score,
+    renormalize and scale; dweights float32 [rows, top_k].  Returns dscores [rows, experts] of the
+    scores' type (`out`, if given: a matrix whose rows are contiguous)."""
+    import torch
+    et, rows, experts, stride = _rows(scores, "scores")
+    shape = (rows, ids.shape[-1])
+    _check_like(ids, "ids", shape, _ints(), scores.device)
+    _check_like(weights, "weights", shape, (torch.float32,), scores.device)
+    _check_like(dweights, "dweights", shape, (torch.float32,), scores.device)
+    with _On(scores.device, stream):
+        if out is None:
+            out = torch.empty((rows, experts), dtype=scores.dtype, device=scores.device)
+        _, orows, ocols, ostride = _rows(out, "out", scores.dtype)
+        if (orows, ocols) != (rows, experts) or out.device != scores.device:
+            raise TypeError("out must have the scores' shape and device")
+        rs_route_topk_grad(et, scores, stride, ids, weights, dweights, rows, experts, shape[1],
+                           _SCORES[score], renormalize, scale, out, ostride)
+    return out
+
+
+def group_choices(ids, experts, align=1, temp=None, stream=None):
+    """The choices `ids` (int32 or uint32, any shape) ordered by expert, stably, each expert's
+    segment padded to a multiple of `align`: (order, place, starts, counts), int32.
+
+    order [ids.numel() + experts * (align - 1)]: the flat index of the choice at each position,
+    -1 in the padding and behind the last segment.  place (of the ids' shape): each choice's
+    position, -1 where its id is not an expert (-1, or `experts` and above).  starts
+    [experts + 1]: where each segment begins, and the length of all.  counts [experts]."""
+    import torch
+    _check_like(ids, "ids", ids.shape, _ints(), ids.device)
+    if not ids.is_cuda:
+        raise TypeError("ids must be a CUDA tensor")
+    n = ids.numel()
+    need = rs_group_choices(None, n, experts, align, None, None, None, None, None, 0)
+    with _On(ids.device, stream):
+        order = torch.empty(n + experts * (align - 1), dtype=torch.int32, device=ids.device)
+        place = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
+        starts = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+        counts = torch.empty(experts, dtype=torch.int32, device=ids.device)
+        temp = _temp(need, ids.device) if temp is None else temp
+        rs_group_choices(ids, n, experts, align, order, place, starts, counts, temp, temp.numel())
+    return order, place, starts, counts
+
+
+TokenLogprobs = collections.namedtuple(
+    "TokenLogprobs", "logprob entropy lse rank stats top_ids top_logprobs")
+
+
+def token_logprobs(logits, targets=None, top_k=0, scale=1.0, temp=None, stream=None):
+    """Log probabilities under softmax(scale * logits) of rows of logits [rows, vocab] (float32,
+    float16 or bfloat16): a TokenLogprobs of
+
+    logprob [rows] and rank [rows] (int32: logits before the target's, 0 for the first) of the
+    targets (int32 or uint32 [rows]; -1 or `vocab` and above: none, logprob 0 and rank -1), both
+    None without targets; entropy [rows] in nats; lse [rows], the log of the sum of exp; stats
+    [rows, 2], the largest logit and the sum of exp relative to it, which token_logprobs_grad
+    takes; top_ids (int32) and top_logprobs [rows, top_k], the largest logits in order, ties to
+    the lower index, both None with top_k 0.  Floating outputs are float32."""
+    import torch
+    et, rows, vocab, stride = _rows(logits, "logits")
+    dev = logits.device
+    if targets is not None:
+        _check_like(targets, "targets", (rows,), _ints(), dev)
+    need = rs_token_logprobs(et, None, stride, None, rows, vocab, scale, top_k, None, None, None,
+                             None, None, None, None, None, 0)
+    with _On(dev, stream):
+        stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+        lse = torch.empty(rows, dtype=torch.float32, device=dev)
+        entropy = torch.empty(rows, dtype=torch.float32, device=dev)
+        logprob = rank = top_ids = top_logprobs = None
+        if targets is not None:
+            logprob = torch.empty(rows, dtype=torch.float32, device=dev)
+            rank = torch.empty(rows, dtype=torch.int32, device=dev)
+        if top_k:
+            top_ids = torch.empty((rows, top_k), dtype=torch.int32, device=dev)
+            top_logprobs = torch.empty((rows, top_k), dtype=torch.float32, device=dev)
+        temp = _temp(need, dev) if temp is None else temp
+        rs_token_logprobs(et, logits, stride, targets, rows, vocab, scale, top_k, stats, lse,
+                          entropy, logprob, rank, top_ids, top_logprobs, temp, temp.numel())
+    return TokenLogprobs(logprob, entropy, lse, rank, stats, top_ids, top_logprobs)
+
+
+def token_logprobs_grad(logits, stats, targets=None, dlogprob=None, entropy=None, dentropy=None,
+                        dlse=None, scale=1.0, out=None, stream=None):
+    """Gradient for the logits of the sum over rows of dlogprob * logprob + dentropy * entropy +
+    dlse * lse (each float32 [rows], or None), from the stats, and with dentropy the entropy, that
+    token_logprobs gave.  Returns dlogits of the logits' type and shape (`out`, if given: a matrix
+    whose rows are contiguous; it may be the logits themselves)."""
+    import torch
+    et, rows, vocab, stride = _rows(logits, "logits")
+    dev = logits.device
+    _check_like(stats, "stats", (rows, 2), (torch.float32,), dev)
+    if targets is not None:
+        _check_like(targets, "targets", (rows,), _ints(), dev)
+    for t, name in ((dlogprob, "dlogprob"), (entropy, "entropy"), (dentropy, "dentropy"),
+                    (dlse, "dlse")):
+        if t is not None:
+            _check_like(t, name, (rows,), (torch.float32,), dev)
+    with _On(dev, stream):
+        if out is None:
+            out = torch.empty((rows, vocab), dtype=logits.dtype, device=dev)
+        _, orows, ocols, ostride = _rows(out, "out", logits.dtype)
+        if (orows, ocols) != (rows, vocab) or out.device != dev:
+            raise TypeError("out must have the logits' shape and device")
+        rs_token_logprobs_grad(et, logits, stride, targets, stats, entropy, rows, vocab, scale,
+                               dlogprob, dentropy, dlse, out, ostride)
     return out

@@ -1,5 +1,6 @@
 // internal.hpp -- host-side interfaces between the C ABI (rs_api.cpp) and the
-// kernel launchers (radix.hip, compact.hip, bitonic.hip).
+// kernel launchers (radix.hip, compact.hip, scan.hip, bitonic.hip, route.hip,
+// group.hip, logprobs.hip).
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -107,5 +108,78 @@ hipError_t launch_select(int key_type, int op, uint32_t threshold_bits, const ui
 
 hipError_t launch_bitonic(const uint32_t* keys_in, uint32_t* keys_out, uint32_t n, uint32_t tile,
                           int begin_bit, int end_bit, hipStream_t stream);
+
+// ---- rows of scores -----------------------------------------------------------
+
+// Arguments of the calls on rows of scores, as in rs.h; already validated.
+struct RouteArgs {
+    const void* scores;
+    uint64_t row_stride;
+    const float* bias;
+    uint32_t rows, experts, top_k, groups, top_groups, group_best;
+    bool sigmoid, renormalize;
+    float scale;
+    uint32_t* ids;
+    float* weights;
+};
+hipError_t launch_route(int elem_type, const RouteArgs& a, hipStream_t stream);
+
+struct RouteGradArgs {
+    const void* scores;
+    uint64_t row_stride;
+    const uint32_t* ids;
+    const float* weights;
+    const float* dweights;
+    uint32_t rows, experts, top_k;
+    bool sigmoid, renormalize;
+    float scale;
+    void* dscores;
+    uint64_t dscores_stride;
+};
+hipError_t launch_route_grad(int elem_type, const RouteGradArgs& a, hipStream_t stream);
+
+struct GroupArgs {
+    const uint32_t* ids;
+    uint32_t n, experts, align, room;   // room: elements of order
+    uint32_t* order;
+    uint32_t* place;
+    uint32_t* starts;
+    uint32_t* counts;
+};
+size_t group_temp_bytes(uint64_t n, uint32_t experts);
+hipError_t launch_group(const GroupArgs& a, void* temp, hipStream_t stream);
+
+struct LogprobsArgs {
+    const void* logits;
+    uint64_t row_stride;
+    const uint32_t* targets;   // or null, as any output but stats
+    uint32_t rows, vocab, top_k;
+    float scale;
+    float* stats;
+    float* lse;
+    float* entropy;
+    float* logprob;
+    uint32_t* rank;
+    uint32_t* top_ids;
+    float* top_logprobs;
+};
+size_t logprobs_temp_bytes(uint64_t rows, uint32_t vocab, uint32_t top_k);
+hipError_t launch_logprobs(int elem_type, const LogprobsArgs& a, void* temp, hipStream_t stream);
+
+struct LogprobsGradArgs {
+    const void* logits;
+    uint64_t row_stride;
+    const uint32_t* targets;
+    const float* stats;
+    const float* entropy;
+    uint32_t rows, vocab;
+    float scale;
+    const float* dlogprob;
+    const float* dentropy;
+    const float* dlse;
+    void* dlogits;
+    uint64_t dlogits_stride;
+};
+hipError_t launch_logprobs_grad(int elem_type, const LogprobsGradArgs& a, hipStream_t stream);
 
 }  // namespace rs

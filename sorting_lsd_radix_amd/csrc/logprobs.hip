@@ -1,0 +1,470 @@
+// logprobs.hip -- log probabilities of given tokens with entropy, rank and
+// top alternatives, and their gradient for the logits.
+//
+// One read of a row gives its softmax statistics: every thread keeps a
+// reference r, s = sum of 2^d and t = sum of d 2^d with d = (x - r) a,
+// a = scale * log2(e), and the largest x it has seen; sums with different
+// references join as s 2^delta, (t + s delta) 2^delta with delta = (r - m) a.
+// Then ln of the sum of exp is c m + ln s, and the entropy ln s - ln2 t / s.
+// A row is one block's work, or, where rows are few, several blocks' (parts),
+// whose results a second launch joins.
+#include "internal.hpp"
+#include "rows_common.hpp"
+
+namespace rs {
+
+namespace {
+
+constexpr int kLpBlock = 256;
+constexpr int kLpWaves = kLpBlock / kWave;
+constexpr uint32_t kLpMinPart = 4096;     // smallest part of a split row, in elements
+constexpr uint32_t kLpMaxParts = 64;
+constexpr uint32_t kLpBlocks = 1024;      // blocks that a split aims at
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kInf = __builtin_huge_valf();
+// A sum's reference moves when the largest x is further than this from it, in
+// powers of two: far below f32's range (sums reach 2^30 * 2^16), and near
+// enough that the rounding of d (16 * 2^-24) stays under a millionth.
+constexpr float kMaxShift = 16.0f;
+
+// Where a row's parts begin and end: multiples of 8 elements, so that no
+// 16-byte vector of the row is in two parts.
+struct Parts {
+    uint32_t count, size;
+};
+
+Parts lp_parts(uint64_t rows, uint32_t vocab) {
+    uint64_t want = rows ? kLpBlocks / rows : 1;
+    const uint64_t most = vocab / kLpMinPart;
+    if (want > most) want = most;
+    if (want > kLpMaxParts) want = kLpMaxParts;
+    if (want < 1) want = 1;
+    const uint32_t size = static_cast<uint32_t>(((vocab + want - 1) / want + 7) / 8 * 8);
+    return Parts{(vocab + size - 1) / size, size};
+}
+
+// What is known of a set of logits: the largest, sums relative to it, and how
+// many come before the target.
+struct Sums {
+    float m, s, t;
+    uint32_t ahead;
+};
+
+__device__ __forceinline__ Sums join(const Sums& x, const Sums& y, float a) {
+    Sums r;
+    r.m = fmaxf(x.m, y.m);
+    r.ahead = x.ahead + y.ahead;
+    r.s = 0.0f;
+    r.t = 0.0f;
+    auto add = [&](const Sums& p) {
+        if (p.s != 0.0f) {   // of nothing but -inf: adds nothing, and has no reference
+            const float d = fmaxf((p.m - r.m) * a, -1000.0f);
+            const float f = __builtin_amdgcn_exp2f(d);
+            r.s += p.s * f;
+            r.t += (p.t + p.s * d) * f;
+        }
+    };
+    add(x);
+    add(y);
+    return r;
+}
+
+template <class T>
+struct RowVec {
+    static constexpr int N = 16 / sizeof(T);
+    T v[N];
+};
+
+// Elements v * N .. of a row of n elements; behind its end -inf.  Rows may
+// start on any element, so the compiler is told of no alignment.
+template <class T>
+__device__ __forceinline__ void load_vec(const T* in, uint32_t v, uint32_t n, float (&x)[RowVec<T>::N]) {
+    constexpr uint32_t N = RowVec<T>::N;
+    const uint32_t at = v * N;
+    if (at + N <= n) {
+        RowVec<T> r;
+        __builtin_memcpy(&r, in + at, sizeof(r));
+#pragma unroll
+        for (uint32_t j = 0; j < N; ++j) x[j] = static_cast<float>(r.v[j]);
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < N; ++j) x[j] = at + j < n ? static_cast<float>(in[at + j]) : -kInf;
+    }
+}
+
+// The 64 lanes' keys in decreasing order (bitonic network).
+__device__ __forceinline__ uint64_t wave_sort_desc(uint64_t k) {
+    const uint32_t lane = lane_id();
+#pragma unroll
+    for (uint32_t size = 2; size <= kWave; size <<= 1) {
+#pragma unroll
+        for (uint32_t j = size >> 1; j > 0; j >>= 1) {
+            const uint64_t o = __shfl_xor(k, j, kWave);
+            const bool keep_max = ((lane & j) == 0) == ((lane & size) == 0);
+            k = keep_max ? (k > o ? k : o) : (k < o ? k : o);
+        }
+    }
+    return k;
+}
+
+// The best 64 of two lists in decreasing order, in decreasing order.
+__device__ __forceinline__ uint64_t wave_merge_desc(uint64_t x, uint64_t y) {
+    const uint32_t lane = lane_id();
+    const uint64_t r = __shfl(y, kWave - 1 - lane, kWave);
+    uint64_t k = x > r ? x : r;   // the best 64, a bitonic sequence
+#pragma unroll
+    for (uint32_t j = kWave / 2; j > 0; j >>= 1) {
+        const uint64_t o = __shfl_xor(k, j, kWave);
+        k = ((lane & j) == 0) ? (k > o ? k : o) : (k < o ? k : o);
+    }
+    return k;
+}
+
+// A logit in a list: its order pattern, then the lower index first.  Lists
+// hold 0 where they have no element.
+__device__ __forceinline__ uint64_t list_key(uint32_t order, uint32_t index) {
+    return (static_cast<uint64_t>(order) << 32) | static_cast<uint32_t>(~index);
+}
+
+struct SelectShared {
+    uint32_t bins[256];
+    uint32_t wave[2][kLpWaves];
+    uint32_t digit, need, found;
+    uint64_t top[kWave];
+};
+
+// The first k (at most n) of a row part's n elements in the row's order,
+// whatever they are, by a radix select on the order patterns: four counts of
+// 8-bit digits find the k-th pattern, then the patterns above it are
+// collected, and of those equal to it the first by index.  s.top[0, k)
+// receives the keys, in any order.
+template <class T>
+__device__ void radix_select(const T* in, uint32_t n, uint32_t base, uint32_t k, SelectShared& s) {
+    constexpr uint32_t N = RowVec<T>::N;
+    const uint32_t tid = threadIdx.x, wave = tid / kWave, lane = tid & (kWave - 1);
+    const uint32_t vecs = (n + N - 1) / N;
+    uint32_t prefix = 0, need = k;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        s.bins[tid] = 0;
+        __syncthreads();
+        for (uint32_t v = tid; v < vecs; v += kLpBlock) {
+            float x[N];
+            load_vec(in, v, n, x);
+            for (uint32_t j = 0; j < N; ++j) {
+                const uint32_t o = order32(x[j]);
+                if (v * N + j < n && (shift == 24 || ((o ^ prefix) >> (shift + 8)) == 0))
+                    atomicAdd(&s.bins[(o >> shift) & 255u], 1u);
+            }
+        }
+        __syncthreads();
+        // thread t holds digit 255 - t: how many have a larger digit
+        const uint32_t own = s.bins[255 - tid];
+        const uint32_t incl = wave_inclusive_sum(own);
+        if (lane == kWave - 1) s.wave[0][wave] = incl;
+        __syncthreads();
+        uint32_t above = incl - own;
+        for (uint32_t w = 0; w < wave; ++w) above += s.wave[0][w];
+        if (above < need && need <= above + own) {
+            s.digit = 255 - tid;
+            s.need = need - above;
+        }
+        __syncthreads();
+        prefix |= s.digit << shift;
+        need = s.need;
+    }
+    if (tid == 0) s.found = 0;
+    __syncthreads();
+    for (uint32_t v = tid; v < vecs; v += kLpBlock) {
+        float x[N];
+        load_vec(in, v, n, x);
+        for (uint32_t j = 0; j < N; ++j) {
+            const uint32_t o = order32(x[j]);
+            if (v * N + j < n && o > prefix) s.top[atomicAdd(&s.found, 1u)] = list_key(o, base + v * N + j);
+        }
+    }
+    uint32_t taken = 0;   // equal ones so far, in the order of the row
+    for (uint32_t v0 = 0, it = 0; v0 < vecs && taken < need; v0 += kLpBlock, ++it) {
+        const uint32_t v = v0 + tid;
+        uint32_t mine = 0;
+        if (v < vecs) {
+            float x[N];
+            load_vec(in, v, n, x);
+            for (uint32_t j = 0; j < N; ++j)
+                if (v * N + j < n && order32(x[j]) == prefix) mine |= 1u << j;
+        }
+        const uint32_t own = __popc(mine);
+        const uint32_t incl = wave_inclusive_sum(own);
+        if (lane == kWave - 1) s.wave[it & 1][wave] = incl;
+        __syncthreads();
+        uint32_t at = taken + incl - own;
+        for (uint32_t w = 0; w < kLpWaves; ++w) {
+            const uint32_t c = s.wave[it & 1][w];
+            if (w < wave) at += c;
+            taken += c;
+        }
+        for (uint32_t j = 0; j < N; ++j)
+            if ((mine >> j) & 1u) {
+                if (at < need) s.top[k - need + at] = list_key(prefix, base + v * N + j);
+                ++at;
+            }
+    }
+    __syncthreads();
+}
+
+// Writes a row's results.  Called by one wave; lane i has the i-th list key.
+__device__ __forceinline__ void finish_row(const LogprobsArgs& p, uint32_t row, Sums z, float x_target,
+                                           bool has_target, uint64_t key) {
+    const uint32_t lane = lane_id();
+    const bool empty = z.m == -kInf && z.s == 0.0f;
+    if (z.m == kInf) z.s = __builtin_nanf("");
+    const float ln_s = empty ? 0.0f : logf(z.s);
+    auto ln_p = [&](float x) { return x == -kInf && z.s == z.s ? -kInf : (x - z.m) * p.scale - ln_s; };
+    if (lane == 0) {
+        p.stats[2ull * row] = z.m;
+        p.stats[2ull * row + 1] = z.s;
+        if (p.lse) p.lse[row] = empty ? -kInf : z.m * p.scale + ln_s;
+        if (p.entropy) {
+            const float h = empty ? 0.0f : ln_s - kLn2 * (z.t / z.s);
+            p.entropy[row] = h < 0.0f ? 0.0f : h;   // rounding alone makes it negative
+        }
+        if (p.logprob) p.logprob[row] = has_target ? ln_p(x_target) : 0.0f;
+        if (p.rank) p.rank[row] = has_target && x_target == x_target ? z.ahead : 0xFFFFFFFFu;
+    }
+    if (lane < p.top_k) {
+        const uint32_t o = static_cast<uint32_t>(key >> 32);
+        const float x = o == 1u ? __builtin_nanf("")
+                                : __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o);
+        p.top_ids[static_cast<uint64_t>(row) * p.top_k + lane] = ~static_cast<uint32_t>(key);
+        p.top_logprobs[static_cast<uint64_t>(row) * p.top_k + lane] = ln_p(x);
+    }
+}
+
+// Block (part, row): the sums and, with top_k, the list of one part of a row.
+// With one part the row is finished here; otherwise part q of a row leaves
+// its sums at sums[row * parts + q] and its list at lists[(row * parts + q) * top_k].
+template <int ELEM, bool RANK, bool TOP>
+__global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LogprobsArgs p, Parts parts, Sums* __restrict__ sums,
+                                                            uint64_t* __restrict__ lists) {
+    using T = typename Elem<ELEM>::T;
+    constexpr uint32_t N = RowVec<T>::N;
+    __shared__ Sums s_sums[kLpWaves];
+    __shared__ SelectShared s_select;
+    const uint32_t tid = threadIdx.x, wave = tid / kWave, lane = tid & (kWave - 1);
+    const uint32_t block = block_id();
+    const uint32_t row = block / parts.count;
+    const uint32_t part = block - row * parts.count;
+    if (row >= p.rows) return;
+    const uint32_t base = part * parts.size;
+    const uint32_t n = p.vocab - base < parts.size ? p.vocab - base : parts.size;
+    const T* whole = static_cast<const T*>(p.logits) + row * p.row_stride;
+    const T* in = whole + base;
+    const float a = p.scale * kLog2e;
+
+    const uint32_t target = p.targets ? p.targets[row] : 0xFFFFFFFFu;
+    const bool has_target = target < p.vocab;
+    const float x_target = has_target ? static_cast<float>(whole[target]) : 0.0f;
+
+    float m = -kInf, r = 0.0f, s = 0.0f, t = 0.0f;
+    uint32_t ahead = 0;
+    const uint32_t vecs = (n + N - 1) / N;
+    for (uint32_t v = tid; v < vecs; v += kLpBlock) {
+        float x[N];
+        load_vec(in, v, n, x);
+        float top = x[0];
+#pragma unroll
+        for (uint32_t j = 1; j < N; ++j) top = fmaxf(top, x[j]);
+        if (top > m) {
+            m = top;
+            if (!(fabsf((m - r) * a) <= kMaxShift) && m < kInf) {
+                if (s != 0.0f) {
+                    const float d = fmaxf((r - m) * a, -1000.0f);
+                    const float f = __builtin_amdgcn_exp2f(d);
+                    t = (t + s * d) * f;
+                    s *= f;
+                }
+                r = m;
+            }
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < N; ++j) {
+            const float d = (x[j] - r) * a;
+            const float e = __builtin_amdgcn_exp2f(d);
+            s += e;
+            t = fmaf(e, fmaxf(d, -1000.0f), t);
+        }
+        if (RANK) {
+#pragma unroll
+            for (uint32_t j = 0; j < N; ++j)
+                ahead += (x[j] > x_target || (x[j] == x_target && base + v * N + j < target)) ? 1u : 0u;
+        }
+    }
+    // relative to the thread's largest
+    Sums z{m, s, t, ahead};
+    if (s != 0.0f && m < kInf) {
+        const float d = (r - m) * a;
+        const float f = __builtin_amdgcn_exp2f(d);
+        z.s = s * f;
+        z.t = (t + s * d) * f;
+    }
+#pragma unroll
+    for (int off = kWave / 2; off > 0; off >>= 1) {
+        const Sums o{__shfl_xor(z.m, off, kWave), __shfl_xor(z.s, off, kWave), __shfl_xor(z.t, off, kWave),
+                     __shfl_xor(z.ahead, off, kWave)};
+        z = join(z, o, a);
+    }
+    if (lane == 0) s_sums[wave] = z;
+    if (TOP) radix_select(in, n, base, p.top_k < n ? p.top_k : n, s_select);
+    __syncthreads();
+    if (wave != 0) return;
+    z = s_sums[0];
+    for (uint32_t w = 1; w < kLpWaves; ++w) z = join(z, s_sums[w], a);
+    uint64_t key = 0;
+    if (TOP) key = wave_sort_desc(lane < p.top_k && lane < n ? s_select.top[lane] : 0ull);
+    if (parts.count == 1) {
+        finish_row(p, row, z, x_target, has_target, key);
+    } else {
+        if (lane == 0) sums[block] = z;
+        if (TOP && lane < p.top_k) lists[static_cast<uint64_t>(block) * p.top_k + lane] = key;
+    }
+}
+
+// One wave a row: joins the parts.
+template <int ELEM>
+__global__ __launch_bounds__(kWave) void logprobs_join_kernel(LogprobsArgs p, Parts parts, const Sums* __restrict__ sums,
+                                                              const uint64_t* __restrict__ lists) {
+    using T = typename Elem<ELEM>::T;
+    const uint32_t row = block_id(), lane = threadIdx.x;
+    if (row >= p.rows) return;
+    const float a = p.scale * kLog2e;
+    const uint32_t target = p.targets ? p.targets[row] : 0xFFFFFFFFu;
+    const bool has_target = target < p.vocab;
+    const float x_target =
+        has_target ? static_cast<float>(static_cast<const T*>(p.logits)[row * p.row_stride + target]) : 0.0f;
+    const uint64_t first = static_cast<uint64_t>(row) * parts.count;
+    Sums z{-kInf, 0.0f, 0.0f, 0u};
+    if (lane < parts.count) z = sums[first + lane];   // at most kWave parts
+#pragma unroll
+    for (int off = kWave / 2; off > 0; off >>= 1) {
+        const Sums o{__shfl_xor(z.m, off, kWave), __shfl_xor(z.s, off, kWave), __shfl_xor(z.t, off, kWave),
+                     __shfl_xor(z.ahead, off, kWave)};
+        z = join(z, o, a);
+    }
+    uint64_t key = 0;
+    if (p.top_k)
+        for (uint32_t q = 0; q < parts.count; ++q)
+            key = wave_merge_desc(key, lane < p.top_k ? lists[(first + q) * p.top_k + lane] : 0ull);
+    finish_row(p, row, z, x_target, has_target, key);
+}
+static_assert(kLpMaxParts <= kWave, "the joining wave has a lane for each part");
+
+// Block (part of a row, row): dx = e (c0 + c1 d) with e = 2^d, d = (x - m) a, plus
+// the target's own term.
+constexpr uint32_t kLpGradVecs = 4;   // 16-byte vectors of a thread
+template <int ELEM>
+__global__ __launch_bounds__(kLpBlock) void logprobs_grad_kernel(LogprobsGradArgs p, uint32_t blocks_a_row) {
+    using T = typename Elem<ELEM>::T;
+    constexpr uint32_t N = RowVec<T>::N;
+    const uint32_t block = block_id();
+    const uint32_t row = block / blocks_a_row;
+    if (row >= p.rows) return;
+    const uint32_t v0 = (block - row * blocks_a_row) * (kLpBlock * kLpGradVecs) + threadIdx.x;
+    const T* in = static_cast<const T*>(p.logits) + row * p.row_stride;
+    T* out = static_cast<T*>(p.dlogits) + row * p.dlogits_stride;
+    const float a = p.scale * kLog2e;
+    const float m = p.stats[2ull * row], s = p.stats[2ull * row + 1];
+    const uint32_t target = p.targets ? p.targets[row] : 0xFFFFFFFFu;
+    const float g = p.dlogprob && target < p.vocab ? p.dlogprob[row] : 0.0f;
+    const float h = p.dentropy ? p.dentropy[row] : 0.0f;
+    const float q = p.dlse ? p.dlse[row] : 0.0f;
+    const bool empty = m == -kInf && s == 0.0f;
+    const float big_h = p.dentropy ? p.entropy[row] : 0.0f;
+    const float c0 = empty ? 0.0f : p.scale * (q - g - (p.dentropy ? h * (big_h - logf(s)) : 0.0f)) / s;
+    const float c1 = empty ? 0.0f : -p.scale * h * kLn2 / s;
+    const float own = empty ? 0.0f : p.scale * g;
+    const uint32_t vecs = (p.vocab + N - 1) / N;
+#pragma unroll
+    for (uint32_t i = 0; i < kLpGradVecs; ++i) {
+        const uint32_t v = v0 + i * kLpBlock;
+        if (v >= vecs) break;
+        float x[N];
+        load_vec(in, v, p.vocab, x);
+        RowVec<T> o;
+#pragma unroll
+        for (uint32_t j = 0; j < N; ++j) {
+            const float d = empty ? 0.0f : (x[j] - m) * a;
+            const float e = __builtin_amdgcn_exp2f(d);
+            float dx = e * fmaf(c1, fmaxf(d, -1000.0f), c0);
+            if (v * N + j == target) dx += own;
+            o.v[j] = static_cast<T>(dx);
+        }
+        if ((v + 1) * N <= p.vocab) {
+            __builtin_memcpy(out + v * N, &o, sizeof(o));
+        } else {
+#pragma unroll
+            for (uint32_t j = 0; j < N; ++j)
+                if (v * N + j < p.vocab) out[v * N + j] = o.v[j];
+        }
+    }
+}
+
+template <int ELEM, bool RANK>
+hipError_t logprobs_elem(const LogprobsArgs& p, void* temp, hipStream_t stream) {
+    const Parts parts = lp_parts(p.rows, p.vocab);
+    const uint64_t blocks = static_cast<uint64_t>(p.rows) * parts.count;
+    uint64_t* lists = static_cast<uint64_t*>(temp);
+    Sums* sums = reinterpret_cast<Sums*>(lists + (parts.count > 1 ? blocks * p.top_k : 0));
+    timing_before(stream, RS_KERNEL_LOGPROBS);
+    if (p.top_k)
+        logprobs_kernel<ELEM, RANK, true><<<many_blocks(blocks), kLpBlock, 0, stream>>>(p, parts, sums, lists);
+    else
+        logprobs_kernel<ELEM, RANK, false><<<many_blocks(blocks), kLpBlock, 0, stream>>>(p, parts, sums, lists);
+    hipError_t e = hipGetLastError();
+    timing_after(stream);
+    if (e != hipSuccess || parts.count == 1) return e;
+    timing_before(stream, RS_KERNEL_LOGPROBS_JOIN);
+    logprobs_join_kernel<ELEM><<<many_blocks(p.rows), kWave, 0, stream>>>(p, parts, sums, lists);
+    e = hipGetLastError();
+    timing_after(stream);
+    return e;
+}
+
+template <int ELEM>
+hipError_t grad_elem(const LogprobsGradArgs& p, hipStream_t stream) {
+    constexpr uint32_t kSpan = kLpBlock * kLpGradVecs * RowVec<typename Elem<ELEM>::T>::N;
+    const uint32_t blocks_a_row = (p.vocab + kSpan - 1) / kSpan;
+    timing_before(stream, RS_KERNEL_LOGPROBS_GRAD);
+    logprobs_grad_kernel<ELEM><<<many_blocks(static_cast<uint64_t>(p.rows) * blocks_a_row), kLpBlock, 0, stream>>>(p, blocks_a_row);
+    const hipError_t e = hipGetLastError();
+    timing_after(stream);
+    return e;
+}
+
+}  // namespace
+
+size_t logprobs_temp_bytes(uint64_t rows, uint32_t vocab, uint32_t top_k) {
+    const Parts parts = lp_parts(rows, vocab);
+    if (rows == 0 || parts.count == 1) return 16;
+    return rows * parts.count * (sizeof(Sums) + 8 * static_cast<size_t>(top_k));
+}
+
+hipError_t launch_logprobs(int elem_type, const LogprobsArgs& p, void* temp, hipStream_t stream) {
+    switch (elem_type) {
+    case RS_ELEM_F32:
+        return p.rank ? logprobs_elem<RS_ELEM_F32, true>(p, temp, stream) : logprobs_elem<RS_ELEM_F32, false>(p, temp, stream);
+    case RS_ELEM_F16:
+        return p.rank ? logprobs_elem<RS_ELEM_F16, true>(p, temp, stream) : logprobs_elem<RS_ELEM_F16, false>(p, temp, stream);
+    default:
+        return p.rank ? logprobs_elem<RS_ELEM_BF16, true>(p, temp, stream) : logprobs_elem<RS_ELEM_BF16, false>(p, temp, stream);
+    }
+}
+
+hipError_t launch_logprobs_grad(int elem_type, const LogprobsGradArgs& p, hipStream_t stream) {
+    switch (elem_type) {
+    case RS_ELEM_F32: return grad_elem<RS_ELEM_F32>(p, stream);
+    case RS_ELEM_F16: return grad_elem<RS_ELEM_F16>(p, stream);
+    default: return grad_elem<RS_ELEM_BF16>(p, stream);
+    }
+}
+
+}  // namespace rs

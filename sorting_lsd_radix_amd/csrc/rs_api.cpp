@@ -404,15 +404,250 @@ rs_status rs_bitonic_tile(const uint32_t* keys_in, uint32_t* keys_out, uint64_t 
     return e == hipSuccess ? RS_OK : RS_ERR_HIP;
 }
 
+// ---- rows of scores --------------------------------------------------------------
+
+namespace rs {
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+size_t elem_bytes(int elem_type) { return elem_type == RS_ELEM_F32 ? 4 : 2; }
+
+// The buffers of a call: none may overlap another.  (A fixed array: these
+// checks allocate nothing and cannot throw.)
+class Buffers {
+  public:
+    void add(const void* p, uint64_t bytes) {
+        if (p != nullptr && bytes != 0) r_[n_++] = range_of(p, bytes);
+    }
+    bool overlap() const {
+        for (int i = 0; i < n_; ++i)
+            for (int j = i + 1; j < n_; ++j)
+                if (r_[i].lo < r_[j].hi && r_[j].lo < r_[i].hi) return true;
+        return false;
+    }
+
+  private:
+    Range r_[16];
+    int n_ = 0;
+};
+
+// Bytes from the first element of a matrix of rows to behind its last one;
+// false if they do not fit an address.
+bool matrix_bytes(int elem_type, uint64_t rows, uint64_t stride, uint32_t cols, uint64_t* bytes) {
+    uint64_t n = 0;
+    if (rows == 0) {
+        *bytes = 0;
+        return true;
+    }
+    if (__builtin_mul_overflow(rows - 1, stride, &n) || __builtin_add_overflow(n, cols, &n)) return false;
+    if (n >= (uint64_t{1} << 60)) return false;
+    *bytes = n * elem_bytes(elem_type);
+    return true;
+}
+
+bool matrix_aligned(int elem_type, const void* p) {
+    return (reinterpret_cast<uintptr_t>(p) & (elem_bytes(elem_type) - 1)) == 0;
+}
+
+bool elem_ok(int elem_type) { return elem_type >= RS_ELEM_F32 && elem_type <= RS_ELEM_BF16; }
+
+bool positive(float x) { return x > 0.0f && x < __builtin_huge_valf(); }
+
+}  // namespace
+}  // namespace rs
+
+rs_status rs_route_topk(rs_elem_type elem_type, const void* scores, uint64_t row_stride,
+                        const float* bias, uint64_t rows, uint32_t experts, uint32_t top_k,
+                        rs_score_fn score_fn, uint32_t groups, uint32_t top_groups,
+                        uint32_t group_best, int renormalize, float scale, uint32_t* ids,
+                        float* weights, hipStream_t stream) {
+    using namespace rs;
+    if (!elem_ok(elem_type)) return RS_ERR_INVALID_VALUE;
+    if (score_fn != RS_SCORE_SOFTMAX && score_fn != RS_SCORE_SIGMOID) return RS_ERR_INVALID_VALUE;
+    if (rows >= RS_MAX_N || experts > RS_MAX_EXPERTS || groups > RS_MAX_GROUPS || top_k > RS_MAX_TOP_K)
+        return RS_ERR_UNSUPPORTED_SIZE;
+    if (experts == 0 || groups == 0 || experts % groups != 0) return RS_ERR_INVALID_VALUE;
+    const uint32_t size = experts / groups;
+    if (top_groups == 0 || top_groups > groups) return RS_ERR_INVALID_VALUE;
+    if (group_best < 1 || group_best > 2 || group_best > size) return RS_ERR_INVALID_VALUE;
+    if (top_k == 0 || top_k > top_groups * size) return RS_ERR_INVALID_VALUE;
+    if (!positive(scale)) return RS_ERR_INVALID_VALUE;
+    uint64_t bytes = 0;
+    if (!matrix_bytes(elem_type, rows, row_stride, experts, &bytes)) return RS_ERR_INVALID_VALUE;
+    if (rows == 0) return RS_OK;
+    if (scores == nullptr || ids == nullptr || weights == nullptr) return RS_ERR_INVALID_VALUE;
+    if (!matrix_aligned(elem_type, scores) || !aligned4(bias) || !aligned4(ids) || !aligned4(weights))
+        return RS_ERR_MISALIGNED;
+    Buffers b, in;
+    b.add(ids, rows * top_k * 4);
+    b.add(weights, rows * top_k * 4);
+    in = b;   // the inputs may share memory with each other
+    b.add(scores, bytes);
+    in.add(bias, static_cast<uint64_t>(experts) * 4);
+    if (b.overlap() || in.overlap()) return RS_ERR_OVERLAP;
+    const RouteArgs a{scores,     row_stride, bias,       static_cast<uint32_t>(rows),
+                      experts,    top_k,      groups,     top_groups,
+                      group_best, score_fn == RS_SCORE_SIGMOID, renormalize != 0, scale,
+                      ids,        weights};
+    return launch_route(elem_type, a, stream) == hipSuccess ? RS_OK : RS_ERR_HIP;
+}
+
+rs_status rs_route_topk_grad(rs_elem_type elem_type, const void* scores, uint64_t row_stride,
+                             const uint32_t* ids, const float* weights, const float* dweights,
+                             uint64_t rows, uint32_t experts, uint32_t top_k, rs_score_fn score_fn,
+                             int renormalize, float scale, void* dscores, uint64_t dscores_stride,
+                             hipStream_t stream) {
+    using namespace rs;
+    if (!elem_ok(elem_type)) return RS_ERR_INVALID_VALUE;
+    if (score_fn != RS_SCORE_SOFTMAX && score_fn != RS_SCORE_SIGMOID) return RS_ERR_INVALID_VALUE;
+    if (rows >= RS_MAX_N || experts > RS_MAX_EXPERTS || top_k > RS_MAX_TOP_K) return RS_ERR_UNSUPPORTED_SIZE;
+    if (experts == 0 || top_k == 0 || top_k > experts || !positive(scale)) return RS_ERR_INVALID_VALUE;
+    if (dscores_stride < experts && rows > 1) return RS_ERR_INVALID_VALUE;
+    uint64_t in_bytes = 0, out_bytes = 0;
+    if (!matrix_bytes(elem_type, rows, row_stride, experts, &in_bytes) ||
+        !matrix_bytes(elem_type, rows, dscores_stride, experts, &out_bytes))
+        return RS_ERR_INVALID_VALUE;
+    if (rows == 0) return RS_OK;
+    if (!scores || !ids || !weights || !dweights || !dscores) return RS_ERR_INVALID_VALUE;
+    if (!matrix_aligned(elem_type, scores) || !matrix_aligned(elem_type, dscores) || !aligned4(ids) ||
+        !aligned4(weights) || !aligned4(dweights))
+        return RS_ERR_MISALIGNED;
+    const struct { const void* p; uint64_t bytes; } ins[] = {
+        {scores, in_bytes}, {ids, rows * top_k * 4}, {weights, rows * top_k * 4}, {dweights, rows * top_k * 4}};
+    for (const auto& i : ins) {
+        Buffers b;
+        b.add(dscores, out_bytes);
+        b.add(i.p, i.bytes);
+        if (b.overlap()) return RS_ERR_OVERLAP;
+    }
+    const RouteGradArgs a{scores, row_stride, ids, weights, dweights, static_cast<uint32_t>(rows), experts, top_k,
+                          score_fn == RS_SCORE_SIGMOID, renormalize != 0, scale, dscores, dscores_stride};
+    return launch_route_grad(elem_type, a, stream) == hipSuccess ? RS_OK : RS_ERR_HIP;
+}
+
+rs_status rs_group_choices(const uint32_t* ids, uint64_t n, uint32_t experts, uint32_t align,
+                           uint32_t* order, uint32_t* place, uint32_t* starts, uint32_t* counts,
+                           void* d_temp, size_t* temp_bytes, hipStream_t stream) {
+    using namespace rs;
+    if (temp_bytes == nullptr || experts == 0 || align == 0) return RS_ERR_INVALID_VALUE;
+    if (experts > RS_MAX_EXPERTS || n >= RS_MAX_N) return RS_ERR_UNSUPPORTED_SIZE;
+    const uint64_t room = n + static_cast<uint64_t>(experts) * (align - 1);
+    if (room >= RS_MAX_N) return RS_ERR_UNSUPPORTED_SIZE;
+    const size_t need = group_temp_bytes(n, experts);
+    if (d_temp == nullptr) {
+        *temp_bytes = need;
+        return RS_OK;
+    }
+    if (starts == nullptr || counts == nullptr) return RS_ERR_INVALID_VALUE;
+    if ((n > 0 && (ids == nullptr || place == nullptr)) || (room > 0 && order == nullptr)) return RS_ERR_INVALID_VALUE;
+    if (!aligned4(starts) || !aligned4(counts) || !aligned16(d_temp)) return RS_ERR_MISALIGNED;
+    if ((n > 0 && (!aligned16(ids) || !aligned16(place))) || (room > 0 && !aligned16(order))) return RS_ERR_MISALIGNED;
+    if (*temp_bytes < need) return RS_ERR_TEMP_TOO_SMALL;
+    Buffers b;
+    b.add(ids, n * 4);
+    b.add(place, n * 4);
+    b.add(order, room * 4);
+    b.add(starts, (static_cast<uint64_t>(experts) + 1) * 4);
+    b.add(counts, static_cast<uint64_t>(experts) * 4);
+    b.add(d_temp, need);
+    if (b.overlap()) return RS_ERR_OVERLAP;
+    const GroupArgs a{ids, static_cast<uint32_t>(n), experts, align, static_cast<uint32_t>(room),
+                      order, place, starts, counts};
+    return launch_group(a, d_temp, stream) == hipSuccess ? RS_OK : RS_ERR_HIP;
+}
+
+rs_status rs_token_logprobs(rs_elem_type elem_type, const void* logits, uint64_t row_stride,
+                            const uint32_t* targets, uint64_t rows, uint32_t vocab, float scale,
+                            uint32_t top_k, float* stats, float* lse, float* entropy,
+                            float* logprob, uint32_t* rank, uint32_t* top_ids, float* top_logprobs,
+                            void* d_temp, size_t* temp_bytes, hipStream_t stream) {
+    using namespace rs;
+    if (temp_bytes == nullptr || !elem_ok(elem_type)) return RS_ERR_INVALID_VALUE;
+    if (rows >= RS_MAX_N || vocab >= RS_MAX_N || top_k > RS_MAX_TOP_K) return RS_ERR_UNSUPPORTED_SIZE;
+    if (vocab == 0 || top_k > vocab) return RS_ERR_INVALID_VALUE;
+    if (!(scale >= 0x1p-60f && scale <= 0x1p60f)) return RS_ERR_INVALID_VALUE;
+    uint64_t bytes = 0;
+    if (!matrix_bytes(elem_type, rows, row_stride, vocab, &bytes)) return RS_ERR_INVALID_VALUE;
+    const size_t need = logprobs_temp_bytes(rows, vocab, top_k);
+    if (d_temp == nullptr) {
+        *temp_bytes = need;
+        return RS_OK;
+    }
+    if (rows == 0) return RS_OK;
+    if (logits == nullptr || stats == nullptr) return RS_ERR_INVALID_VALUE;
+    if (targets == nullptr && (logprob != nullptr || rank != nullptr)) return RS_ERR_INVALID_VALUE;
+    if ((top_k > 0) != (top_ids != nullptr) || (top_k > 0) != (top_logprobs != nullptr)) return RS_ERR_INVALID_VALUE;
+    if (!matrix_aligned(elem_type, logits) || !aligned4(targets) || !aligned4(stats) || !aligned4(lse) ||
+        !aligned4(entropy) || !aligned4(logprob) || !aligned4(rank) || !aligned4(top_ids) ||
+        !aligned4(top_logprobs) || !aligned16(d_temp))
+        return RS_ERR_MISALIGNED;
+    if (*temp_bytes < need) return RS_ERR_TEMP_TOO_SMALL;
+    Buffers b, in;
+    b.add(stats, rows * 8);
+    b.add(lse, rows * 4);
+    b.add(entropy, rows * 4);
+    b.add(logprob, rows * 4);
+    b.add(rank, rows * 4);
+    b.add(top_ids, rows * top_k * 4);
+    b.add(top_logprobs, rows * top_k * 4);
+    b.add(d_temp, need);
+    in = b;   // the inputs may share memory with each other
+    b.add(logits, bytes);
+    in.add(targets, rows * 4);
+    if (b.overlap() || in.overlap()) return RS_ERR_OVERLAP;
+    const LogprobsArgs a{logits, row_stride, targets, static_cast<uint32_t>(rows), vocab, top_k, scale,
+                         stats,  lse,        entropy, logprob, rank, top_ids, top_logprobs};
+    return launch_logprobs(elem_type, a, d_temp, stream) == hipSuccess ? RS_OK : RS_ERR_HIP;
+}
+
+rs_status rs_token_logprobs_grad(rs_elem_type elem_type, const void* logits, uint64_t row_stride,
+                                 const uint32_t* targets, const float* stats, const float* entropy,
+                                 uint64_t rows, uint32_t vocab, float scale, const float* dlogprob,
+                                 const float* dentropy, const float* dlse, void* dlogits,
+                                 uint64_t dlogits_stride, hipStream_t stream) {
+    using namespace rs;
+    if (!elem_ok(elem_type)) return RS_ERR_INVALID_VALUE;
+    if (rows >= RS_MAX_N || vocab >= RS_MAX_N) return RS_ERR_UNSUPPORTED_SIZE;
+    if (vocab == 0 || (dlogits_stride < vocab && rows > 1)) return RS_ERR_INVALID_VALUE;
+    if (!(scale >= 0x1p-60f && scale <= 0x1p60f)) return RS_ERR_INVALID_VALUE;
+    uint64_t in_bytes = 0, out_bytes = 0;
+    if (!matrix_bytes(elem_type, rows, row_stride, vocab, &in_bytes) ||
+        !matrix_bytes(elem_type, rows, dlogits_stride, vocab, &out_bytes))
+        return RS_ERR_INVALID_VALUE;
+    if (rows == 0) return RS_OK;   // an empty array's pointer may be null
+    if (!dlogprob && !dentropy && !dlse) return RS_ERR_INVALID_VALUE;
+    if (!logits || !stats || !dlogits || (dlogprob && !targets) || (dentropy && !entropy))
+        return RS_ERR_INVALID_VALUE;
+    if (!matrix_aligned(elem_type, logits) || !matrix_aligned(elem_type, dlogits) || !aligned4(targets) ||
+        !aligned4(stats) || !aligned4(entropy) || !aligned4(dlogprob) || !aligned4(dentropy) || !aligned4(dlse))
+        return RS_ERR_MISALIGNED;
+    const bool in_place = logits == dlogits && (row_stride == dlogits_stride || rows == 1);
+    const struct { const void* p; uint64_t bytes; } ins[] = {
+        {in_place ? nullptr : logits, in_bytes}, {targets, rows * 4}, {stats, rows * 8}, {entropy, rows * 4},
+        {dlogprob, rows * 4}, {dentropy, rows * 4}, {dlse, rows * 4}};
+    for (const auto& i : ins) {
+        Buffers b;
+        b.add(dlogits, out_bytes);
+        b.add(i.p, i.bytes);
+        if (b.overlap()) return RS_ERR_OVERLAP;
+    }
+    const LogprobsGradArgs a{logits,   row_stride, targets, stats,   entropy, static_cast<uint32_t>(rows),
+                             vocab,    scale,      dlogprob, dentropy, dlse,   dlogits,
+                             dlogits_stride};
+    return launch_logprobs_grad(elem_type, a, stream) == hipSuccess ? RS_OK : RS_ERR_HIP;
+}
+
 const char* rs_status_string(rs_status status) {
     switch (status) {
         case RS_OK: return "RS_OK: success";
         case RS_ERR_INVALID_VALUE: return "RS_ERR_INVALID_VALUE: invalid argument";
         case RS_ERR_UNSUPPORTED_SIZE:
-            return "RS_ERR_UNSUPPORTED_SIZE: n must be below 2^30 (2^29 for 64-bit and two-key sorts)";
+            return "RS_ERR_UNSUPPORTED_SIZE: n must be below 2^30 (2^29 for 64-bit and two-key sorts), "
+                   "and the counts of a call on rows of scores within its limits";
         case RS_ERR_TEMP_TOO_SMALL: return "RS_ERR_TEMP_TOO_SMALL: temporary buffer too small";
         case RS_ERR_OVERLAP: return "RS_ERR_OVERLAP: buffers overlap";
-        case RS_ERR_MISALIGNED: return "RS_ERR_MISALIGNED: pointer not 16-byte aligned";
+        case RS_ERR_MISALIGNED: return "RS_ERR_MISALIGNED: pointer not aligned (to 16 bytes unless the call says less)";
         case RS_ERR_HIP: return "RS_ERR_HIP: HIP launch or runtime error";
     }
     return "unknown rs_status";
