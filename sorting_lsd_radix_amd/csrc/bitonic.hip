@@ -88,17 +88,6 @@ __global__ __launch_bounds__(kBitonicBlock) void bitonic_tile_kernel(
 // ascending half of its bitonic sequence), the larger otherwise.
 constexpr int kBitonicRegThreads = 256;
 
-template <int M>
-__device__ __forceinline__ uint32_t lane_xor(uint32_t x) {
-    static_assert(M == 1 || M == 2 || M == 4 || M == 8 || M == 16 || M == 32, "lane distance");
-    if constexpr (M == 1) return __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, false);   // quad_perm 1,0,3,2
-    else if constexpr (M == 2) return __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, false);   // quad_perm 2,3,0,1
-    else if constexpr (M == 8) return __builtin_amdgcn_mov_dpp(x, 0x128, 0xF, 0xF, false);  // row_ror:8
-    else if constexpr (M == 4 || M == 16)   // swizzle, bitmask mode: lane ^ M within 32 lanes
-        return static_cast<uint32_t>(__builtin_amdgcn_ds_swizzle(static_cast<int>(x), 0x1F | (M << 10)));
-    else return __shfl_xor(x, 32, kWave);
-}
-
 __device__ __forceinline__ uint32_t keep(uint32_t x, uint32_t y, uint32_t e, uint32_t j, uint32_t k) {
     const bool keep_min = ((e & j) == 0) == ((e & k) == 0);
     return keep_min ? min(x, y) : max(x, y);

@@ -78,6 +78,19 @@ __device__ __forceinline__ uint32_t next_chunked_tile(uint32_t* sched, uint32_t 
     return t < tiles ? static_cast<uint32_t>(t) : tiles;
 }
 
+// The value of lane ^ M: DPP quad permutes for 1 and 2, a row rotate for 8,
+// swizzles for 4 and 16, a lane permute for 32.
+template <int M>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t x) {
+    static_assert(M == 1 || M == 2 || M == 4 || M == 8 || M == 16 || M == 32, "lane distance");
+    if constexpr (M == 1) return __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, false);   // quad_perm 1,0,3,2
+    else if constexpr (M == 2) return __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, false);   // quad_perm 2,3,0,1
+    else if constexpr (M == 8) return __builtin_amdgcn_mov_dpp(x, 0x128, 0xF, 0xF, false);  // row_ror:8
+    else if constexpr (M == 4 || M == 16)   // swizzle, bitmask mode: lane ^ M within 32 lanes
+        return static_cast<uint32_t>(__builtin_amdgcn_ds_swizzle(static_cast<int>(x), 0x1F | (M << 10)));
+    else return __shfl_xor(x, 32, kWave);
+}
+
 // Order transform of a sort's keys.  Every key type and direction maps a key
 // to an unsigned pattern whose unsigned order is the wanted order by XOR-ing
 // each 32-bit word with a mask chosen by the key's sign bit (the top bit of

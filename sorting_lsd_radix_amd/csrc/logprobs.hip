@@ -27,6 +27,9 @@ constexpr float kInf = __builtin_huge_valf();
 // powers of two: far below f32's range (sums reach 2^30 * 2^16), and near
 // enough that the rounding of d (16 * 2^-24) stays under a millionth.
 constexpr float kMaxShift = 16.0f;
+// Largest |r a|: above it (logits of some 1e30, as the lowest value of a type
+// that masks a whole row) x a - r a may overflow, and the sums are taken again.
+constexpr float kMaxReference = 1e30f;
 
 // Where a row's parts begin and end: multiples of 8 elements, so that no
 // 16-byte vector of the row is in two parts.
@@ -76,15 +79,21 @@ struct RowVec {
     T v[N];
 };
 
-// Elements v * N .. of a row of n elements; behind its end -inf.  Rows may
-// start on any element, so the compiler is told of no alignment.
+// Rows may start on any element: the compiler is told of no alignment.
+template <class T>
+__device__ __forceinline__ RowVec<T> load_raw(const T* at) {
+    RowVec<T> r;
+    __builtin_memcpy(&r, at, sizeof(r));
+    return r;
+}
+
+// Elements v * N .. of a row of n elements; behind its end -inf.
 template <class T>
 __device__ __forceinline__ void load_vec(const T* in, uint32_t v, uint32_t n, float (&x)[RowVec<T>::N]) {
     constexpr uint32_t N = RowVec<T>::N;
     const uint32_t at = v * N;
     if (at + N <= n) {
-        RowVec<T> r;
-        __builtin_memcpy(&r, in + at, sizeof(r));
+        const RowVec<T> r = load_raw(in + at);
 #pragma unroll
         for (uint32_t j = 0; j < N; ++j) x[j] = static_cast<float>(r.v[j]);
     } else {
@@ -93,41 +102,19 @@ __device__ __forceinline__ void load_vec(const T* in, uint32_t v, uint32_t n, fl
     }
 }
 
-// The 64 lanes' keys in decreasing order (bitonic network).
-__device__ __forceinline__ uint64_t wave_sort_desc(uint64_t k) {
-    const uint32_t lane = lane_id();
-#pragma unroll
-    for (uint32_t size = 2; size <= kWave; size <<= 1) {
-#pragma unroll
-        for (uint32_t j = size >> 1; j > 0; j >>= 1) {
-            const uint64_t o = __shfl_xor(k, j, kWave);
-            const bool keep_max = ((lane & j) == 0) == ((lane & size) == 0);
-            k = keep_max ? (k > o ? k : o) : (k < o ? k : o);
-        }
-    }
-    return k;
-}
-
-// The best 64 of two lists in decreasing order, in decreasing order.
-__device__ __forceinline__ uint64_t wave_merge_desc(uint64_t x, uint64_t y) {
-    const uint32_t lane = lane_id();
-    const uint64_t r = __shfl(y, kWave - 1 - lane, kWave);
-    uint64_t k = x > r ? x : r;   // the best 64, a bitonic sequence
-#pragma unroll
-    for (uint32_t j = kWave / 2; j > 0; j >>= 1) {
-        const uint64_t o = __shfl_xor(k, j, kWave);
-        k = ((lane & j) == 0) ? (k > o ? k : o) : (k < o ? k : o);
-    }
-    return k;
-}
-
 // A logit in a list: its order pattern, then the lower index first.  Lists
 // hold 0 where they have no element.
 __device__ __forceinline__ uint64_t list_key(uint32_t order, uint32_t index) {
     return (static_cast<uint64_t>(order) << 32) | static_cast<uint32_t>(~index);
 }
 
+constexpr uint32_t kLpCandidates = 512;   // logits that a block's threshold may let through
+
 struct SelectShared {
+    uint64_t cand[kLpCandidates];
+    uint32_t max[kLpWaves][kWave];
+    uint32_t flagged[kLpBlock];
+    uint32_t flags, count, tau;
     uint32_t bins[256];
     uint32_t wave[2][kLpWaves];
     uint32_t digit, need, found;
@@ -240,14 +227,181 @@ __device__ __forceinline__ void finish_row(const LogprobsArgs& p, uint32_t row, 
     }
 }
 
+// A thread's running sums over d = x a + c, in powers of two: c = -r a puts the
+// reference r at 0.  One fused multiply-add gives d, rounded once, and every
+// use of the reference goes through the same c, so that its rounding cancels.
+struct Running {
+    float m = -kInf, c = 0.0f, s = 0.0f, t = 0.0f;
+
+    // Called with a new largest m: moves the reference there, unless it is near
+    // enough, or so large (1e30) that x a + c could overflow (slow_sums then).
+    __device__ __forceinline__ void reference(float a) {
+        if (!(fabsf(fmaf(m, a, c)) <= kMaxShift) && fabsf(m * a) <= kMaxReference) {
+            const float d = fmaxf(-m * a - c, -1000.0f);
+            const float f = __builtin_amdgcn_exp2f(d);
+            if (s != 0.0f) {
+                t = (t + s * d) * f;
+                s *= f;
+            }
+            c = -m * a;
+        }
+    }
+
+    template <int N>
+    __device__ __forceinline__ void add(const float (&x)[N], float a) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) m = fmaxf(m, x[j]);
+        reference(a);
+        float s2[2] = {0.0f, 0.0f}, t2[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float d = fmaf(x[j], a, c);
+            const float e = __builtin_amdgcn_exp2f(d);
+            s2[j & 1] += e;
+            t2[j & 1] = fmaf(e, fmaxf(d, -1000.0f), t2[j & 1]);   // a masked logit adds 0 * -1000
+        }
+        s += s2[0] + s2[1];
+        t += t2[0] + t2[1];
+    }
+
+    __device__ __forceinline__ Sums relative_to_largest(float a) const {
+        if (!(fabsf(m * a) <= kMaxReference)) return Sums{m, s == s ? 0.0f : s, 0.0f, 0u};
+        const float d = fmaf(m, a, c);
+        const float f = __builtin_amdgcn_exp2f(-d);
+        return Sums{m, s * f, (t - s * d) * f, 0u};
+    }
+};
+
+// Where |largest * a| > kMaxReference: the block's sums again, with x - m formed
+// before the product.  m is finite.
+template <class T>
+__device__ __attribute__((noinline)) Sums slow_sums(const T* in, uint32_t n, float m, float a, Sums* s_sums) {
+    constexpr uint32_t N = RowVec<T>::N;
+    const uint32_t tid = threadIdx.x;
+    float s = 0.0f, t = 0.0f;
+    for (uint32_t v = tid; v < (n + N - 1) / N; v += kLpBlock) {
+        float x[N];
+        load_vec(in, v, n, x);
+        for (uint32_t j = 0; j < N; ++j) {
+            const float d = (x[j] - m) * a;
+            const float e = __builtin_amdgcn_exp2f(d);
+            s += e;
+            t = fmaf(e, fmaxf(d, -1000.0f), t);
+        }
+    }
+    s = lanes_sum(s);
+    t = lanes_sum(t);
+    __syncthreads();
+    if ((tid & (kWave - 1)) == 0) s_sums[tid / kWave] = Sums{m, s, t, 0u};
+    __syncthreads();
+    Sums z{m, 0.0f, 0.0f, 0u};
+    for (uint32_t w = 0; w < kLpWaves; ++w) {
+        z.s += s_sums[w].s;
+        z.t += s_sums[w].t;
+    }
+    return z;
+}
+
+// Logits before the target by comparisons of single elements, where the
+// target's logit is -inf (no value is below it, see the kernel).
+template <class T>
+__device__ __attribute__((noinline)) uint32_t slow_ahead(const T* in, uint32_t n, uint32_t base, uint32_t target) {
+    constexpr uint32_t N = RowVec<T>::N;
+    uint32_t ahead = 0;
+    for (uint32_t v = threadIdx.x; v < (n + N - 1) / N; v += kLpBlock) {
+        float x[N];
+        load_vec(in, v, n, x);
+        for (uint32_t j = 0; j < N; ++j)
+            ahead += x[j] > -kInf || (x[j] == -kInf && base + v * N + j < target);
+    }
+    return lanes_sum(ahead);
+}
+
+// The first k <= n of a part's logits: wave 0 returns them, lane i the i-th.
+// m is the thread's largest logit (of the vectors tid, tid + kLpBlock, ...).
+//
+// The k-th largest of the threads' largest logits is a threshold that at
+// least k logits reach, and in a row without many ties hardly more: only the
+// threads whose largest reaches it can hold one of the first k, and only
+// their shares are read again, one share by a whole wave at a time.  What
+// reaches the threshold is collected and sorted by (value, index).  Where
+// more is collected than the list takes (ties, or the best logits crowded in
+// few shares), or where masks leave fewer than k, the radix select reads the
+// part instead.
+template <class T>
+__device__ __forceinline__ uint64_t best_of_part(const T* in, uint32_t n, uint32_t base, uint32_t k, float m,
+                                                 SelectShared& s) {
+    constexpr uint32_t N = RowVec<T>::N;
+    const uint32_t tid = threadIdx.x, wave = tid / kWave, lane = tid & (kWave - 1);
+    const uint32_t vecs = (n + N - 1) / N;
+    const bool all = n <= kLpCandidates;   // no threshold: everything is collected
+    const uint32_t lowest = order32(-kInf);
+    if (tid == 0) s.flags = s.count = 0;
+    uint32_t tau = 0;
+    if (!all) {
+        const uint32_t mine = order32(m);
+        s.max[wave][lane] = wave_sort_desc(mine);
+        __syncthreads();
+        if (wave == 0) {
+            uint32_t list = s.max[0][lane];
+#pragma unroll
+            for (int w = 1; w < kLpWaves; ++w) list = wave_merge_desc(list, s.max[w][lane]);
+            if (lane == k - 1) s.tau = list;
+        }
+        __syncthreads();
+        tau = s.tau > lowest ? s.tau : lowest + 1;   // never the masked ones
+        if (mine >= tau) s.flagged[atomicAdd(&s.flags, 1u)] = tid;
+    }
+    __syncthreads();
+    const uint32_t shares = all ? kLpBlock : s.flags;
+    for (uint32_t i = wave; i < shares; i += kLpWaves) {
+        if (__hip_atomic_load(&s.count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) > kLpCandidates) break;
+        const uint32_t share = all ? i : s.flagged[i];
+        for (uint32_t v = share + lane * kLpBlock; v < vecs; v += kWave * kLpBlock) {
+            float x[N];
+            load_vec(in, v, n, x);
+#pragma unroll
+            for (uint32_t j = 0; j < N; ++j) {
+                const uint32_t o = order32(x[j]);
+                if (o >= tau && v * N + j < n) {
+                    const uint32_t at = atomicAdd(&s.count, 1u);
+                    if (at < kLpCandidates) s.cand[at] = list_key(o, base + v * N + j);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const uint32_t count = s.count;
+    if (count > kLpCandidates || count < k) {
+        radix_select(in, n, base, k, s);
+        return wave == 0 ? wave_sort_desc(lane < k ? s.top[lane] : uint64_t{0}) : 0;
+    }
+    uint64_t key = 0;
+    if (wave == 0) {
+        for (uint32_t i = 0; i < count; i += kWave) {
+            const uint64_t next = wave_sort_desc(i + lane < count ? s.cand[i + lane] : uint64_t{0});
+            key = i == 0 ? next : wave_merge_desc(key, next);
+        }
+    }
+    return key;
+}
+
 // Block (part, row): the sums and, with top_k, the list of one part of a row.
 // With one part the row is finished here; otherwise part q of a row leaves
 // its sums at sums[row * parts + q] and its list at lists[(row * parts + q) * top_k].
+//
+// Thread t reads the 16-byte vectors t, t + 256, ... of the part, 16 elements
+// a step, the next step's loads in flight.  Logits before the target are
+// counted as wave masks (a compare and scalar instructions): behind the
+// target those above it, in front of it those above the next value below it,
+// which are the ones not below it; the vector that holds the target is
+// counted as behind it and its equal logits in front of it added.
 template <int ELEM, bool RANK, bool TOP>
 __global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LogprobsArgs p, Parts parts, Sums* __restrict__ sums,
                                                             uint64_t* __restrict__ lists) {
     using T = typename Elem<ELEM>::T;
     constexpr uint32_t N = RowVec<T>::N;
+    constexpr uint32_t U = 16 / N;   // vectors of a step
     __shared__ Sums s_sums[kLpWaves];
     __shared__ SelectShared s_select;
     const uint32_t tid = threadIdx.x, wave = tid / kWave, lane = tid & (kWave - 1);
@@ -264,63 +418,70 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LogprobsArgs p, Part
     const uint32_t target = p.targets ? p.targets[row] : 0xFFFFFFFFu;
     const bool has_target = target < p.vocab;
     const float x_target = has_target ? static_cast<float>(whole[target]) : 0.0f;
+    // the next value below the target's logit; vectors before this one are in front of the target
+    const uint32_t xt = __float_as_uint(x_target);
+    const float below = (xt << 1) == 0 ? __uint_as_float(0x80000001u) : __uint_as_float((xt >> 31) ? xt + 1 : xt - 1);
+    const uint32_t at_target = has_target && target >= base ? (target - base) / N : 0u;
 
-    float m = -kInf, r = 0.0f, s = 0.0f, t = 0.0f;
-    uint32_t ahead = 0;
-    const uint32_t vecs = (n + N - 1) / N;
-    for (uint32_t v = tid; v < vecs; v += kLpBlock) {
-        float x[N];
-        load_vec(in, v, n, x);
-        float top = x[0];
+    Running r;
+    uint32_t ahead = 0;   // of the wave
+    auto count_ahead = [&](const float* x, uint32_t v) {
+        const float over = v < at_target ? below : x_target;
 #pragma unroll
-        for (uint32_t j = 1; j < N; ++j) top = fmaxf(top, x[j]);
-        if (top > m) {
-            m = top;
-            if (!(fabsf((m - r) * a) <= kMaxShift) && m < kInf) {
-                if (s != 0.0f) {
-                    const float d = fmaxf((r - m) * a, -1000.0f);
-                    const float f = __builtin_amdgcn_exp2f(d);
-                    t = (t + s * d) * f;
-                    s *= f;
-                }
-                r = m;
+        for (uint32_t j = 0; j < N; ++j) ahead += static_cast<uint32_t>(__builtin_popcountll(ballot(x[j] > over)));
+    };
+    const uint32_t vecs = (n + N - 1) / N;
+    const uint32_t steps = n / (kLpBlock * 16);
+    if (steps > 0) {
+        RowVec<T> raw[U];
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) raw[u] = load_raw(in + (u * kLpBlock + tid) * N);
+        for (uint32_t i = 0; i < steps; ++i) {
+            const uint32_t v = i * (U * kLpBlock) + tid;
+            float x[16];
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u)
+#pragma unroll
+                for (uint32_t j = 0; j < N; ++j) x[u * N + j] = static_cast<float>(raw[u].v[j]);
+            if (i + 1 < steps) {
+#pragma unroll
+                for (uint32_t u = 0; u < U; ++u) raw[u] = load_raw(in + (v + (U + u) * kLpBlock) * N);
+            }
+            r.add(x, a);
+            if (RANK) {
+#pragma unroll
+                for (uint32_t u = 0; u < U; ++u) count_ahead(x + u * N, v + u * kLpBlock);
             }
         }
-#pragma unroll
-        for (uint32_t j = 0; j < N; ++j) {
-            const float d = (x[j] - r) * a;
-            const float e = __builtin_amdgcn_exp2f(d);
-            s += e;
-            t = fmaf(e, fmaxf(d, -1000.0f), t);
-        }
-        if (RANK) {
-#pragma unroll
-            for (uint32_t j = 0; j < N; ++j)
-                ahead += (x[j] > x_target || (x[j] == x_target && base + v * N + j < target)) ? 1u : 0u;
-        }
     }
-    // relative to the thread's largest
-    Sums z{m, s, t, ahead};
-    if (s != 0.0f && m < kInf) {
-        const float d = (r - m) * a;
-        const float f = __builtin_amdgcn_exp2f(d);
-        z.s = s * f;
-        z.t = (t + s * d) * f;
+    for (uint32_t v = steps * (U * kLpBlock) + tid; v - tid < vecs; v += kLpBlock) {   // uniform
+        float x[N];
+        load_vec(in, v, n, x);
+        r.add(x, a);
+        if (RANK) count_ahead(x, v);
     }
-#pragma unroll
-    for (int off = kWave / 2; off > 0; off >>= 1) {
-        const Sums o{__shfl_xor(z.m, off, kWave), __shfl_xor(z.s, off, kWave), __shfl_xor(z.t, off, kWave),
-                     __shfl_xor(z.ahead, off, kWave)};
-        z = join(z, o, a);
+    if (RANK && has_target && x_target == -kInf) {
+        ahead = slow_ahead(in, n, base, target);
+    } else if (RANK && has_target && target >= base && target - base < n && wave == 0) {
+        const uint32_t at = at_target * N + lane;
+        ahead += static_cast<uint32_t>(__builtin_popcountll(
+            ballot(lane < N && base + at < target && static_cast<float>(in[at < n ? at : 0]) == x_target)));
     }
+    Sums z = r.relative_to_largest(a);
+    z = lanes_reduce(z, [&](const Sums& x, const Sums& y) { return join(x, y, a); });
+    z.ahead = ahead;
     if (lane == 0) s_sums[wave] = z;
-    if (TOP) radix_select(in, n, base, p.top_k < n ? p.top_k : n, s_select);
     __syncthreads();
-    if (wave != 0) return;
     z = s_sums[0];
     for (uint32_t w = 1; w < kLpWaves; ++w) z = join(z, s_sums[w], a);
+    if (fabsf(z.m) < kInf && fabsf(z.m * a) > kMaxReference) {
+        const uint32_t counted = z.ahead;
+        z = slow_sums(in, n, z.m, a, s_sums);
+        z.ahead = counted;
+    }
     uint64_t key = 0;
-    if (TOP) key = wave_sort_desc(lane < p.top_k && lane < n ? s_select.top[lane] : 0ull);
+    if (TOP) key = best_of_part(in, n, base, p.top_k < n ? p.top_k : n, r.m, s_select);
+    if (wave != 0) return;
     if (parts.count == 1) {
         finish_row(p, row, z, x_target, has_target, key);
     } else {
@@ -329,32 +490,44 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LogprobsArgs p, Part
     }
 }
 
-// One wave a row: joins the parts.
+// One block a row joins its parts: wave w merges the lists w, w + 8, ..., then
+// the waves' lists merge in pairs.
+constexpr int kLpJoinWaves = 8;
 template <int ELEM>
-__global__ __launch_bounds__(kWave) void logprobs_join_kernel(LogprobsArgs p, Parts parts, const Sums* __restrict__ sums,
-                                                              const uint64_t* __restrict__ lists) {
+__global__ __launch_bounds__(kLpJoinWaves* kWave) void logprobs_join_kernel(LogprobsArgs p, Parts parts,
+                                                                            const Sums* __restrict__ sums,
+                                                                            const uint64_t* __restrict__ lists) {
     using T = typename Elem<ELEM>::T;
-    const uint32_t row = block_id(), lane = threadIdx.x;
+    __shared__ uint64_t s_list[kLpJoinWaves][kWave];
+    const uint32_t row = block_id(), wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
     if (row >= p.rows) return;
     const float a = p.scale * kLog2e;
-    const uint32_t target = p.targets ? p.targets[row] : 0xFFFFFFFFu;
-    const bool has_target = target < p.vocab;
-    const float x_target =
-        has_target ? static_cast<float>(static_cast<const T*>(p.logits)[row * p.row_stride + target]) : 0.0f;
     const uint64_t first = static_cast<uint64_t>(row) * parts.count;
     Sums z{-kInf, 0.0f, 0.0f, 0u};
-    if (lane < parts.count) z = sums[first + lane];   // at most kWave parts
-#pragma unroll
-    for (int off = kWave / 2; off > 0; off >>= 1) {
-        const Sums o{__shfl_xor(z.m, off, kWave), __shfl_xor(z.s, off, kWave), __shfl_xor(z.t, off, kWave),
-                     __shfl_xor(z.ahead, off, kWave)};
-        z = join(z, o, a);
+    uint32_t target = 0xFFFFFFFFu;
+    float x_target = 0.0f;
+    if (wave == 0) {
+        if (lane < parts.count) z = sums[first + lane];   // at most kWave parts
+        if (p.targets) target = p.targets[row];
+        if (target < p.vocab)
+            x_target = static_cast<float>(static_cast<const T*>(p.logits)[row * p.row_stride + target]);
     }
     uint64_t key = 0;
-    if (p.top_k)
-        for (uint32_t q = 0; q < parts.count; ++q)
-            key = wave_merge_desc(key, lane < p.top_k ? lists[(first + q) * p.top_k + lane] : 0ull);
-    finish_row(p, row, z, x_target, has_target, key);
+    if (p.top_k) {
+        for (uint32_t q = wave; q < parts.count; q += kLpJoinWaves) {
+            const uint64_t next = lane < p.top_k ? lists[(first + q) * p.top_k + lane] : uint64_t{0};
+            key = q == wave ? next : wave_merge_desc(key, next);
+        }
+#pragma unroll
+        for (uint32_t half = kLpJoinWaves / 2; half > 0; half >>= 1) {
+            if (wave >= half && wave < 2 * half) s_list[wave][lane] = key;
+            __syncthreads();
+            if (wave < half) key = wave_merge_desc(key, s_list[wave + half][lane]);
+        }
+    }
+    if (wave != 0) return;
+    z = lanes_reduce(z, [&](const Sums& x, const Sums& y) { return join(x, y, a); });
+    finish_row(p, row, z, x_target, target < p.vocab, key);
 }
 static_assert(kLpMaxParts <= kWave, "the joining wave has a lane for each part");
 
@@ -423,7 +596,7 @@ hipError_t logprobs_elem(const LogprobsArgs& p, void* temp, hipStream_t stream) 
     timing_after(stream);
     if (e != hipSuccess || parts.count == 1) return e;
     timing_before(stream, RS_KERNEL_LOGPROBS_JOIN);
-    logprobs_join_kernel<ELEM><<<many_blocks(p.rows), kWave, 0, stream>>>(p, parts, sums, lists);
+    logprobs_join_kernel<ELEM><<<many_blocks(p.rows), kLpJoinWaves * kWave, 0, stream>>>(p, parts, sums, lists);
     e = hipGetLastError();
     timing_after(stream);
     return e;

@@ -44,7 +44,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
         x[j] = e < a.experts ? static_cast<float>(in[e]) : -__builtin_huge_valf();
         m = fmaxf(m, x[j]);
     }
-    m = wave_max(m);
+    m = lanes_max(m);
     const bool empty = m == -__builtin_huge_valf();   // of softmax rows with NaN too: the sum is NaN then
     double total = 1.0;
     if (!SIGMOID) {
@@ -53,7 +53,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
         for (int j = 0; j < V; ++j)
             if (lane * V + j < a.experts)
                 mine += (empty && x[j] == x[j]) ? 0.0 : exp(static_cast<double>(x[j]) - static_cast<double>(m));
-        total = wave_sum(mine);
+        total = lanes_sum(mine);
     }
     auto prob = [&](float v) -> double {
         if (SIGMOID) return 1.0 / (1.0 + exp(-static_cast<double>(v)));
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
     const double p = mine ? prob(s_x[wave][chosen]) : 0.0;
     double w = static_cast<double>(a.scale) * p;
     if (a.renormalize) {
-        const double sum = wave_sum(p);
+        const double sum = lanes_sum(p);
         w = sum == 0.0 ? 0.0 : w / sum;
     }
     if (mine) {
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(RouteGra
     const uint32_t id = mine ? a.ids[at] : 0xFFFFFFFFu;
     const float w = mine ? a.weights[at] : 0.0f;
     const float dw = mine ? a.dweights[at] : 0.0f;
-    const float d = wave_sum(dw * w);
+    const float d = lanes_sum(dw * w);
     float part = w * (a.renormalize ? dw - d / a.scale : dw);   // the choice's own term
 
     float dx[V];
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(RouteGra
             x[j] = e < a.experts ? static_cast<float>(in[e]) : -__builtin_huge_valf();
             m = fmaxf(m, x[j]);
         }
-        m = wave_max(m);
+        m = lanes_max(m);
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j)
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(RouteGra
                 x[j] = expf(x[j] - m);
                 sum += x[j];
             }
-        sum = wave_sum(sum);
+        sum = lanes_sum(sum);
         const bool empty = m == -__builtin_huge_valf();   // p = 0 (and d = 0, or NaN where the weights are)
 #pragma unroll
         for (int j = 0; j < V; ++j) dx[j] = -(empty ? 0.0f : x[j] / sum) * d;

@@ -50,17 +50,74 @@ __device__ __forceinline__ uint64_t order64_masked(double x) {
     return (x > -__builtin_huge_val()) ? u ^ (sign | 0x8000000000000000ull) : 1ull;
 }
 
-__device__ __forceinline__ float wave_max(float x) {
+// The value of lane ^ M, of any type of whole words.
+template <int M, class T>
+__device__ __forceinline__ T lane_xor_of(T x) {
+    static_assert(sizeof(T) % 4 == 0, "whole words");
+    uint32_t w[sizeof(T) / 4];
+    __builtin_memcpy(w, &x, sizeof(T));
 #pragma unroll
-    for (int off = kWave / 2; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor(x, off, kWave));
+    for (uint32_t& v : w) v = lane_xor<M>(v);
+    __builtin_memcpy(&x, w, sizeof(T));
     return x;
 }
 
-template <class T>
-__device__ __forceinline__ T wave_sum(T x) {
-#pragma unroll
-    for (int off = kWave / 2; off > 0; off >>= 1) x += __shfl_xor(x, off, kWave);
+// op over aligned groups of N lanes; every lane of a group gets the result.
+template <int N = kWave, class T, class Op>
+__device__ __forceinline__ T lanes_reduce(T x, Op op) {
+    if constexpr (N > 1) x = op(x, lane_xor_of<1>(x));
+    if constexpr (N > 2) x = op(x, lane_xor_of<2>(x));
+    if constexpr (N > 4) x = op(x, lane_xor_of<4>(x));
+    if constexpr (N > 8) x = op(x, lane_xor_of<8>(x));
+    if constexpr (N > 16) x = op(x, lane_xor_of<16>(x));
+    if constexpr (N > 32) x = op(x, lane_xor_of<32>(x));
     return x;
+}
+
+template <int N = kWave, class T>
+__device__ __forceinline__ T lanes_max(T x) {
+    return lanes_reduce<N>(x, [](T a, T b) { return a > b ? a : b; });
+}
+template <int N = kWave>
+__device__ __forceinline__ float lanes_max(float x) {
+    return lanes_reduce<N>(x, [](float a, float b) { return fmaxf(a, b); });
+}
+
+template <int N = kWave, class T>
+__device__ __forceinline__ T lanes_sum(T x) {
+    return lanes_reduce<N>(x, [](T a, T b) { return a + b; });
+}
+
+// One step of a bitonic network over the wave's lanes: of lane and lane ^ J
+// the lower keeps the larger where (lane & SIZE) == 0, the smaller elsewhere.
+template <int SIZE, int J, class T>
+__device__ __forceinline__ T lanes_merge_steps(T k, uint32_t lane) {
+    const T o = lane_xor_of<J>(k);
+    const bool keep_max = ((lane & J) == 0) == ((lane & SIZE) == 0);
+    k = ((k > o) == keep_max) ? k : o;   // unsigned keys; of equal ones either will do
+    if constexpr (J > 1) k = lanes_merge_steps<SIZE, J / 2>(k, lane);
+    return k;
+}
+
+// The 64 lanes' keys in decreasing order.
+template <int SIZE = 2, class T>
+__device__ __forceinline__ T wave_sort_desc(T k) {
+    k = lanes_merge_steps<SIZE, SIZE / 2>(k, lane_id());
+    if constexpr (SIZE < kWave) k = wave_sort_desc<SIZE * 2>(k);
+    return k;
+}
+
+// The best 64 of two lists in decreasing order, in decreasing order: the
+// larger of lane l of one and lane 63 - l of the other form a bitonic sequence.
+template <class T>
+__device__ __forceinline__ T wave_merge_desc(T x, T y) {
+    T r = lane_xor_of<1>(y);
+    r = lane_xor_of<2>(r);
+    r = lane_xor_of<4>(r);
+    r = lane_xor_of<8>(r);
+    r = lane_xor_of<16>(r);
+    r = lane_xor_of<32>(r);
+    return lanes_merge_steps<kWave, kWave / 2>(x > r ? x : r, lane_id());
 }
 
 }  // namespace rs
