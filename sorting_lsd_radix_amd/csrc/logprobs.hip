@@ -79,12 +79,17 @@ struct RowVec {
     T v[N];
 };
 
-// Rows may start on any element: the compiler is told of no alignment.
-template <class T>
+// A 16-byte vector that may start on any element (2 bytes, the smallest).
+typedef uint32_t AnyVec __attribute__((ext_vector_type(4), aligned(2)));
+
+// STREAM: the data is read once and is not kept in the caches.
+template <bool STREAM, class T>
 __device__ __forceinline__ RowVec<T> load_raw(const T* at) {
-    RowVec<T> r;
-    __builtin_memcpy(&r, at, sizeof(r));
-    return r;
+    const AnyVec* p = reinterpret_cast<const AnyVec*>(at);
+    AnyVec v;
+    if constexpr (STREAM) v = __builtin_nontemporal_load(p);
+    else v = *p;
+    return __builtin_bit_cast(RowVec<T>, v);
 }
 
 // Elements v * N .. of a row of n elements; behind its end -inf.
@@ -93,7 +98,7 @@ __device__ __forceinline__ void load_vec(const T* in, uint32_t v, uint32_t n, fl
     constexpr uint32_t N = RowVec<T>::N;
     const uint32_t at = v * N;
     if (at + N <= n) {
-        const RowVec<T> r = load_raw(in + at);
+        const RowVec<T> r = load_raw<false>(in + at);
 #pragma unroll
         for (uint32_t j = 0; j < N; ++j) x[j] = static_cast<float>(r.v[j]);
     } else {
@@ -133,7 +138,7 @@ __device__ void radix_select(const T* in, uint32_t n, uint32_t base, uint32_t k,
     const uint32_t vecs = (n + N - 1) / N;
     uint32_t prefix = 0, need = k;
     for (int shift = 24; shift >= 0; shift -= 8) {
-        s.bins[tid] = 0;
+        if (tid < 256) s.bins[tid] = 0;
         __syncthreads();
         for (uint32_t v = tid; v < vecs; v += kLpBlock) {
             float x[N];
@@ -146,7 +151,7 @@ __device__ void radix_select(const T* in, uint32_t n, uint32_t base, uint32_t k,
         }
         __syncthreads();
         // thread t holds digit 255 - t: how many have a larger digit
-        const uint32_t own = s.bins[255 - tid];
+        const uint32_t own = tid < 256 ? s.bins[255 - tid] : 0u;
         const uint32_t incl = wave_inclusive_sum(own);
         if (lane == kWave - 1) s.wave[0][wave] = incl;
         __syncthreads();
@@ -247,10 +252,10 @@ struct Running {
         }
     }
 
+    // Adds the logits of one step; `top` is the largest of them.
     template <int N>
-    __device__ __forceinline__ void add(const float (&x)[N], float a) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) m = fmaxf(m, x[j]);
+    __device__ __forceinline__ void add(const float (&x)[N], float top, float a) {
+        m = fmaxf(m, top);
         reference(a);
         float s2[2] = {0.0f, 0.0f}, t2[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -317,57 +322,82 @@ __device__ __attribute__((noinline)) uint32_t slow_ahead(const T* in, uint32_t n
     return lanes_sum(ahead);
 }
 
+// The steps in which a thread read its share of a part: 16 elements each (U
+// vectors, U * kLpBlock vectors apart from step to step), then single vectors.
+// Of them TOP keeps the largest steps' largest logits, and the first's number.
+struct Steps {
+    float best = -kInf, next = -kInf;   // the two largest of the steps' largest logits
+    uint32_t at = 0;                    // the step of `best`
+    __device__ __forceinline__ void add(float top, uint32_t step) {
+        at = top > best ? step : at;
+        next = __builtin_amdgcn_fmed3f(top, best, next);
+        best = fmaxf(best, top);
+    }
+};
+
 // The first k <= n of a part's logits: wave 0 returns them, lane i the i-th.
-// m is the thread's largest logit (of the vectors tid, tid + kLpBlock, ...).
 //
 // The k-th largest of the threads' largest logits is a threshold that at
 // least k logits reach, and in a row without many ties hardly more: only the
-// threads whose largest reaches it can hold one of the first k, and only
-// their shares are read again, one share by a whole wave at a time.  What
-// reaches the threshold is collected and sorted by (value, index).  Where
-// more is collected than the list takes (ties, or the best logits crowded in
-// few shares), or where masks leave fewer than k, the radix select reads the
-// part instead.
+// threads whose largest reaches it can hold one of the first k.  Such a thread
+// reads the step that holds its largest again; where a second step of it
+// reaches the threshold too, a whole wave reads the thread's share.  (Reading
+// whole shares in every case cost 20 us of 123 at 2048 rows of 131072 bf16
+// logits.)  What reaches the threshold is collected and sorted by (value,
+// index).  Where more is collected than the list takes (ties, or the best
+// logits crowded in few shares), or where masks leave fewer than k, the radix
+// select reads the part instead.
 template <class T>
-__device__ __forceinline__ uint64_t best_of_part(const T* in, uint32_t n, uint32_t base, uint32_t k, float m,
-                                                 SelectShared& s) {
+__device__ __forceinline__ uint64_t best_of_part(const T* in, uint32_t n, uint32_t base, uint32_t k,
+                                                 const Steps& steps, uint32_t full_steps, SelectShared& s) {
     constexpr uint32_t N = RowVec<T>::N;
+    constexpr uint32_t U = 16 / N;
     const uint32_t tid = threadIdx.x, wave = tid / kWave, lane = tid & (kWave - 1);
     const uint32_t vecs = (n + N - 1) / N;
     const bool all = n <= kLpCandidates;   // no threshold: everything is collected
     const uint32_t lowest = order32(-kInf);
-    if (tid == 0) s.flags = s.count = 0;
     uint32_t tau = 0;
-    if (!all) {
-        const uint32_t mine = order32(m);
-        s.max[wave][lane] = wave_sort_desc(mine);
-        __syncthreads();
-        if (wave == 0) {
-            uint32_t list = s.max[0][lane];
+    auto collect = [&](uint32_t v) {
+        float x[N];
+        load_vec(in, v, n, x);
 #pragma unroll
-            for (int w = 1; w < kLpWaves; ++w) list = wave_merge_desc(list, s.max[w][lane]);
-            if (lane == k - 1) s.tau = list;
+        for (uint32_t j = 0; j < N; ++j) {
+            const uint32_t o = order32(x[j]);
+            if (o >= tau && v * N + j < n) {
+                const uint32_t at = atomicAdd(&s.count, 1u);
+                if (at < kLpCandidates) s.cand[at] = list_key(o, base + v * N + j);
+            }
         }
+    };
+    if (tid == 0) s.flags = s.count = 0;
+    if (all) {
+        __syncthreads();
+        for (uint32_t v = tid; v < vecs; v += kLpBlock) collect(v);
+    } else {
+        const uint32_t mine = order32(steps.best);
+        uint32_t list = wave_sort_desc(mine);
+#pragma unroll
+        for (uint32_t half = kLpWaves / 2; half > 0; half >>= 1) {
+            if (wave >= half && wave < 2 * half) s.max[wave][lane] = list;
+            __syncthreads();
+            if (wave < half) list = wave_merge_desc(list, s.max[wave + half][lane]);
+        }
+        if (wave == 0 && lane == k - 1) s.tau = list;
         __syncthreads();
         tau = s.tau > lowest ? s.tau : lowest + 1;   // never the masked ones
-        if (mine >= tau) s.flagged[atomicAdd(&s.flags, 1u)] = tid;
-    }
-    __syncthreads();
-    const uint32_t shares = all ? kLpBlock : s.flags;
-    for (uint32_t i = wave; i < shares; i += kLpWaves) {
-        if (__hip_atomic_load(&s.count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) > kLpCandidates) break;
-        const uint32_t share = all ? i : s.flagged[i];
-        for (uint32_t v = share + lane * kLpBlock; v < vecs; v += kWave * kLpBlock) {
-            float x[N];
-            load_vec(in, v, n, x);
-#pragma unroll
-            for (uint32_t j = 0; j < N; ++j) {
-                const uint32_t o = order32(x[j]);
-                if (o >= tau && v * N + j < n) {
-                    const uint32_t at = atomicAdd(&s.count, 1u);
-                    if (at < kLpCandidates) s.cand[at] = list_key(o, base + v * N + j);
-                }
+        if (mine >= tau) {
+            if (order32(steps.next) >= tau) {
+                s.flagged[atomicAdd(&s.flags, 1u)] = tid;
+            } else {
+                const bool whole = steps.at < full_steps;
+                const uint32_t v = tid + kLpBlock * (whole ? steps.at * U : full_steps * U + steps.at - full_steps);
+                for (uint32_t u = 0; u < (whole ? U : 1); ++u) collect(v + u * kLpBlock);
             }
+        }
+        __syncthreads();
+        for (uint32_t i = wave; i < s.flags; i += kLpWaves) {
+            if (__hip_atomic_load(&s.count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) > kLpCandidates) break;
+            for (uint32_t v = s.flagged[i] + lane * kLpBlock; v < vecs; v += kWave * kLpBlock) collect(v);
         }
     }
     __syncthreads();
@@ -396,7 +426,7 @@ __device__ __forceinline__ uint64_t best_of_part(const T* in, uint32_t n, uint32
 // target those above it, in front of it those above the next value below it,
 // which are the ones not below it; the vector that holds the target is
 // counted as behind it and its equal logits in front of it added.
-template <int ELEM, bool RANK, bool TOP>
+template <int ELEM, bool TOP, bool STREAM>
 __global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LogprobsArgs p, Parts parts, Sums* __restrict__ sums,
                                                             uint64_t* __restrict__ lists) {
     using T = typename Elem<ELEM>::T;
@@ -417,16 +447,22 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LogprobsArgs p, Part
 
     const uint32_t target = p.targets ? p.targets[row] : 0xFFFFFFFFu;
     const bool has_target = target < p.vocab;
+    const bool rank = has_target && p.rank != nullptr;
     const float x_target = has_target ? static_cast<float>(whole[target]) : 0.0f;
-    // the next value below the target's logit; vectors before this one are in front of the target
+    // what a counted logit is above: behind the target its logit, in front of it (vectors before
+    // at_target) the next value below; +inf counts nothing
     const uint32_t xt = __float_as_uint(x_target);
-    const float below = (xt << 1) == 0 ? __uint_as_float(0x80000001u) : __uint_as_float((xt >> 31) ? xt + 1 : xt - 1);
-    const uint32_t at_target = has_target && target >= base ? (target - base) / N : 0u;
+    const float over_behind = rank ? x_target : kInf;
+    const float over_front = !rank ? kInf
+                             : (xt << 1) == 0 ? __uint_as_float(0x80000001u)
+                                              : __uint_as_float((xt >> 31) ? xt + 1 : xt - 1);
+    const uint32_t at_target = rank && target >= base ? (target - base) / N : 0u;
 
     Running r;
+    Steps top_steps;
     uint32_t ahead = 0;   // of the wave
     auto count_ahead = [&](const float* x, uint32_t v) {
-        const float over = v < at_target ? below : x_target;
+        const float over = v < at_target ? over_front : over_behind;
 #pragma unroll
         for (uint32_t j = 0; j < N; ++j) ahead += static_cast<uint32_t>(__builtin_popcountll(ballot(x[j] > over)));
     };
@@ -434,35 +470,50 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LogprobsArgs p, Part
     const uint32_t steps = n / (kLpBlock * 16);
     if (steps > 0) {
         RowVec<T> raw[U];
+        float x[16];
+        auto load = [&](uint32_t i) {
 #pragma unroll
-        for (uint32_t u = 0; u < U; ++u) raw[u] = load_raw(in + (u * kLpBlock + tid) * N);
-        for (uint32_t i = 0; i < steps; ++i) {
-            const uint32_t v = i * (U * kLpBlock) + tid;
-            float x[16];
+            for (uint32_t u = 0; u < U; ++u) raw[u] = load_raw<STREAM>(in + ((i * U + u) * kLpBlock + tid) * N);
+        };
+        auto convert = [&] {
 #pragma unroll
             for (uint32_t u = 0; u < U; ++u)
 #pragma unroll
                 for (uint32_t j = 0; j < N; ++j) x[u * N + j] = static_cast<float>(raw[u].v[j]);
-            if (i + 1 < steps) {
+        };
+        auto add = [&](uint32_t i) {
+            float top = x[0];
 #pragma unroll
-                for (uint32_t u = 0; u < U; ++u) raw[u] = load_raw(in + (v + (U + u) * kLpBlock) * N);
-            }
-            r.add(x, a);
-            if (RANK) {
+            for (int j = 1; j < 16; ++j) top = fmaxf(top, x[j]);
+            r.add(x, top, a);
+            if (TOP) top_steps.add(top, i);
+            if (ballot(top > over_front) != 0) {   // a likely target has few above it
 #pragma unroll
-                for (uint32_t u = 0; u < U; ++u) count_ahead(x + u * N, v + u * kLpBlock);
+                for (uint32_t u = 0; u < U; ++u) count_ahead(x + u * N, (i * U + u) * kLpBlock + tid);
             }
+        };
+        load(0);
+        for (uint32_t i = 0; i + 1 < steps; ++i) {
+            convert();
+            load(i + 1);
+            add(i);
         }
+        convert();
+        add(steps - 1);
     }
-    for (uint32_t v = steps * (U * kLpBlock) + tid; v - tid < vecs; v += kLpBlock) {   // uniform
+    for (uint32_t v = steps * (U * kLpBlock) + tid, i = steps; v - tid < vecs; v += kLpBlock, ++i) {   // uniform
         float x[N];
         load_vec(in, v, n, x);
-        r.add(x, a);
-        if (RANK) count_ahead(x, v);
+        float top = x[0];
+#pragma unroll
+        for (uint32_t j = 1; j < N; ++j) top = fmaxf(top, x[j]);
+        r.add(x, top, a);
+        if (TOP) top_steps.add(top, i);
+        if (ballot(top > over_front) != 0) count_ahead(x, v);
     }
-    if (RANK && has_target && x_target == -kInf) {
+    if (rank && x_target == -kInf) {
         ahead = slow_ahead(in, n, base, target);
-    } else if (RANK && has_target && target >= base && target - base < n && wave == 0) {
+    } else if (rank && target >= base && target - base < n && wave == 0) {
         const uint32_t at = at_target * N + lane;
         ahead += static_cast<uint32_t>(__builtin_popcountll(
             ballot(lane < N && base + at < target && static_cast<float>(in[at < n ? at : 0]) == x_target)));
@@ -480,7 +531,7 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LogprobsArgs p, Part
         z.ahead = counted;
     }
     uint64_t key = 0;
-    if (TOP) key = best_of_part(in, n, base, p.top_k < n ? p.top_k : n, r.m, s_select);
+    if (TOP) key = best_of_part(in, n, base, p.top_k < n ? p.top_k : n, top_steps, steps, s_select);
     if (wave != 0) return;
     if (parts.count == 1) {
         finish_row(p, row, z, x_target, has_target, key);
@@ -581,17 +632,22 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_grad_kernel(LogprobsGradArg
     }
 }
 
-template <int ELEM, bool RANK>
+// Above this size (the last-level cache's) logits are read around the caches:
+// 2048 rows of 131072 bf16 101 -> 87 us, of f32 180 -> 157 us; below it the
+// caches may still hold them (257 rows of 50021 f32: 18.6 us against 20.0).
+constexpr uint64_t kLpStreamBytes = uint64_t{1} << 28;
+
+template <int ELEM>
 hipError_t logprobs_elem(const LogprobsArgs& p, void* temp, hipStream_t stream) {
     const Parts parts = lp_parts(p.rows, p.vocab);
     const uint64_t blocks = static_cast<uint64_t>(p.rows) * parts.count;
+    const bool around = static_cast<uint64_t>(p.rows) * p.vocab * sizeof(typename Elem<ELEM>::T) > kLpStreamBytes;
     uint64_t* lists = static_cast<uint64_t*>(temp);
     Sums* sums = reinterpret_cast<Sums*>(lists + (parts.count > 1 ? blocks * p.top_k : 0));
+    const auto kernel = p.top_k ? (around ? logprobs_kernel<ELEM, true, true> : logprobs_kernel<ELEM, true, false>)
+                                : (around ? logprobs_kernel<ELEM, false, true> : logprobs_kernel<ELEM, false, false>);
     timing_before(stream, RS_KERNEL_LOGPROBS);
-    if (p.top_k)
-        logprobs_kernel<ELEM, RANK, true><<<many_blocks(blocks), kLpBlock, 0, stream>>>(p, parts, sums, lists);
-    else
-        logprobs_kernel<ELEM, RANK, false><<<many_blocks(blocks), kLpBlock, 0, stream>>>(p, parts, sums, lists);
+    kernel<<<many_blocks(blocks), kLpBlock, 0, stream>>>(p, parts, sums, lists);
     hipError_t e = hipGetLastError();
     timing_after(stream);
     if (e != hipSuccess || parts.count == 1) return e;
@@ -623,12 +679,9 @@ size_t logprobs_temp_bytes(uint64_t rows, uint32_t vocab, uint32_t top_k) {
 
 hipError_t launch_logprobs(int elem_type, const LogprobsArgs& p, void* temp, hipStream_t stream) {
     switch (elem_type) {
-    case RS_ELEM_F32:
-        return p.rank ? logprobs_elem<RS_ELEM_F32, true>(p, temp, stream) : logprobs_elem<RS_ELEM_F32, false>(p, temp, stream);
-    case RS_ELEM_F16:
-        return p.rank ? logprobs_elem<RS_ELEM_F16, true>(p, temp, stream) : logprobs_elem<RS_ELEM_F16, false>(p, temp, stream);
-    default:
-        return p.rank ? logprobs_elem<RS_ELEM_BF16, true>(p, temp, stream) : logprobs_elem<RS_ELEM_BF16, false>(p, temp, stream);
+    case RS_ELEM_F32: return logprobs_elem<RS_ELEM_F32>(p, temp, stream);
+    case RS_ELEM_F16: return logprobs_elem<RS_ELEM_F16>(p, temp, stream);
+    default: return logprobs_elem<RS_ELEM_BF16>(p, temp, stream);
     }
 }
 
