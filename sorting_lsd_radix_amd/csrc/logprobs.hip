@@ -224,9 +224,7 @@ __device__ __forceinline__ void finish_row(const LogprobsArgs& p, uint32_t row, 
         if (p.rank) p.rank[row] = has_target && x_target == x_target ? z.ahead : 0xFFFFFFFFu;
     }
     if (lane < p.top_k) {
-        const uint32_t o = static_cast<uint32_t>(key >> 32);
-        const float x = o == 1u ? __builtin_nanf("")
-                                : __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o);
+        const float x = value_of_order32(static_cast<uint32_t>(key >> 32));
         p.top_ids[static_cast<uint64_t>(row) * p.top_k + lane] = ~static_cast<uint32_t>(key);
         p.top_logprobs[static_cast<uint64_t>(row) * p.top_k + lane] = ln_p(x);
     }

@@ -1,9 +1,13 @@
 // route.hip -- a router's choices: the best experts of each row of scores,
 // their weights, and the weights' gradient.
 //
-// One wave works on one row.  The row's scores are read once into registers:
-// lane l holds experts l * V .. l * V + V - 1, so that (lane, slot) is the
-// order of the experts and a tie between lanes goes to the lower one.
+// A row is the work of L lanes (16, 32 or 64) of a wave, which so works on 64 /
+// L rows at once: lane l of a row holds its experts l V .. l V + V - 1 in
+// registers, read once.  The reductions over a row are then log2(L) lane
+// exchanges that serve every row of the wave.
+//
+// The choice compares s in 64 bits: at 16384 rows of 256 experts whose s are
+// compared in f32, some rows choose another expert than the definition's.
 #include "internal.hpp"
 #include "rows_common.hpp"
 
@@ -11,239 +15,383 @@ namespace rs {
 
 namespace {
 
-constexpr int kRouteWaves = 4;                      // rows of a block
+constexpr int kRouteWaves = 4;
 
-// The largest of the lanes' 64-bit patterns, and the lowest lane that has it.
-__device__ __forceinline__ uint64_t wave_best(uint64_t k, uint32_t* lane_of) {
-    uint64_t b = k;
-#pragma unroll
-    for (int off = kWave / 2; off > 0; off >>= 1) {
-        const uint64_t o = __shfl_xor(b, off, kWave);
-        b = o > b ? o : b;
-    }
-    *lane_of = static_cast<uint32_t>(__builtin_ctzll(ballot(k == b)));
-    return b;
+// s of experts that cannot be chosen, and of masked ones (behind every other,
+// but a choice where nothing else is left).  No s is so low: scores and
+// biases are f32.
+constexpr double kExcluded = -__builtin_huge_val();
+constexpr double kMasked = -1.7976931348623157e308;
+
+// exp(x): 2^n exp(r) with n = x / ln 2 to nearest and |r| <= ln 2 / 2, exp(r) by
+// Taylor's series to r^13 / 13! (the next term is below 2^-57).  Arguments
+// beyond +-1100 (infinities among them) give infinity and 0; NaN gives 0.
+__device__ __forceinline__ double exp64(double x) {
+    x = fmin(fmax(x, -1100.0), 1100.0);
+    const double n = rint(x * 1.4426950408889634074);
+    double r = fma(n, -0.69314718055994530942, x);
+    r = fma(n, -2.3190468138462995584e-17, r);   // ln 2 less its double
+    double e = 1.0 / 6227020800.0;
+    e = fma(e, r, 1.0 / 479001600.0);
+    e = fma(e, r, 1.0 / 39916800.0);
+    e = fma(e, r, 1.0 / 3628800.0);
+    e = fma(e, r, 1.0 / 362880.0);
+    e = fma(e, r, 1.0 / 40320.0);
+    e = fma(e, r, 1.0 / 5040.0);
+    e = fma(e, r, 1.0 / 720.0);
+    e = fma(e, r, 1.0 / 120.0);
+    e = fma(e, r, 1.0 / 24.0);
+    e = fma(e, r, 1.0 / 6.0);
+    e = fma(e, r, 0.5);
+    e = fma(e, r, 1.0);
+    e = fma(e, r, 1.0);
+    return ldexp(e, static_cast<int>(n));
 }
 
-template <int ELEM, int V, bool SIGMOID>
-__global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) {
+// What a row's probabilities are computed with: sigmoid, or softmax with the
+// largest score m and the sum of exp relative to it (1 where only ratios are
+// wanted), and whether the row has a NaN (softmax: all its p are NaN).
+struct Prob {
+    bool sigmoid, nan;
+    double m, sum;
+
+    __device__ __forceinline__ double operator()(float x) const {
+        if (sigmoid) return x != x ? __builtin_nan("") : 1.0 / (1.0 + exp64(-static_cast<double>(x)));
+        if (nan || m == __builtin_huge_val()) return __builtin_nan("");
+        if (m == -__builtin_huge_val()) return 0.0;
+        return exp64(static_cast<double>(x) - m) / sum;
+    }
+};
+
+// A row's candidates in LDS, at most L.
+struct Candidate {
+    double s;
+    float x;
+    uint32_t e;
+};
+
+// The kept groups of the wave's rows, as masks (equal in a row's lanes).  score
+// [experts] and best [groups] are the row's own LDS; lane l has written the
+// scores of its experts.  P = L / (groups, rounded up to a power of two) lanes
+// share a group; the best two of each meet by lane exchanges.
+template <int L>
+__device__ __forceinline__ uint64_t kept_groups(const RouteArgs& a, const double* score, double* best_of) {
+    const uint32_t lane = lane_id();
+    const uint32_t sub = lane & (L - 1);
+    const uint32_t size = a.experts / a.groups;
+    uint32_t p = L;   // lanes of a group
+    while (p * a.groups > L) p >>= 1;
+    const uint32_t g = sub / p;
+    double best = kExcluded, next = kExcluded;
+    if (g < a.groups) {
+        for (uint32_t i = sub & (p - 1); i < size; i += p) {
+            const double s = score[g * size + i];
+            next = fmax(next, fmin(best, s));
+            best = fmax(best, s);
+        }
+    }
+    for (uint32_t o = 1; o < p; o <<= 1) {
+        const double b = __shfl_xor(best, o, kWave), n = __shfl_xor(next, o, kWave);
+        next = fmax(fmax(next, n), fmin(best, b));
+        best = fmax(best, b);
+    }
+    if (g < a.groups && (sub & (p - 1)) == 0)
+        best_of[g] = a.group_best == 2 && next > kMasked ? best + next : best;
+    wave_fence();
+    bool kept = false;
+    if (sub < a.groups) {   // groups before this one
+        const double mine = best_of[sub];
+        uint32_t before = 0;
+        for (uint32_t i = 0; i < a.groups; ++i) {
+            const double o = best_of[i];
+            before += o > mine || (o == mine && i < sub);
+        }
+        kept = before < a.top_groups;
+    }
+    const uint64_t all = ballot(kept) >> (lane - sub);
+    return L == kWave ? all : all & ((1ull << (L & 63)) - 1);
+}
+
+template <int ELEM, int L, int V>
+__global__ __launch_bounds__(kRouteWaves* kWave, 4) void route_kernel(RouteArgs a) {
     using T = typename Elem<ELEM>::T;
-    __shared__ double s_score[kRouteWaves][RS_MAX_EXPERTS];
-    __shared__ float s_x[kRouteWaves][RS_MAX_EXPERTS];
-    const uint32_t wave = threadIdx.x / kWave;
+    constexpr uint32_t R = kWave / L;   // rows of a wave
+    __shared__ Candidate s_list[kRouteWaves * R][L];
+    extern __shared__ double s_groups[];   // with groups: a row's scores, then its groups' scores
     const uint32_t lane = threadIdx.x & (kWave - 1);
-    const uint32_t row = block_id() * kRouteWaves + wave;
-    if (row >= a.rows) return;
+    const uint32_t sub = lane & (L - 1);
+    const uint32_t slot = threadIdx.x / L;   // the row's place in the block
+    const uint32_t row_or_more = block_id() * (kRouteWaves * R) + slot;
+    const bool active = row_or_more < a.rows;
+    const uint32_t row = active ? row_or_more : a.rows - 1;   // every lane takes part in the exchanges
     const T* in = static_cast<const T*>(a.scores) + row * a.row_stride;
+    const uint32_t first = sub * V;
+    const uint32_t real = first < a.experts ? a.experts - first : 0u;   // of the lane's V, those that exist
 
     float x[V];
-    float m = -__builtin_huge_valf();
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const uint32_t e = lane * V + j;
-        x[j] = e < a.experts ? static_cast<float>(in[e]) : -__builtin_huge_valf();
-        m = fmaxf(m, x[j]);
-    }
-    m = lanes_max(m);
-    const bool empty = m == -__builtin_huge_valf();   // of softmax rows with NaN too: the sum is NaN then
-    double total = 1.0;
-    if (!SIGMOID) {
-        double mine = 0.0;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (lane * V + j < a.experts)
-                mine += (empty && x[j] == x[j]) ? 0.0 : exp(static_cast<double>(x[j]) - static_cast<double>(m));
-        total = lanes_sum(mine);
-    }
-    auto prob = [&](float v) -> double {
-        if (SIGMOID) return 1.0 / (1.0 + exp(-static_cast<double>(v)));
-        if (empty && total == 0.0) return 0.0;
-        return exp(static_cast<double>(v) - static_cast<double>(m)) / total;
-    };
+    load_some<V>(in + (real ? first : 0u), real, -__builtin_huge_valf(), x);
 
-    uint64_t key[V];
-    const bool by_p = a.bias != nullptr;
-    const bool group_p = a.groups > 1 && (by_p || a.group_best == 2);
+    Prob prob{a.sigmoid, false, 0.0, 1.0};
+    if (!a.sigmoid) {
+        float m = x[0];
+        bool nan = x[0] != x[0];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const uint32_t e = lane * V + j;
-        key[j] = 0;
-        if (e < a.experts) {
-            const bool masked = !(x[j] > -__builtin_huge_valf());
-            double s = x[j];
-            if (by_p) s = masked ? -__builtin_huge_val() : prob(x[j]) + static_cast<double>(a.bias[e]);
-            key[j] = order64_masked(s);
-            if (a.groups > 1) s_score[wave][e] = group_p && !by_p ? (masked ? -__builtin_huge_val() : prob(x[j])) : s;
-            s_x[wave][e] = x[j];
+        for (int j = 1; j < V; ++j) {
+            m = fmaxf(m, x[j]);
+            nan |= x[j] != x[j];
         }
+        m = lanes_max<L>(m);
+        const uint64_t nans = ballot(nan) >> (lane - sub);
+        prob.m = m != m ? -__builtin_huge_val() : static_cast<double>(m);
+        prob.nan = (L == kWave ? nans : nans & ((1ull << (L & 63)) - 1)) != 0;
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-
-    if (a.groups > 1) {
-        const uint32_t size = a.experts / a.groups;
-        uint64_t gkey = 0;
-        if (lane < a.groups) {
-            double best = -__builtin_huge_val(), next = -__builtin_huge_val();
-            for (uint32_t i = 0; i < size; ++i) {
-                const double s = s_score[wave][lane * size + i];
-                if (s > best) {
-                    next = best;
-                    best = s;
-                } else if (s > next) {
-                    next = s;
-                }
-            }
-            if (a.group_best == 2 && next > -__builtin_huge_val()) best += next;
-            gkey = order64_masked(best);
-        }
-        uint64_t kept = 0;
-        for (uint32_t r = 0; r < a.top_groups; ++r) {
-            uint32_t g;
-            wave_best(gkey, &g);
-            kept |= 1ull << g;
-            if (lane == g) gkey = 0;
-        }
+    // p of every expert, where the choice or the weights' sum needs them.  A pair of
+    // exponentials at a time: all at once would take every register.
+    const bool by_p = a.bias != nullptr || (a.groups > 1 && a.group_best == 2);
+    double s[V];
+    if (a.sigmoid && by_p) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint32_t e = lane * V + j;
-            if (e < a.experts && !((kept >> (e / size)) & 1ull)) key[j] = 0;
+            s[j] = 1.0 / (1.0 + exp64(-static_cast<double>(x[j])));
+            if (j & 1) __builtin_amdgcn_sched_barrier(0);
+        }
+    } else if (!a.sigmoid && (by_p || !a.renormalize)) {   // otherwise the sum cancels
+        double sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            s[j] = exp64(static_cast<double>(x[j]) - prob.m);   // behind the last expert 0
+            sum += s[j];
+            if (j & 1) __builtin_amdgcn_sched_barrier(0);
+        }
+        prob.sum = lanes_sum<L>(sum);
+        const double inv = prob.nan || prob.m == __builtin_huge_val() ? __builtin_nan("") : 1.0 / prob.sum;
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] *= inv;
+    }
+
+    // s, and with groups the scores that the groups go by
+    float bias[V];
+    if (a.bias != nullptr) load_some<V>(a.bias + (real ? first : 0u), real, 0.0f, bias);
+    double* score = s_groups + slot * (a.experts + a.groups);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        if (a.bias != nullptr) s[j] += static_cast<double>(bias[j]);
+        const double by = by_p ? s[j] : static_cast<double>(x[j]);
+        const bool masked = !(x[j] > -__builtin_huge_valf());
+        const double g = masked || !(by > -__builtin_huge_val()) ? kMasked : by;
+        s[j] = a.bias != nullptr ? g : masked ? kMasked : static_cast<double>(x[j]);
+        if (static_cast<uint32_t>(j) >= real) s[j] = kExcluded;
+        else if (a.groups > 1) score[first + j] = g;
+    }
+
+    if (a.groups > 1) {
+        wave_fence();
+        const uint64_t kept = kept_groups<L>(a, score, score + a.experts);
+        const uint32_t size = a.experts / a.groups;
+        uint32_t g = first / size, in_group = first - g * size;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (!((kept >> (g & 63)) & 1ull)) s[j] = kExcluded;
+            if (++in_group == size) {
+                in_group = 0;
+                ++g;
+            }
         }
     }
 
-    uint32_t chosen = 0;   // lane r holds the r-th choice
-    for (uint32_t r = 0; r < a.top_k; ++r) {
-        uint64_t mine = 0;
-        uint32_t slot = 0;
+    // A threshold that at least top_k of the row reach: the top_k-th of its lanes'
+    // best, in f32 and two steps lower (below what it was rounded from, -0.0 being
+    // the step below +0.0).
+    double best = s[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) best = fmax(best, s[j]);
+    const uint32_t sorted = lanes_sort_desc<L>(order32(static_cast<float>(best)));
+    const uint32_t kth = __shfl(sorted, static_cast<int>(lane - sub + (a.top_k <= L ? a.top_k - 1 : L - 1)), kWave);
+    const bool open = kth <= order32(-__builtin_huge_valf()) + 2u || a.top_k > L;   // masked ones may be chosen
+    const double tau = open ? kMasked : static_cast<double>(value_of_order32(kth - 2u));
+
+    // What reaches it is collected; where that is more than the list holds, the
+    // choices are taken one after the other instead.
+    uint32_t count = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) count += s[j] >= tau;
+    const uint32_t incl = wave_inclusive_sum(count);
+    const uint32_t last = __shfl(incl, static_cast<int>(lane | (L - 1)), kWave);
+    const uint32_t previous = __shfl(incl, static_cast<int>((lane - sub - 1) & (kWave - 1)), kWave);   // by every lane
+    const uint32_t before = lane >= L ? previous : 0u;
+    const uint32_t found = last - before;
+    const bool fits = found <= L;
+    if (fits) {
+        uint32_t at = incl - count - before;
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if (key[j] > mine) {
-                mine = key[j];
-                slot = j;
-            }
-        uint32_t from;
-        wave_best(mine, &from);
-        const uint32_t e = __shfl(lane * V + slot, from, kWave);
-        if (lane == from) {
+            if (s[j] >= tau) s_list[slot][at++] = Candidate{s[j], x[j], first + j};
+    }
+    wave_fence();
+    // Lane i has candidate i; its place is the number of candidates before it.
+    bool chosen = fits && sub < found;
+    Candidate c = s_list[slot][chosen ? sub : 0u];
+    uint32_t place = 0;
+    for (uint32_t i = 0; ballot(fits && i < found) != 0; ++i) {
+        const Candidate o = s_list[slot][i];
+        place += i < found && (o.s > c.s || (o.s == c.s && o.e < c.e));
+    }
+    chosen = chosen && place < a.top_k;
+    if (ballot(!fits) != 0) {
+        for (uint32_t r = 0; r < a.top_k; ++r) {
+            double mine = s[0], mx = kExcluded;
+            float v = x[0];
+            uint32_t at = 0;
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (j == static_cast<int>(slot)) key[j] = 0;
+            for (int j = 1; j < V; ++j)
+                if (s[j] > mine) {
+                    mine = s[j];
+                    v = x[j];
+                    at = j;
+                }
+            mx = lanes_max<L>(mine);
+            const uint64_t with = ballot(mine == mx) >> (lane - sub);
+            const uint32_t from = static_cast<uint32_t>(__builtin_ctzll(with));   // the lowest lane of the row
+            const uint32_t e = __shfl(first + at, static_cast<int>(lane - sub + from), kWave);
+            const float xe = __shfl(v, static_cast<int>(lane - sub + from), kWave);
+            if (sub == from) {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (j == static_cast<int>(at)) s[j] = kExcluded;
+            }
+            if (!fits && sub == r) {
+                c = Candidate{0.0, xe, e};
+                place = r;
+                chosen = true;
+            }
         }
-        if (lane == r) chosen = e;
     }
 
-    const bool mine = lane < a.top_k;
-    const double p = mine ? prob(s_x[wave][chosen]) : 0.0;
+    const double p = chosen ? prob(c.x) : 0.0;
     double w = static_cast<double>(a.scale) * p;
     if (a.renormalize) {
-        const double sum = lanes_sum(p);
+        const double sum = lanes_sum<L>(p);
         w = sum == 0.0 ? 0.0 : w / sum;
     }
-    if (mine) {
-        const uint64_t at = static_cast<uint64_t>(row) * a.top_k + lane;
-        a.ids[at] = chosen;
-        a.weights[at] = static_cast<float>(w);
+    if (chosen && active) {
+        const uint64_t to = static_cast<uint64_t>(row) * a.top_k + place;
+        a.ids[to] = c.e;
+        a.weights[to] = static_cast<float>(w);
     }
 }
 
-template <int ELEM, int V, bool SIGMOID>
+// The gradient: every lane has one choice, whose term (summed over the choices
+// of its expert) it puts into the row's LDS copy, which starts as zeros; the
+// lane then writes its V experts, with the softmax's term that reaches them
+// all where the weights are not renormalised.
+template <int ELEM, int L, int V>
 __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(RouteGradArgs a) {
     using T = typename Elem<ELEM>::T;
-    const uint32_t wave = threadIdx.x / kWave;
+    constexpr uint32_t R = kWave / L;
+    __shared__ float s_dx[kRouteWaves * R][L * V];
     const uint32_t lane = threadIdx.x & (kWave - 1);
-    const uint32_t row = block_id() * kRouteWaves + wave;
-    if (row >= a.rows) return;
+    const uint32_t sub = lane & (L - 1);
+    const uint32_t slot = threadIdx.x / L;
+    const uint32_t row_or_more = block_id() * (kRouteWaves * R) + slot;
+    const bool active = row_or_more < a.rows;
+    const uint32_t row = active ? row_or_more : a.rows - 1;
     const T* in = static_cast<const T*>(a.scores) + row * a.row_stride;
-    T* out = static_cast<T*>(a.dscores) + row * a.dscores_stride;
-
-    const bool mine = lane < a.top_k;
-    const uint64_t at = static_cast<uint64_t>(row) * a.top_k + lane;
-    const uint32_t id = mine ? a.ids[at] : 0xFFFFFFFFu;
-    const float w = mine ? a.weights[at] : 0.0f;
-    const float dw = mine ? a.dweights[at] : 0.0f;
-    const float d = lanes_sum(dw * w);
-    float part = w * (a.renormalize ? dw - d / a.scale : dw);   // the choice's own term
+    const uint32_t first = sub * V;
+    const uint32_t real = first < a.experts ? a.experts - first : 0u;
 
     float dx[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) dx[j] = 0.0f;
-    if (SIGMOID) {
-        if (id < a.experts) part *= 1.0f / (1.0f + expf(static_cast<float>(in[id])));
-    } else if (!a.renormalize) {
+    for (int j = 0; j < V; ++j) s_dx[slot][first + j] = 0.0f;
+    const bool mine = sub < a.top_k;
+    const uint64_t at = static_cast<uint64_t>(row) * a.top_k + (mine ? sub : 0u);
+    const uint32_t id = mine ? a.ids[at] : 0xFFFFFFFFu;
+    const float w = a.weights[at];
+    const float dw = a.dweights[at];
+    const float d = lanes_sum<L>(mine ? dw * w : 0.0f);
+    float part = w * (a.renormalize ? dw - d / a.scale : dw);
+    if (a.sigmoid && id < a.experts) part *= 1.0f / (1.0f + expf(static_cast<float>(in[id])));
+    float term = 0.0f;
+    for (uint32_t r = 0; r < a.top_k; ++r) {
+        const uint32_t e = __shfl(id, static_cast<int>(lane - sub + r), kWave);
+        const float g = __shfl(part, static_cast<int>(lane - sub + r), kWave);
+        term += e == id ? g : 0.0f;
+    }
+    wave_fence();
+    if (id < a.experts) s_dx[slot][id] = term;   // the same from every lane of the expert
+    wave_fence();
+    if (!a.sigmoid && !a.renormalize) {
         float x[V];
-        float m = -__builtin_huge_valf();
+        load_some<V>(in + (real ? first : 0u), real, -__builtin_huge_valf(), x);
+        float m = x[0];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const uint32_t e = lane * V + j;
-            x[j] = e < a.experts ? static_cast<float>(in[e]) : -__builtin_huge_valf();
-            m = fmaxf(m, x[j]);
-        }
-        m = lanes_max(m);
+        for (int j = 1; j < V; ++j) m = fmaxf(m, x[j]);
+        m = lanes_max<L>(m);
+        const bool empty = m == -__builtin_huge_valf();   // p = 0 (and d = 0, or NaN where the weights are)
         float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (lane * V + j < a.experts) {
-                x[j] = expf(x[j] - m);
-                sum += x[j];
-            }
-        sum = lanes_sum(sum);
-        const bool empty = m == -__builtin_huge_valf();   // p = 0 (and d = 0, or NaN where the weights are)
+        for (int j = 0; j < V; ++j) {
+            dx[j] = expf(x[j] - m);
+            sum += static_cast<uint32_t>(j) < real ? dx[j] : 0.0f;
+        }
+        sum = lanes_sum<L>(sum);
 #pragma unroll
-        for (int j = 0; j < V; ++j) dx[j] = -(empty ? 0.0f : x[j] / sum) * d;
-    }
-    for (uint32_t r = 0; r < a.top_k; ++r) {
-        const uint32_t e = __shfl(id, r, kWave);
-        const float g = __shfl(part, r, kWave);
+        for (int j = 0; j < V; ++j) dx[j] = fmaf(-(empty ? 0.0f : dx[j] / sum), d, s_dx[slot][first + j]);
+    } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (e == lane * V + j) dx[j] += g;
+        for (int j = 0; j < V; ++j) dx[j] = s_dx[slot][first + j];
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const uint32_t e = lane * V + j;
-        if (e < a.experts) out[e] = static_cast<T>(dx[j]);
-    }
+    if (active && real) store_some<V>(static_cast<T*>(a.dscores) + row * a.dscores_stride + first, real, dx);
 }
 
-template <int ELEM, int V>
+template <int ELEM, int L, int V>
 hipError_t route_shape(const RouteArgs& a, hipStream_t stream) {
-    const uint32_t blocks = (a.rows + kRouteWaves - 1) / kRouteWaves;
+    constexpr uint32_t rows = kRouteWaves * kWave / L;
+    const size_t lds = a.groups > 1 ? rows * (a.experts + a.groups) * sizeof(double) : 0;
     timing_before(stream, RS_KERNEL_ROUTE);
-    if (a.sigmoid)
-        route_kernel<ELEM, V, true><<<many_blocks(blocks), kRouteWaves * kWave, 0, stream>>>(a);
-    else
-        route_kernel<ELEM, V, false><<<many_blocks(blocks), kRouteWaves * kWave, 0, stream>>>(a);
+    route_kernel<ELEM, L, V><<<many_blocks((a.rows + rows - 1) / rows), kRouteWaves * kWave, lds, stream>>>(a);
     const hipError_t e = hipGetLastError();
     timing_after(stream);
     return e;
 }
 
-template <int ELEM, int V>
+template <int ELEM, int L, int V>
 hipError_t grad_shape(const RouteGradArgs& a, hipStream_t stream) {
-    const uint32_t blocks = (a.rows + kRouteWaves - 1) / kRouteWaves;
+    constexpr uint32_t rows = kRouteWaves * kWave / L;
     timing_before(stream, RS_KERNEL_ROUTE_GRAD);
-    if (a.sigmoid)
-        route_grad_kernel<ELEM, V, true><<<many_blocks(blocks), kRouteWaves * kWave, 0, stream>>>(a);
-    else
-        route_grad_kernel<ELEM, V, false><<<many_blocks(blocks), kRouteWaves * kWave, 0, stream>>>(a);
+    route_grad_kernel<ELEM, L, V><<<many_blocks((a.rows + rows - 1) / rows), kRouteWaves * kWave, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     timing_after(stream);
     return e;
 }
 
+// Lanes of a row: as few as hold the experts in at most 16 registers each, and
+// for the choice twice top_k (the list of candidates holds one for each lane,
+// and among L lanes' bests about 1.3 top_k of the row reach the top_k-th) and
+// one for each group.
 template <int ELEM>
 hipError_t route_elem(const RouteArgs& a, hipStream_t stream) {
-    if (a.experts <= 64) return route_shape<ELEM, 1>(a, stream);
-    if (a.experts <= 256) return route_shape<ELEM, 4>(a, stream);
-    return route_shape<ELEM, 16>(a, stream);
+    if (a.experts <= 256 && a.top_k <= 8 && a.groups <= 16) {
+        if (a.experts <= 64) return route_shape<ELEM, 16, 4>(a, stream);
+        if (a.experts <= 128) return route_shape<ELEM, 16, 8>(a, stream);
+        return route_shape<ELEM, 16, 16>(a, stream);
+    }
+    if (a.experts <= 512 && a.top_k <= 16 && a.groups <= 32) {
+        if (a.experts <= 128) return route_shape<ELEM, 32, 4>(a, stream);
+        return route_shape<ELEM, 32, 16>(a, stream);
+    }
+    if (a.experts <= 256) return route_shape<ELEM, 64, 4>(a, stream);
+    return route_shape<ELEM, 64, 16>(a, stream);
 }
 
 template <int ELEM>
 hipError_t grad_elem(const RouteGradArgs& a, hipStream_t stream) {
-    if (a.experts <= 64) return grad_shape<ELEM, 1>(a, stream);
-    if (a.experts <= 256) return grad_shape<ELEM, 4>(a, stream);
-    return grad_shape<ELEM, 16>(a, stream);
+    if (a.experts <= 256 && a.top_k <= 16) {
+        if (a.experts <= 64) return grad_shape<ELEM, 16, 4>(a, stream);
+        if (a.experts <= 128) return grad_shape<ELEM, 16, 8>(a, stream);
+        return grad_shape<ELEM, 16, 16>(a, stream);
+    }
+    if (a.experts <= 512 && a.top_k <= 32) return grad_shape<ELEM, 32, 16>(a, stream);
+    return grad_shape<ELEM, 64, 16>(a, stream);
 }
 
 }  // namespace

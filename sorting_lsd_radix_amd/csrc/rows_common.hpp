@@ -42,12 +42,44 @@ __device__ __forceinline__ uint32_t order32(float x) {
     return (x == x) ? u ^ (sign | 0x80000000u) : 1u;
 }
 
-// The same in 64 bits, for scores that are compared in 64 bits; -inf and NaN
-// (masked) share one pattern, 1.
-__device__ __forceinline__ uint64_t order64_masked(double x) {
-    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
-    const uint64_t sign = static_cast<uint64_t>(static_cast<int64_t>(u) >> 63);
-    return (x > -__builtin_huge_val()) ? u ^ (sign | 0x8000000000000000ull) : 1ull;
+// The value whose order pattern is `o` (a NaN for NaN's).
+__device__ __forceinline__ float value_of_order32(uint32_t o) {
+    return o == 1u ? __builtin_nanf("") : __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o);
+}
+
+// The wave's own LDS writes are visible to its lanes' reads behind this.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// V consecutive elements at `at`, of which the first `n` exist; `fill` for the others.
+template <int V, class T>
+__device__ __forceinline__ void load_some(const T* at, uint32_t n, float fill, float (&x)[V]) {
+    if (n >= V) {
+        struct { T v[V]; } r;
+        __builtin_memcpy(&r, at, sizeof(r));   // no alignment beyond the element's
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = static_cast<float>(r.v[j]);
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < V; ++j) x[j] = j < n ? static_cast<float>(at[j]) : fill;
+    }
+}
+
+template <int V, class T>
+__device__ __forceinline__ void store_some(T* at, uint32_t n, const float (&x)[V]) {
+    struct { T v[V]; } r;
+#pragma unroll
+    for (int j = 0; j < V; ++j) r.v[j] = static_cast<T>(x[j]);
+    if (n >= V) {
+        __builtin_memcpy(at, &r, sizeof(r));
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < V; ++j)
+            if (j < n) at[j] = r.v[j];
+    }
 }
 
 // The value of lane ^ M, of any type of whole words.
@@ -83,6 +115,11 @@ __device__ __forceinline__ float lanes_max(float x) {
     return lanes_reduce<N>(x, [](float a, float b) { return fmaxf(a, b); });
 }
 
+template <int N = kWave>
+__device__ __forceinline__ double lanes_max(double x) {
+    return lanes_reduce<N>(x, [](double a, double b) { return fmax(a, b); });
+}
+
 template <int N = kWave, class T>
 __device__ __forceinline__ T lanes_sum(T x) {
     return lanes_reduce<N>(x, [](T a, T b) { return a + b; });
@@ -99,12 +136,17 @@ __device__ __forceinline__ T lanes_merge_steps(T k, uint32_t lane) {
     return k;
 }
 
-// The 64 lanes' keys in decreasing order.
-template <int SIZE = 2, class T>
-__device__ __forceinline__ T wave_sort_desc(T k) {
-    k = lanes_merge_steps<SIZE, SIZE / 2>(k, lane_id());
-    if constexpr (SIZE < kWave) k = wave_sort_desc<SIZE * 2>(k);
+// The keys of every aligned group of N lanes in decreasing order.
+template <int N, int SIZE = 2, class T>
+__device__ __forceinline__ T lanes_sort_desc(T k) {
+    if constexpr (N > 1) k = lanes_merge_steps<SIZE, SIZE / 2>(k, lane_id() & (N - 1));
+    if constexpr (SIZE < N) k = lanes_sort_desc<N, SIZE * 2>(k);
     return k;
+}
+
+template <class T>
+__device__ __forceinline__ T wave_sort_desc(T k) {
+    return lanes_sort_desc<kWave>(k);
 }
 
 // The best 64 of two lists in decreasing order, in decreasing order: the
