@@ -6,8 +6,13 @@
 // registers, read once.  The reductions over a row are then log2(L) lane
 // exchanges that serve every row of the wave.
 //
-// The choice compares s in 64 bits: at 16384 rows of 256 experts whose s are
-// compared in f32, some rows choose another expert than the definition's.
+// The choice is by s in 64 bits (in f32, some of 16384 rows of 256 experts
+// choose another expert than the definition's), yet only a row's candidates
+// are computed so: s in f32, which is off by at most kOff, leaves out every
+// expert that cannot be among the first, and decides which groups are kept
+// unless two scores at the border are too near (then the row's s are all taken
+// in 64 bits).  64-bit arithmetic for every expert cost 45 us of 32768 rows of
+// 512 experts' sigmoids with a bias, against 30 without.
 #include "internal.hpp"
 #include "rows_common.hpp"
 
@@ -17,11 +22,20 @@ namespace {
 
 constexpr int kRouteWaves = 4;
 
-// s of experts that cannot be chosen, and of masked ones (behind every other,
-// but a choice where nothing else is left).  No s is so low: scores and
-// biases are f32.
+constexpr float kInf = __builtin_huge_valf();
+
+// In 64 bits, s of experts that cannot be chosen and of masked ones (behind
+// every other, but a choice where nothing else is left); no s is so low, as
+// scores and biases are f32.  In f32 these are NaN and -inf.
 constexpr double kExcluded = -__builtin_huge_val();
 constexpr double kMasked = -1.7976931348623157e308;
+
+// How far s in f32 may be off: kOff + kOffRel |s|.  p = 1 / (1 + e) has at most
+// 4 roundings' worth, 2^-22 (exp2's argument is off by 2^-24 |x log2 e|, which
+// moves p by less than p (1 - p) |x| 2^-24 < 2^-26; exp2 and the reciprocal are
+// off by 2^-23 relative, the sum by 2^-24); adding the bias 2^-24 |s|.  Twice that.
+constexpr float kOff = 0x1p-21f;
+constexpr float kOffRel = 0x1p-23f;
 
 // exp(x): 2^n exp(r) with n = x / ln 2 to nearest and |r| <= ln 2 / 2, exp(r) by
 // Taylor's series to r^13 / 13! (the next term is below 2^-57).  Arguments
@@ -70,50 +84,67 @@ struct Candidate {
     uint32_t e;
 };
 
-// The kept groups of the wave's rows, as masks (equal in a row's lanes).  score
-// [experts] and best [groups] are the row's own LDS; lane l has written the
-// scores of its experts.  P = L / (groups, rounded up to a power of two) lanes
-// share a group; the best two of each meet by lane exchanges.
-template <int L>
-__device__ __forceinline__ uint64_t kept_groups(const RouteArgs& a, const double* score, double* best_of) {
+// The kept groups of the wave's rows, as masks (equal in a row's lanes), from
+// the scores (f32 or 64 bits) in the row's LDS: score [experts], and room for
+// best_of [groups].  Lane l has written its experts' scores.  P = L / (groups,
+// rounded up to a power of two) lanes share a group; the best two of each meet
+// by lane exchanges.  off, rel: how far two groups' scores may be off together;
+// `unclear` tells whether that leaves the row's choice open.
+template <int L, class S>
+__device__ __forceinline__ uint64_t kept_groups(const RouteArgs& a, const S* score, S* best_of, S masked, S off,
+                                                S rel, bool* unclear) {
     const uint32_t lane = lane_id();
     const uint32_t sub = lane & (L - 1);
     const uint32_t size = a.experts / a.groups;
     uint32_t p = L;   // lanes of a group
     while (p * a.groups > L) p >>= 1;
     const uint32_t g = sub / p;
-    double best = kExcluded, next = kExcluded;
+    S best = masked, next = masked;
     if (g < a.groups) {
+#pragma unroll 4
         for (uint32_t i = sub & (p - 1); i < size; i += p) {
-            const double s = score[g * size + i];
+            const S s = score[g * size + i];
             next = fmax(next, fmin(best, s));
             best = fmax(best, s);
         }
     }
     for (uint32_t o = 1; o < p; o <<= 1) {
-        const double b = __shfl_xor(best, o, kWave), n = __shfl_xor(next, o, kWave);
+        const S b = __shfl_xor(best, o, kWave), n = __shfl_xor(next, o, kWave);
         next = fmax(fmax(next, n), fmin(best, b));
         best = fmax(best, b);
     }
-    if (g < a.groups && (sub & (p - 1)) == 0)
-        best_of[g] = a.group_best == 2 && next > kMasked ? best + next : best;
+    if (g < a.groups && (sub & (p - 1)) == 0) {
+        S sum = a.group_best == 2 && next > masked ? best + next : best;
+        // a sum below f32's range is not a masked group's
+        if (sizeof(S) == 4 && best > masked) sum = fmax(sum, S(-3.402823466e38f));
+        best_of[g] = sum;
+    }
     wave_fence();
-    bool kept = false;
-    if (sub < a.groups) {   // groups before this one
-        const double mine = best_of[sub];
-        uint32_t before = 0;
+    bool kept = false, open = false;
+    if (sub < a.groups) {   // groups before this one, and groups that may be
+        const S mine = best_of[sub];
+        uint32_t before = 0, near = 0;
+#pragma unroll 4
         for (uint32_t i = 0; i < a.groups; ++i) {
-            const double o = best_of[i];
-            before += o > mine || (o == mine && i < sub);
+            const S o = best_of[i];
+            const bool close = i != sub && o != mine && o > masked && mine > masked &&
+                               fabs(o - mine) <= off + rel * (fabs(o) + fabs(mine));
+            // equal scores are a tie if they are exact, or if nothing is left in both
+            const bool tie = i != sub && o == mine && (off == S(0) || mine == masked);
+            near += close || (i != sub && o == mine && !tie);
+            before += (o > mine && !close) || (tie && i < sub);
         }
         kept = before < a.top_groups;
+        open = kept && before + near >= a.top_groups;
     }
-    const uint64_t all = ballot(kept) >> (lane - sub);
-    return L == kWave ? all : all & ((1ull << (L & 63)) - 1);
+    const uint32_t shift = lane - sub;
+    const uint64_t mask = L == kWave ? ~0ull : (1ull << (L & 63)) - 1;
+    *unclear = ((ballot(open) >> shift) & mask) != 0;
+    return (ballot(kept) >> shift) & mask;
 }
 
 template <int ELEM, int L, int V>
-__global__ __launch_bounds__(kRouteWaves* kWave, 4) void route_kernel(RouteArgs a) {
+__global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) {
     using T = typename Elem<ELEM>::T;
     constexpr uint32_t R = kWave / L;   // rows of a wave
     __shared__ Candidate s_list[kRouteWaves * R][L];
@@ -127,11 +158,16 @@ __global__ __launch_bounds__(kRouteWaves* kWave, 4) void route_kernel(RouteArgs 
     const T* in = static_cast<const T*>(a.scores) + row * a.row_stride;
     const uint32_t first = sub * V;
     const uint32_t real = first < a.experts ? a.experts - first : 0u;   // of the lane's V, those that exist
+    const bool biased = a.bias != nullptr;
+    const bool by_p = biased || (a.groups > 1 && a.group_best == 2);   // something goes by p, not by the scores
 
-    float x[V];
-    load_some<V>(in + (real ? first : 0u), real, -__builtin_huge_valf(), x);
+    float x[V], bias[V];
+    load_some<V>(in + (real ? first : 0u), real, -kInf, x);
+    if (biased) load_some<V>(a.bias + (real ? first : 0u), real, 0.0f, bias);
 
+    // p in f32, in key[]; the softmax's sum in 64 bits
     Prob prob{a.sigmoid, false, 0.0, 1.0};
+    float key[V];
     if (!a.sigmoid) {
         float m = x[0];
         bool nan = x[0] != x[0];
@@ -144,54 +180,70 @@ __global__ __launch_bounds__(kRouteWaves* kWave, 4) void route_kernel(RouteArgs 
         const uint64_t nans = ballot(nan) >> (lane - sub);
         prob.m = m != m ? -__builtin_huge_val() : static_cast<double>(m);
         prob.nan = (L == kWave ? nans : nans & ((1ull << (L & 63)) - 1)) != 0;
-    }
-    // p of every expert, where the choice or the weights' sum needs them.  A pair of
-    // exponentials at a time: all at once would take every register.
-    const bool by_p = a.bias != nullptr || (a.groups > 1 && a.group_best == 2);
-    double s[V];
-    if (a.sigmoid && by_p) {
+        if (by_p || !a.renormalize) {   // otherwise the sum cancels
+            double sum = 0.0;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            s[j] = 1.0 / (1.0 + exp64(-static_cast<double>(x[j])));
-            if (j & 1) __builtin_amdgcn_sched_barrier(0);
+            for (int j = 0; j < V; ++j) {
+                const double e = exp64(static_cast<double>(x[j]) - prob.m);   // behind the last expert 0
+                key[j] = static_cast<float>(e);
+                sum += e;
+                if (j & 1) __builtin_amdgcn_sched_barrier(0);   // all at once would take every register
+            }
+            prob.sum = lanes_sum<L>(sum);
+            const float inv = prob.nan || m == kInf ? __builtin_nanf("") : static_cast<float>(1.0 / prob.sum);
+#pragma unroll
+            for (int j = 0; j < V; ++j) key[j] *= inv;
         }
-    } else if (!a.sigmoid && (by_p || !a.renormalize)) {   // otherwise the sum cancels
-        double sum = 0.0;
+    } else if (by_p) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            s[j] = exp64(static_cast<double>(x[j]) - prob.m);   // behind the last expert 0
-            sum += s[j];
-            if (j & 1) __builtin_amdgcn_sched_barrier(0);
-        }
-        prob.sum = lanes_sum<L>(sum);
-        const double inv = prob.nan || prob.m == __builtin_huge_val() ? __builtin_nan("") : 1.0 / prob.sum;
-#pragma unroll
-        for (int j = 0; j < V; ++j) s[j] *= inv;
+        for (int j = 0; j < V; ++j)
+            key[j] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[j] * -1.44269504088896341f));
     }
 
-    // s, and with groups the scores that the groups go by
-    float bias[V];
-    if (a.bias != nullptr) load_some<V>(a.bias + (real ? first : 0u), real, 0.0f, bias);
-    double* score = s_groups + slot * (a.experts + a.groups);
+    // What the groups go by, and what the experts go by
+    float* score = reinterpret_cast<float*>(s_groups + slot * (a.experts + a.groups));
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        if (a.bias != nullptr) s[j] += static_cast<double>(bias[j]);
-        const double by = by_p ? s[j] : static_cast<double>(x[j]);
-        const bool masked = !(x[j] > -__builtin_huge_valf());
-        const double g = masked || !(by > -__builtin_huge_val()) ? kMasked : by;
-        s[j] = a.bias != nullptr ? g : masked ? kMasked : static_cast<double>(x[j]);
-        if (static_cast<uint32_t>(j) >= real) s[j] = kExcluded;
-        else if (a.groups > 1) score[first + j] = g;
+        if (biased) key[j] += bias[j];
+        const float by = by_p ? key[j] : x[j];
+        const bool masked = !(x[j] > -kInf);
+        const float g = masked || !(by > -kInf) ? -kInf : by;
+        key[j] = static_cast<uint32_t>(j) >= real ? __builtin_nanf("") : biased ? g : masked ? -kInf : x[j];
+        if (a.groups > 1 && static_cast<uint32_t>(j) < real) score[first + j] = g;
     }
+    // The same s in 64 bits
+    auto exact = [&](float v, uint32_t e, bool masked) {
+        if (masked) return kMasked;
+        return biased ? prob(v) + static_cast<double>(a.bias[e]) : static_cast<double>(v);
+    };
 
     if (a.groups > 1) {
         wave_fence();
-        const uint64_t kept = kept_groups<L>(a, score, score + a.experts);
+        bool unclear;
+        uint64_t kept = kept_groups<L, float>(a, score, score + a.experts, -kInf, by_p ? 4 * kOff : 0.0f,
+                                              by_p ? 2 * kOffRel : 0.0f, &unclear);
+        if (ballot(unclear) != 0) {
+            double* wide = s_groups + slot * (a.experts + a.groups);
+            wave_fence();
+#pragma unroll 1
+            for (uint32_t j = 0; j < V; ++j) {
+                const uint32_t e = first + j;
+                if (j < real) {
+                    const float v = static_cast<float>(in[e]);
+                    const double p = by_p ? prob(v) + (biased ? static_cast<double>(a.bias[e]) : 0.0) : v;
+                    wide[e] = v > -kInf && p > -__builtin_huge_val() ? p : kMasked;
+                }
+            }
+            wave_fence();
+            bool none;
+            const uint64_t sure = kept_groups<L, double>(a, wide, wide + a.experts, kMasked, 0.0, 0.0, &none);
+            kept = unclear ? sure : kept;
+        }
         const uint32_t size = a.experts / a.groups;
         uint32_t g = first / size, in_group = first - g * size;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            if (!((kept >> (g & 63)) & 1ull)) s[j] = kExcluded;
+            if (!((kept >> (g & 63)) & 1ull)) key[j] = __builtin_nanf("");
             if (++in_group == size) {
                 in_group = 0;
                 ++g;
@@ -200,46 +252,70 @@ __global__ __launch_bounds__(kRouteWaves* kWave, 4) void route_kernel(RouteArgs 
     }
 
     // A threshold that at least top_k of the row reach: the top_k-th of its lanes'
-    // best, in f32 and two steps lower (below what it was rounded from, -0.0 being
-    // the step below +0.0).
-    double best = s[0];
+    // best.  An expert among the first top_k in 64 bits is no further below it
+    // in f32 than twice what s may be off.
+    float best = key[0];
 #pragma unroll
-    for (int j = 1; j < V; ++j) best = fmax(best, s[j]);
-    const uint32_t sorted = lanes_sort_desc<L>(order32(static_cast<float>(best)));
+    for (int j = 1; j < V; ++j) best = fmaxf(best, key[j]);
+    const uint32_t sorted = lanes_sort_desc<L>(order32(best));
     const uint32_t kth = __shfl(sorted, static_cast<int>(lane - sub + (a.top_k <= L ? a.top_k - 1 : L - 1)), kWave);
-    const bool open = kth <= order32(-__builtin_huge_valf()) + 2u || a.top_k > L;   // masked ones may be chosen
-    const double tau = open ? kMasked : static_cast<double>(value_of_order32(kth - 2u));
+    float tau = -kInf;   // fewer lanes have one that is not masked: every one is a candidate
+    if (a.top_k <= L && kth > order32(-kInf)) {
+        tau = value_of_order32(kth);
+        if (biased && tau < kInf) tau -= 2 * (kOff + kOffRel * fabsf(tau));
+    }
 
     // What reaches it is collected; where that is more than the list holds, the
     // choices are taken one after the other instead.
     uint32_t count = 0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) count += s[j] >= tau;
+    for (int j = 0; j < V; ++j) count += key[j] >= tau;
     const uint32_t incl = wave_inclusive_sum(count);
     const uint32_t last = __shfl(incl, static_cast<int>(lane | (L - 1)), kWave);
     const uint32_t previous = __shfl(incl, static_cast<int>((lane - sub - 1) & (kWave - 1)), kWave);   // by every lane
     const uint32_t before = lane >= L ? previous : 0u;
     const uint32_t found = last - before;
     const bool fits = found <= L;
+    constexpr uint32_t kMaskedBit = 1u << 31;
     if (fits) {
         uint32_t at = incl - count - before;
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if (s[j] >= tau) s_list[slot][at++] = Candidate{s[j], x[j], first + j};
+            if (key[j] >= tau) {
+                s_list[slot][at].x = x[j];
+                s_list[slot][at++].e = (first + j) | (key[j] > -kInf ? 0u : kMaskedBit);
+            }
     }
     wave_fence();
     // Lane i has candidate i; its place is the number of candidates before it.
     bool chosen = fits && sub < found;
-    Candidate c = s_list[slot][chosen ? sub : 0u];
+    Candidate c{kExcluded, -kInf, 0u};
+    if (chosen) {
+        c.x = s_list[slot][sub].x;
+        c.e = s_list[slot][sub].e;
+        const bool masked = (c.e & kMaskedBit) != 0;
+        c.e &= ~kMaskedBit;
+        c.s = exact(c.x, c.e, masked);
+        s_list[slot][sub] = c;
+    }
+    wave_fence();
     uint32_t place = 0;
-    for (uint32_t i = 0; ballot(fits && i < found) != 0; ++i) {
-        const Candidate o = s_list[slot][i];
+    const uint32_t most = lanes_max(fits ? found : 0u);
+#pragma unroll 4
+    for (uint32_t i = 0; i < most; ++i) {
+        const Candidate o = s_list[slot][i < found ? i : 0u];
         place += i < found && (o.s > c.s || (o.s == c.s && o.e < c.e));
     }
     chosen = chosen && place < a.top_k;
     if (ballot(!fits) != 0) {
+        double s[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            s[j] = key[j] != key[j] ? kExcluded : exact(x[j], first + j, !(key[j] > -kInf));
+            __builtin_amdgcn_sched_barrier(0);
+        }
         for (uint32_t r = 0; r < a.top_k; ++r) {
-            double mine = s[0], mx = kExcluded;
+            double mine = s[0];
             float v = x[0];
             uint32_t at = 0;
 #pragma unroll
@@ -249,8 +325,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave, 4) void route_kernel(RouteArgs 
                     v = x[j];
                     at = j;
                 }
-            mx = lanes_max<L>(mine);
-            const uint64_t with = ballot(mine == mx) >> (lane - sub);
+            const uint64_t with = ballot(mine == lanes_max<L>(mine)) >> (lane - sub);
             const uint32_t from = static_cast<uint32_t>(__builtin_ctzll(with));   // the lowest lane of the row
             const uint32_t e = __shfl(first + at, static_cast<int>(lane - sub + from), kWave);
             const float xe = __shfl(v, static_cast<int>(lane - sub + from), kWave);
@@ -364,33 +439,39 @@ hipError_t grad_shape(const RouteGradArgs& a, hipStream_t stream) {
     return e;
 }
 
-// Lanes of a row: as few as hold the experts in at most 16 registers each, and
-// for the choice twice top_k (the list of candidates holds one for each lane,
-// and among L lanes' bests about 1.3 top_k of the row reach the top_k-th) and
-// one for each group.
-template <int ELEM>
-hipError_t route_elem(const RouteArgs& a, hipStream_t stream) {
-    if (a.experts <= 256 && a.top_k <= 8 && a.groups <= 16) {
-        if (a.experts <= 64) return route_shape<ELEM, 16, 4>(a, stream);
-        if (a.experts <= 128) return route_shape<ELEM, 16, 8>(a, stream);
-        return route_shape<ELEM, 16, 16>(a, stream);
-    }
-    if (a.experts <= 512 && a.top_k <= 16 && a.groups <= 32) {
-        if (a.experts <= 128) return route_shape<ELEM, 32, 4>(a, stream);
-        return route_shape<ELEM, 32, 16>(a, stream);
-    }
-    if (a.experts <= 256) return route_shape<ELEM, 64, 4>(a, stream);
-    return route_shape<ELEM, 64, 16>(a, stream);
+template <int ELEM, int L>
+hipError_t route_lanes(const RouteArgs& a, hipStream_t stream) {
+    if (a.experts <= L) return route_shape<ELEM, L, 1>(a, stream);
+    if (a.experts <= 2 * L) return route_shape<ELEM, L, 2>(a, stream);
+    if (a.experts <= 4 * L) return route_shape<ELEM, L, 4>(a, stream);
+    if constexpr (L == kWave)
+        if (a.experts > 8 * L) return route_shape<ELEM, L, 16>(a, stream);
+    return route_shape<ELEM, L, 8>(a, stream);
 }
 
+// Lanes of a row: enough that every group has one, that a lane has at most 8
+// experts (of 256 and 32 lanes; 16 lanes with 16 each, fewer waves that wait
+// longer: 30 -> 22 us at 16384 rows with groups), and that there are twice
+// top_k: about 1.4 top_k of a row reach the top_k-th of the lanes' bests then,
+// and the list of candidates has a place for each lane.  Experts are spread
+// over all lanes for the same reason.
+template <int ELEM>
+hipError_t route_elem(const RouteArgs& a, hipStream_t stream) {
+    if (a.experts <= 128 && a.top_k <= 8 && a.groups <= 16) return route_lanes<ELEM, 16>(a, stream);
+    if (a.experts <= 256 && a.top_k <= 16 && a.groups <= 32) return route_lanes<ELEM, 32>(a, stream);
+    return route_lanes<ELEM, 64>(a, stream);
+}
+
+// The gradient has no list: lanes for the choices, and at most 8 experts each
+// up to 512 (32 lanes with 16 each: 30 us against 23 at 32768 rows of 512).
 template <int ELEM>
 hipError_t grad_elem(const RouteGradArgs& a, hipStream_t stream) {
-    if (a.experts <= 256 && a.top_k <= 16) {
+    if (a.experts <= 128 && a.top_k <= 16) {
         if (a.experts <= 64) return grad_shape<ELEM, 16, 4>(a, stream);
-        if (a.experts <= 128) return grad_shape<ELEM, 16, 8>(a, stream);
-        return grad_shape<ELEM, 16, 16>(a, stream);
+        return grad_shape<ELEM, 16, 8>(a, stream);
     }
-    if (a.experts <= 512 && a.top_k <= 32) return grad_shape<ELEM, 32, 16>(a, stream);
+    if (a.experts <= 256 && a.top_k <= 32) return grad_shape<ELEM, 32, 8>(a, stream);
+    if (a.experts <= 512) return grad_shape<ELEM, 64, 8>(a, stream);
     return grad_shape<ELEM, 64, 16>(a, stream);
 }
 
