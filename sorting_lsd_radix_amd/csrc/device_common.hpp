@@ -78,6 +78,13 @@ __device__ __forceinline__ uint32_t next_chunked_tile(uint32_t* sched, uint32_t 
     return t < tiles ? static_cast<uint32_t>(t) : tiles;
 }
 
+// The wave's own LDS writes are visible to its lanes' reads behind this.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The value of lane ^ M: DPP quad permutes for 1 and 2, a row rotate for 8,
 // swizzles for 4 and 16, a lane permute for 32.
 template <int M>

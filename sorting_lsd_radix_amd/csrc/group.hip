@@ -1,11 +1,19 @@
 // group.hip -- the choices of a router ordered by expert: a stable partition
 // with one side for each expert.
 //
-// Three launches: every tile counts its choices of each expert; one block
-// turns the counts into the experts' segments and every tile's offsets in
-// them; every tile puts its choices in their places.  Nothing depends on the
-// order in which blocks or atomics run: counts are sums, and the rank of a
-// choice in its tile comes from ballots over waves that take turns.
+// A block ranks a tile of choices: wave w holds the w-th run of 64 ITEMS
+// choices in registers, 64 a row, so that (wave, row, lane) is input order.  A
+// choice's rank among its expert's in the wave is the wave's count of earlier
+// rows plus the peers in lower lanes, found by a ballot for each bit of the
+// expert's number; sums over waves, tiles and experts give its place.  Nothing
+// depends on the order in which blocks or atomics run.
+//
+//  * One tile: one launch does it all.
+//  * Up to kShortSum counts (tiles * experts): two launches.  Every tile
+//    counts its choices; then every tile sums the counts of earlier and of all
+//    tiles itself, which is cheaper than a launch in between.
+//  * Above: a launch in between turns the counts of each expert into the
+//    tiles' offsets and a total.
 #include "internal.hpp"
 #include "device_common.hpp"
 
@@ -13,134 +21,255 @@ namespace rs {
 
 namespace {
 
-constexpr int kGroupBlock = 256;
-constexpr uint32_t kGroupTile = 4096;        // smallest tile
-constexpr uint32_t kGroupMaxTiles = 1024;
+constexpr int kGroupBlock = 1024;
+constexpr int kGroupWaves = kGroupBlock / kWave;
 constexpr uint32_t kNone = 0xFFFFFFFFu;
+constexpr uint32_t kShortSum = 1u << 15;
 
-uint32_t group_tile(uint64_t n) {
-    const uint64_t share = (n + kGroupMaxTiles - 1) / kGroupMaxTiles;
-    const uint64_t tile = (share + kGroupBlock - 1) / kGroupBlock * kGroupBlock;
-    return static_cast<uint32_t>(tile < kGroupTile ? kGroupTile : tile);
+// Choices of a thread.  One tile up to 16384 choices; above, tiles small
+// enough to fill the chip (256 CUs) but no smaller than 1024.
+int group_items(uint64_t n) {
+    if (n <= 1024) return 1;
+    if (n <= 4096) return 4;
+    if (n <= 16384) return 16;
+    if (n <= (uint64_t{1} << 18)) return 1;
+    return n <= (uint64_t{1} << 22) ? 4 : 16;
 }
 
 uint32_t group_tiles(uint64_t n) {
-    const uint32_t tile = group_tile(n);
+    const uint64_t tile = static_cast<uint64_t>(kGroupBlock) * group_items(n);
     return static_cast<uint32_t>((n + tile - 1) / tile);
 }
 
-__global__ __launch_bounds__(kGroupBlock) void group_count_kernel(GroupArgs a, uint32_t tile,
-                                                                  uint32_t* __restrict__ tile_counts) {
+template <int ITEMS>
+__global__ __launch_bounds__(kGroupBlock) void group_count_kernel(GroupArgs a, uint32_t* __restrict__ tile_counts) {
     __shared__ uint32_t s_count[RS_MAX_EXPERTS];
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kGroupBlock) s_count[e] = 0;
-    __syncthreads();
-    const uint32_t base = blockIdx.x * tile;
-    const uint32_t end = a.n - base < tile ? a.n : base + tile;
-    for (uint32_t i = base + threadIdx.x; i < end; i += kGroupBlock) {
-        const uint32_t e = a.ids[i];
-        if (e < a.experts) atomicAdd(&s_count[e], 1u);
-    }
-    __syncthreads();
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kGroupBlock)
-        tile_counts[static_cast<uint64_t>(blockIdx.x) * a.experts + e] = s_count[e];
-}
-
-// One block, thread e for expert e: tile_counts become the choices of earlier
-// tiles, and the totals the padded segments.
-__global__ __launch_bounds__(RS_MAX_EXPERTS) void group_scan_kernel(GroupArgs a, uint32_t tiles,
-                                                                    uint32_t* __restrict__ tile_counts) {
-    constexpr int kWaves = RS_MAX_EXPERTS / kWave;
-    __shared__ uint32_t s_wave[kWaves];
-    const uint32_t e = threadIdx.x;
-    uint32_t count = 0;
-    if (e < a.experts) {
-        for (uint32_t t = 0; t < tiles; ++t) {
-            uint32_t* c = &tile_counts[static_cast<uint64_t>(t) * a.experts + e];
-            const uint32_t own = *c;
-            *c = count;
-            count += own;
-        }
-    }
-    const uint32_t padded = (count + a.align - 1) / a.align * a.align;
-    const uint32_t incl = wave_inclusive_sum(padded);
-    if ((e & (kWave - 1)) == kWave - 1) s_wave[e / kWave] = incl;
-    __syncthreads();
-    uint32_t before = 0;
-    for (uint32_t w = 0; w < e / kWave; ++w) before += s_wave[w];
-    if (e < a.experts) {
-        a.counts[e] = count;
-        a.starts[e] = before + incl - padded;
-        if (e == a.experts - 1) a.starts[a.experts] = before + incl;
-    }
-}
-
-__global__ __launch_bounds__(kGroupBlock) void group_place_kernel(GroupArgs a, uint32_t tile,
-                                                                  const uint32_t* __restrict__ tile_counts) {
-    __shared__ uint32_t s_next[RS_MAX_EXPERTS];
     const uint32_t tid = threadIdx.x;
-    for (uint32_t e = tid; e < a.experts; e += kGroupBlock)
-        s_next[e] = a.starts[e] + (a.n ? tile_counts[static_cast<uint64_t>(blockIdx.x) * a.experts + e] : 0u);
-    __syncthreads();
-    const uint32_t wave = tid / kWave;
-    const uint32_t base = blockIdx.x * tile;
-    const uint32_t end = a.n - base < tile ? a.n : base + tile;
-    for (uint32_t i0 = base; i0 < end; i0 += kGroupBlock) {
-        const uint32_t i = i0 + tid;
-        const uint32_t e = i < end ? a.ids[i] : kNone;
-        const bool real = e < a.experts;
-        uint64_t same = ballot(real);
-        for (int b = 0; b < 10; ++b) {
-            const uint64_t ones = ballot((e >> b) & 1u);
-            same &= ((e >> b) & 1u) ? ones : ~ones;
-        }
-        const uint32_t rank = count_below(same);
-        uint32_t at = kNone;
-        for (uint32_t w = 0; w < kGroupBlock / kWave; ++w) {   // the waves take turns, in order
-            if (w == wave && real) {
-                at = s_next[e] + rank;
-                // every lane of the expert has read the word before the last of them writes it
-                __builtin_amdgcn_wave_barrier();
-                if (rank + 1 == static_cast<uint32_t>(__builtin_popcountll(same))) s_next[e] = at + 1;
-            }
-            __syncthreads();
-        }
-        if (real) a.order[at] = i;
-        if (i < end) a.place[i] = at;
+    const uint32_t base = blockIdx.x * (kGroupBlock * ITEMS);
+    s_count[tid] = 0;
+    uint32_t e[ITEMS];
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        const uint32_t i = base + j * kGroupBlock + tid;
+        e[j] = i < a.n ? a.ids[i] : kNone;
     }
-    // the padding, and the room behind the last segment
-    for (uint32_t e = blockIdx.x; e < a.experts; e += gridDim.x)
-        for (uint32_t p = a.starts[e] + a.counts[e] + tid; p < a.starts[e + 1]; p += kGroupBlock) a.order[p] = kNone;
-    for (uint32_t p = a.starts[a.experts] + blockIdx.x * kGroupBlock + tid; p < a.room; p += gridDim.x * kGroupBlock)
-        a.order[p] = kNone;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j)
+        if (e[j] < a.experts) atomicAdd(&s_count[e[j]], 1u);
+    __syncthreads();
+    if (tid < a.experts) tile_counts[static_cast<uint64_t>(blockIdx.x) * a.experts + tid] = s_count[tid];
+}
+
+// Block b, experts 64 b .. : tile_counts become the choices of earlier tiles,
+// totals[e] those of all.  Wave w takes a run of tiles: sums it, then, with the
+// sums of earlier runs, writes its offsets.
+__global__ __launch_bounds__(kGroupBlock) void group_scan_kernel(uint32_t experts, uint32_t tiles,
+                                                                 uint32_t* __restrict__ tile_counts,
+                                                                 uint32_t* __restrict__ totals) {
+    __shared__ uint32_t s_sum[kGroupWaves][kWave];
+    const uint32_t wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
+    const uint32_t e = blockIdx.x * kWave + lane;
+    const bool real = e < experts;
+    const uint32_t run = (tiles + kGroupWaves - 1) / kGroupWaves;
+    const uint32_t begin = wave * run < tiles ? wave * run : tiles;
+    const uint32_t end = begin + run < tiles ? begin + run : tiles;
+    uint32_t* col = tile_counts + (real ? e : 0u);
+    uint32_t sum = 0;
+#pragma unroll 8
+    for (uint32_t t = begin; t < end; ++t) sum += real ? col[static_cast<uint64_t>(t) * experts] : 0u;
+    s_sum[wave][lane] = sum;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+    for (uint32_t w = 0; w < kGroupWaves; ++w) {
+        const uint32_t s = s_sum[w][lane];
+        before += w < wave ? s : 0u;
+        all += s;
+    }
+    if (!real) return;
+    if (wave == 0) totals[e] = all;
+    for (uint32_t t0 = begin; t0 < end; t0 += 8) {   // eight loads at a time, ahead of their stores
+        uint32_t c[8];
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) c[j] = t0 + j < end ? col[static_cast<uint64_t>(t0 + j) * experts] : 0u;
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+            if (t0 + j < end) col[static_cast<uint64_t>(t0 + j) * experts] = before;
+            before += c[j];
+        }
+    }
+}
+
+// Where a tile learns of the others' choices.
+enum Source { kAlone, kTileCounts, kTileOffsets };
+
+template <int ITEMS, Source SOURCE>
+__global__ __launch_bounds__(kGroupBlock) void group_place_kernel(GroupArgs a, uint32_t bits,
+                                                                  const uint32_t* __restrict__ tile_counts,
+                                                                  const uint32_t* __restrict__ totals) {
+    // [experts] words: first place of the tile's choices, first and end of the
+    // padding; then [waves][experts] halves: a wave's choices, then those of
+    // the tile's earlier waves
+    extern __shared__ uint32_t s_base[];
+    uint32_t* s_pad = s_base + a.experts;
+    uint32_t* s_end = s_pad + a.experts;
+    __shared__ uint32_t s_wave[kGroupWaves];
+    __shared__ uint32_t s_part[2][kGroupBlock];
+    __shared__ uint32_t s_length;
+    const uint32_t tid = threadIdx.x, wave = tid / kWave, lane = tid & (kWave - 1);
+    uint16_t* s_count = reinterpret_cast<uint16_t*>(s_end + a.experts) + wave * a.experts;   // the wave's
+    const uint32_t tile = blockIdx.x;
+    const uint32_t base = tile * (kGroupBlock * ITEMS) + wave * (kWave * ITEMS) + lane;
+
+    uint32_t e[ITEMS], rank[ITEMS];
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        const uint32_t i = base + j * kWave;
+        e[j] = i < a.n ? a.ids[i] : kNone;
+    }
+    for (uint32_t x = lane; x < a.experts; x += kWave) s_count[x] = 0;
+    if (SOURCE == kTileCounts) {
+        // chunk c of 64 experts and slice q of the tiles for each wave
+        const uint32_t chunks = (a.experts + kWave - 1) / kWave;
+        const uint32_t slices = kGroupWaves / chunks;
+        const uint32_t c = wave % chunks, q = wave / chunks;
+        const uint32_t x = c * kWave + lane;
+        uint32_t before = 0, all = 0;
+        if (q < slices && x < a.experts) {
+#pragma unroll 8
+            for (uint32_t t = q; t < gridDim.x; t += slices) {
+                const uint32_t n = tile_counts[static_cast<uint64_t>(t) * a.experts + x];
+                all += n;
+                before += t < tile ? n : 0u;
+            }
+        }
+        s_part[0][tid] = before;
+        s_part[1][tid] = all;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        const bool real = e[j] < a.experts;
+        uint64_t peers = ballot(real);
+        for (uint32_t b = 0; b < bits; ++b) {
+            const uint64_t ones = ballot((e[j] >> b) & 1u);
+            peers &= ((e[j] >> b) & 1u) ? ones : ~ones;
+        }
+        const uint32_t below = count_below(peers);
+        rank[j] = real ? s_count[e[j]] + below : 0u;
+        wave_fence();   // all peers have read before the last of them writes
+        if (real && below + 1 == static_cast<uint32_t>(__builtin_popcountll(peers)))
+            s_count[e[j]] = static_cast<uint16_t>(rank[j] + 1);
+        wave_fence();
+    }
+    __syncthreads();
+    uint32_t before = 0, total = 0;
+    if (tid < a.experts) {
+        uint16_t* column = reinterpret_cast<uint16_t*>(s_end + a.experts) + tid;
+        uint32_t sum = 0;
+#pragma unroll
+        for (uint32_t w = 0; w < kGroupWaves; ++w) {
+            const uint32_t n = column[w * a.experts];
+            column[w * a.experts] = static_cast<uint16_t>(sum);
+            sum += n;
+        }
+        total = sum;
+        if (SOURCE == kTileCounts) {
+            const uint32_t chunks = (a.experts + kWave - 1) / kWave;
+            total = 0;
+            for (uint32_t q = 0; q < kGroupWaves / chunks; ++q) {
+                before += s_part[0][q * chunks * kWave + tid];
+                total += s_part[1][q * chunks * kWave + tid];
+            }
+        } else if (SOURCE == kTileOffsets) {
+            before = tile_counts[static_cast<uint64_t>(tile) * a.experts + tid];
+            total = totals[tid];
+        }
+    }
+    // the segments: padded totals, summed over the experts
+    const uint32_t padded = (total + a.align - 1) / a.align * a.align;
+    const uint32_t incl = wave_inclusive_sum(padded);
+    if (lane == kWave - 1) s_wave[wave] = incl;
+    __syncthreads();
+    uint32_t start = incl - padded;
+    for (uint32_t w = 0; w < wave; ++w) start += s_wave[w];
+    if (tid < a.experts) {
+        s_base[tid] = start + before;
+        s_pad[tid] = start + total;
+        s_end[tid] = start + padded;
+        if (tid == a.experts - 1) s_length = start + padded;
+        if (tile == 0) {
+            a.counts[tid] = total;
+            a.starts[tid] = start;
+            if (tid == a.experts - 1) a.starts[a.experts] = start + padded;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        const uint32_t i = base + j * kWave;
+        uint32_t at = kNone;
+        if (e[j] < a.experts) {
+            at = s_base[e[j]] + s_count[e[j]] + rank[j];
+            a.order[at] = i;
+        }
+        if (i < a.n) a.place[i] = at;
+    }
+    // the padding, a wave for each expert, and the room behind the last segment
+    if (a.align > 1) {
+        for (uint32_t x = tile * kGroupWaves + wave; x < a.experts; x += gridDim.x * kGroupWaves)
+            for (uint32_t p = s_pad[x] + lane; p < s_end[x]; p += kWave) a.order[p] = kNone;
+    }
+    for (uint32_t p = s_length + tile * kGroupBlock + tid; p < a.room; p += gridDim.x * kGroupBlock) a.order[p] = kNone;
+}
+
+template <int ITEMS>
+hipError_t group_items_of(const GroupArgs& a, uint32_t tiles, uint32_t* temp, hipStream_t stream) {
+    uint32_t bits = 0;
+    while ((1u << bits) < a.experts) ++bits;
+    const size_t lds = a.experts * (3 * sizeof(uint32_t) + kGroupWaves * sizeof(uint16_t));
+    const uint64_t counts = static_cast<uint64_t>(tiles) * a.experts;
+    hipError_t e = hipSuccess;
+    if (tiles > 1) {
+        timing_before(stream, RS_KERNEL_GROUP_COUNT);
+        group_count_kernel<ITEMS><<<dim3(tiles), kGroupBlock, 0, stream>>>(a, temp);
+        e = hipGetLastError();
+        timing_after(stream);
+        if (e != hipSuccess) return e;
+    }
+    uint32_t* totals = temp + counts;
+    if (tiles > 1 && counts > kShortSum) {
+        timing_before(stream, RS_KERNEL_GROUP_SCAN);
+        group_scan_kernel<<<dim3((a.experts + kWave - 1) / kWave), kGroupBlock, 0, stream>>>(a.experts, tiles, temp, totals);
+        e = hipGetLastError();
+        timing_after(stream);
+        if (e != hipSuccess) return e;
+    }
+    timing_before(stream, RS_KERNEL_GROUP_PLACE);
+    const auto kernel = tiles <= 1 ? group_place_kernel<ITEMS, kAlone>
+                        : counts > kShortSum ? group_place_kernel<ITEMS, kTileOffsets>
+                                             : group_place_kernel<ITEMS, kTileCounts>;
+    kernel<<<dim3(tiles ? tiles : 1), kGroupBlock, lds, stream>>>(a, bits, temp, totals);
+    e = hipGetLastError();
+    timing_after(stream);
+    return e;
 }
 
 }  // namespace
 
 size_t group_temp_bytes(uint64_t n, uint32_t experts) {
-    const size_t words = static_cast<size_t>(group_tiles(n)) * experts;
-    return (words ? words : 1) * 4;
+    const uint64_t tiles = group_tiles(n);
+    return tiles > 1 ? (tiles + 1) * experts * sizeof(uint32_t) : 16;
 }
 
 hipError_t launch_group(const GroupArgs& a, void* temp, hipStream_t stream) {
-    uint32_t* tile_counts = static_cast<uint32_t*>(temp);
-    const uint32_t tile = group_tile(a.n), tiles = group_tiles(a.n);
-    if (tiles) {
-        timing_before(stream, RS_KERNEL_GROUP_COUNT);
-        group_count_kernel<<<dim3(tiles), kGroupBlock, 0, stream>>>(a, tile, tile_counts);
-        const hipError_t e = hipGetLastError();
-        timing_after(stream);
-        if (e != hipSuccess) return e;
+    const uint32_t tiles = group_tiles(a.n);
+    uint32_t* words = static_cast<uint32_t*>(temp);
+    switch (group_items(a.n)) {
+    case 1: return group_items_of<1>(a, tiles, words, stream);
+    case 4: return group_items_of<4>(a, tiles, words, stream);
+    default: return group_items_of<16>(a, tiles, words, stream);
     }
-    timing_before(stream, RS_KERNEL_GROUP_SCAN);
-    group_scan_kernel<<<dim3(1), RS_MAX_EXPERTS, 0, stream>>>(a, tiles, tile_counts);
-    hipError_t e = hipGetLastError();
-    timing_after(stream);
-    if (e != hipSuccess) return e;
-    timing_before(stream, RS_KERNEL_GROUP_PLACE);
-    group_place_kernel<<<dim3(tiles ? tiles : 1), kGroupBlock, 0, stream>>>(a, tile, tile_counts);
-    e = hipGetLastError();
-    timing_after(stream);
-    return e;
 }
 
 }  // namespace rs

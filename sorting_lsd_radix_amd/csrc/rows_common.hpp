@@ -47,13 +47,6 @@ __device__ __forceinline__ float value_of_order32(uint32_t o) {
     return o == 1u ? __builtin_nanf("") : __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o);
 }
 
-// The wave's own LDS writes are visible to its lanes' reads behind this.
-__device__ __forceinline__ void wave_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // V consecutive elements at `at`, of which the first `n` exist; `fill` for the others.
 template <int V, class T>
 __device__ __forceinline__ void load_some(const T* at, uint32_t n, float fill, float (&x)[V]) {
