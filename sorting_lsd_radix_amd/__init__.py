@@ -611,41 +611,67 @@ def bitonic_tile(keys, tile, begin_bit=0, end_bit=32, out=None, stream=None):
 
 
 # --- rows of scores -------------------------------------------------------------------
+#
+# Small calls of these are as long as the host takes to make them: the wrappers look torch's
+# types up once, allocate with as few calls as they can and hand plain numbers to the library.
+
+_torch = None
+_ELEMS = {}
+_INTS = ()
+
+
+def _load_torch():
+    global _torch, _INTS
+    if _torch is None:
+        import torch
+        _ELEMS.update({torch.float32: RS_ELEM_F32, torch.float16: RS_ELEM_F16,
+                       torch.bfloat16: RS_ELEM_BF16})
+        _INTS = (torch.int32, torch.uint32)
+        _torch = torch
+    return _torch
+
 
 def _rows(t, name, dtype=None):
     """(elem_type, rows, columns, row stride) of a matrix whose rows are dense."""
-    import torch
-    table = {torch.float32: RS_ELEM_F32, torch.float16: RS_ELEM_F16, torch.bfloat16: RS_ELEM_BF16}
-    if not t.is_cuda or t.dim() != 2 or t.dtype not in table or \
-            (t.stride(1) != 1 and t.shape[1] > 1):
+    shape = t.shape
+    if not t.is_cuda or len(shape) != 2 or t.dtype not in _ELEMS or \
+            (t.stride(1) != 1 and shape[1] > 1):
         raise TypeError("%s must be a 2-D CUDA tensor of float32, float16 or bfloat16 whose rows "
                         "are contiguous" % name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must be of %s" % (name, dtype))
-    return table[t.dtype], t.shape[0], t.shape[1], t.stride(0)
+    return _ELEMS[t.dtype], shape[0], shape[1], t.stride(0)
 
 
-def _check_like(t, name, shape, dtypes, device):
-    """A contiguous tensor of `shape`, one of `dtypes`, on `device`."""
-    if t.device != device or t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or \
+def _check_like(t, name, shape, dtypes, index):
+    """A contiguous CUDA tensor of `shape`, one of `dtypes`, on the device `index`; its address."""
+    if t.dtype not in dtypes or t.shape != shape or not t.is_cuda or t.get_device() != index or \
             not t.is_contiguous():
-        raise TypeError("%s must be a contiguous tensor of shape %s and %s on %s"
-                        % (name, tuple(shape), " or ".join(str(d) for d in dtypes), device))
+        raise TypeError("%s must be a contiguous tensor of shape %s and %s on cuda:%d"
+                        % (name, tuple(shape), " or ".join(str(d) for d in dtypes), index))
+    return t.data_ptr()
+
+
+def _check_out(out, name, rows, cols, dtype, index):
+    """(address, row stride) of a matrix that a call writes."""
+    _, orows, ocols, stride = _rows(out, "out", dtype)
+    if (orows, ocols) != (rows, cols) or out.get_device() != index:
+        raise TypeError("out must have the %s' shape and device" % name)
+    return out.data_ptr(), stride
 
 
 class _On:
-    """The device of a call's tensors as the current one, and the stream it runs on as torch's
-    current one, so that what the call allocates belongs to that stream."""
+    """A device as the current one and a stream (None: torch's current one) as torch's current
+    one, so that what is allocated meanwhile belongs to that stream."""
 
-    def __init__(self, device, stream):
-        import torch
+    def __init__(self, index, stream):
         self._contexts = []
-        if device.index != torch.cuda.current_device():
-            self._contexts.append(torch.cuda.device(device))
+        if index != _torch.cuda.current_device():
+            self._contexts.append(_torch.cuda.device(index))
         if stream is not None:
             if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            self._contexts.append(torch.cuda.stream(stream))
+                stream = _torch.cuda.ExternalStream(stream, device=index)
+            self._contexts.append(_torch.cuda.stream(stream))
 
     def __enter__(self):
         for c in self._contexts:
@@ -656,9 +682,16 @@ class _On:
             c.__exit__(*exc)
 
 
-def _ints():
-    import torch
-    return torch.int32, torch.uint32
+def _run_on(index, stream, call):
+    """call(address of the stream) with the device and the stream as the current ones."""
+    if stream is None and index == _torch.cuda.current_device():
+        return call(_torch._C._cuda_getCurrentRawStream(index))
+    with _On(index, stream):
+        return call(_torch._C._cuda_getCurrentRawStream(index))
+
+
+def _temp_arg(temp, size, device):
+    return _torch.empty(size.value, dtype=_torch.uint8, device=device) if temp is None else temp
 
 
 def route_topk(scores, top_k, bias=None, score="softmax", groups=1, top_groups=1, group_best=1,
@@ -671,16 +704,23 @@ def route_topk(scores, top_k, bias=None, score="softmax", groups=1, top_groups=1
     top_groups groups whose group_best largest biased probabilities have the largest sum.
     Ties go to the lower expert.  The weights are scale * p, divided by the sum of the row's
     chosen p if renormalize."""
-    import torch
+    torch = _load_torch()
     et, rows, experts, stride = _rows(scores, "scores")
+    index = scores.get_device()
     if bias is not None:
-        _check_like(bias, "bias", (experts,), (torch.float32,), scores.device)
-    with _On(scores.device, stream):
-        ids = torch.empty((rows, top_k), dtype=torch.int32, device=scores.device)
-        weights = torch.empty((rows, top_k), dtype=torch.float32, device=scores.device)
-        rs_route_topk(et, scores, stride, bias, rows, experts, top_k, _SCORES[score], groups,
-                      top_groups, group_best, renormalize, scale, ids, weights)
-    return ids, weights
+        bias = _check_like(bias, "bias", (experts,), (torch.float32,), index)
+    fn = _SCORES[score]
+    lib = _load()
+
+    def call(on):
+        ids = torch.empty(rows, top_k, dtype=torch.int32, device=scores.device)
+        weights = torch.empty(rows, top_k, dtype=torch.float32, device=scores.device)
+        _call("rs_route_topk", lib.rs_route_topk(
+            et, scores.data_ptr(), stride, bias, rows, experts, top_k, fn, groups, top_groups,
+            group_best, 1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), on))
+        return ids, weights
+
+    return _run_on(index, stream, call)
 
 
 def route_topk_grad(scores, ids, weights, dweights, score="softmax", renormalize=True, scale=1.0,
@@ -688,21 +728,28 @@ def route_topk_grad(scores, ids, weights, dweights, score="softmax", renormalize
     """Gradient for the scores of the weights that route_topk gave with these ids, score,
     renormalize and scale; dweights float32 [rows, top_k].  Returns dscores [rows, experts] of the
     scores' type (`out`, if given: a matrix whose rows are contiguous)."""
-    import torch
+    torch = _load_torch()
     et, rows, experts, stride = _rows(scores, "scores")
-    shape = (rows, ids.shape[-1])
-    _check_like(ids, "ids", shape, _ints(), scores.device)
-    _check_like(weights, "weights", shape, (torch.float32,), scores.device)
-    _check_like(dweights, "dweights", shape, (torch.float32,), scores.device)
-    with _On(scores.device, stream):
-        if out is None:
-            out = torch.empty((rows, experts), dtype=scores.dtype, device=scores.device)
-        _, orows, ocols, ostride = _rows(out, "out", scores.dtype)
-        if (orows, ocols) != (rows, experts) or out.device != scores.device:
-            raise TypeError("out must have the scores' shape and device")
-        rs_route_topk_grad(et, scores, stride, ids, weights, dweights, rows, experts, shape[1],
-                           _SCORES[score], renormalize, scale, out, ostride)
-    return out
+    index = scores.get_device()
+    top_k = ids.shape[-1]
+    shape = (rows, top_k)
+    f32 = (torch.float32,)
+    args = (_check_like(ids, "ids", shape, _INTS, index),
+            _check_like(weights, "weights", shape, f32, index),
+            _check_like(dweights, "dweights", shape, f32, index))
+    fn = _SCORES[score]
+    lib = _load()
+
+    def call(on):
+        to = torch.empty(rows, experts, dtype=scores.dtype, device=scores.device) if out is None \
+            else out
+        at, ostride = _check_out(to, "scores", rows, experts, scores.dtype, index)
+        _call("rs_route_topk_grad", lib.rs_route_topk_grad(
+            et, scores.data_ptr(), stride, *args, rows, experts, top_k, fn,
+            1 if renormalize else 0, scale, at, ostride, on))
+        return to
+
+    return _run_on(index, stream, call)
 
 
 def group_choices(ids, experts, align=1, temp=None, stream=None):
@@ -713,20 +760,30 @@ def group_choices(ids, experts, align=1, temp=None, stream=None):
     -1 in the padding and behind the last segment.  place (of the ids' shape): each choice's
     position, -1 where its id is not an expert (-1, or `experts` and above).  starts
     [experts + 1]: where each segment begins, and the length of all.  counts [experts]."""
-    import torch
-    _check_like(ids, "ids", ids.shape, _ints(), ids.device)
-    if not ids.is_cuda:
-        raise TypeError("ids must be a CUDA tensor")
+    torch = _load_torch()
+    shape = ids.shape
+    index = ids.get_device() if ids.is_cuda else -1
+    at = _check_like(ids, "ids", shape, _INTS, index)
     n = ids.numel()
-    need = rs_group_choices(None, n, experts, align, None, None, None, None, None, 0)
-    with _On(ids.device, stream):
-        order = torch.empty(n + experts * (align - 1), dtype=torch.int32, device=ids.device)
-        place = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
-        starts = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
-        counts = torch.empty(experts, dtype=torch.int32, device=ids.device)
-        temp = _temp(need, ids.device) if temp is None else temp
-        rs_group_choices(ids, n, experts, align, order, place, starts, counts, temp, temp.numel())
-    return order, place, starts, counts
+    lib = _load()
+    size = ctypes.c_size_t(0)
+    _call("rs_group_choices", lib.rs_group_choices(None, n, experts, align, None, None, None, None,
+                                                   None, ctypes.byref(size), None))
+
+    def call(on):
+        dev, i32 = ids.device, torch.int32
+        order = torch.empty(n + experts * (align - 1), dtype=i32, device=dev)
+        place = torch.empty(shape, dtype=i32, device=dev)
+        starts = torch.empty(experts + 1, dtype=i32, device=dev)
+        counts = torch.empty(experts, dtype=i32, device=dev)
+        work = _temp_arg(temp, size, dev)
+        have = ctypes.c_size_t(work.numel())
+        _call("rs_group_choices", lib.rs_group_choices(
+            at, n, experts, align, order.data_ptr(), place.data_ptr(), starts.data_ptr(),
+            counts.data_ptr(), work.data_ptr(), ctypes.byref(have), on))
+        return order, place, starts, counts
+
+    return _run_on(index, stream, call)
 
 
 TokenLogprobs = collections.namedtuple(
@@ -742,29 +799,42 @@ def token_logprobs(logits, targets=None, top_k=0, scale=1.0, temp=None, stream=N
     None without targets; entropy [rows] in nats; lse [rows], the log of the sum of exp; stats
     [rows, 2], the largest logit and the sum of exp relative to it, which token_logprobs_grad
     takes; top_ids (int32) and top_logprobs [rows, top_k], the largest logits in order, ties to
-    the lower index, both None with top_k 0.  Floating outputs are float32."""
-    import torch
+    the lower index, both None with top_k 0.  Floating outputs are float32; those of [rows] are
+    views of one tensor."""
+    torch = _load_torch()
     et, rows, vocab, stride = _rows(logits, "logits")
-    dev = logits.device
+    index = logits.get_device()
     if targets is not None:
-        _check_like(targets, "targets", (rows,), _ints(), dev)
-    need = rs_token_logprobs(et, None, stride, None, rows, vocab, scale, top_k, None, None, None,
-                             None, None, None, None, None, 0)
-    with _On(dev, stream):
-        stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
-        lse = torch.empty(rows, dtype=torch.float32, device=dev)
-        entropy = torch.empty(rows, dtype=torch.float32, device=dev)
+        given = targets
+        targets = _check_like(given, "targets", (rows,), _INTS, index)
+    lib = _load()
+    size = ctypes.c_size_t(0)
+    _call("rs_token_logprobs", lib.rs_token_logprobs(
+        et, None, stride, None, rows, vocab, scale, top_k, None, None, None, None, None, None,
+        None, None, ctypes.byref(size), None))
+    wanted = targets is not None
+
+    def call(on):
+        dev, f32, i32 = logits.device, torch.float32, torch.int32
+        stats = torch.empty(rows, 2, dtype=f32, device=dev)
+        lse, entropy, *of_target = torch.empty(4 if wanted else 2, rows, dtype=f32,
+                                               device=dev).unbind(0)
         logprob = rank = top_ids = top_logprobs = None
-        if targets is not None:
-            logprob = torch.empty(rows, dtype=torch.float32, device=dev)
-            rank = torch.empty(rows, dtype=torch.int32, device=dev)
+        if wanted:
+            logprob, rank = of_target
+            rank = rank.view(i32)
         if top_k:
-            top_ids = torch.empty((rows, top_k), dtype=torch.int32, device=dev)
-            top_logprobs = torch.empty((rows, top_k), dtype=torch.float32, device=dev)
-        temp = _temp(need, dev) if temp is None else temp
-        rs_token_logprobs(et, logits, stride, targets, rows, vocab, scale, top_k, stats, lse,
-                          entropy, logprob, rank, top_ids, top_logprobs, temp, temp.numel())
-    return TokenLogprobs(logprob, entropy, lse, rank, stats, top_ids, top_logprobs)
+            top_ids = torch.empty(rows, top_k, dtype=i32, device=dev)
+            top_logprobs = torch.empty(rows, top_k, dtype=f32, device=dev)
+        work = _temp_arg(temp, size, dev)
+        have = ctypes.c_size_t(work.numel())
+        _call("rs_token_logprobs", lib.rs_token_logprobs(
+            et, logits.data_ptr(), stride, targets, rows, vocab, scale, top_k, stats.data_ptr(),
+            lse.data_ptr(), entropy.data_ptr(), _ptr(logprob), _ptr(rank), _ptr(top_ids),
+            _ptr(top_logprobs), work.data_ptr(), ctypes.byref(have), on))
+        return TokenLogprobs(logprob, entropy, lse, rank, stats, top_ids, top_logprobs)
+
+    return _run_on(index, stream, call)
 
 
 def token_logprobs_grad(logits, stats, targets=None, dlogprob=None, entropy=None, dentropy=None,
@@ -773,22 +843,24 @@ def token_logprobs_grad(logits, stats, targets=None, dlogprob=None, entropy=None
     dlse * lse (each float32 [rows], or None), from the stats, and with dentropy the entropy, that
     token_logprobs gave.  Returns dlogits of the logits' type and shape (`out`, if given: a matrix
     whose rows are contiguous; it may be the logits themselves)."""
-    import torch
+    torch = _load_torch()
     et, rows, vocab, stride = _rows(logits, "logits")
-    dev = logits.device
-    _check_like(stats, "stats", (rows, 2), (torch.float32,), dev)
-    if targets is not None:
-        _check_like(targets, "targets", (rows,), _ints(), dev)
-    for t, name in ((dlogprob, "dlogprob"), (entropy, "entropy"), (dentropy, "dentropy"),
-                    (dlse, "dlse")):
-        if t is not None:
-            _check_like(t, name, (rows,), (torch.float32,), dev)
-    with _On(dev, stream):
-        if out is None:
-            out = torch.empty((rows, vocab), dtype=logits.dtype, device=dev)
-        _, orows, ocols, ostride = _rows(out, "out", logits.dtype)
-        if (orows, ocols) != (rows, vocab) or out.device != dev:
-            raise TypeError("out must have the logits' shape and device")
-        rs_token_logprobs_grad(et, logits, stride, targets, stats, entropy, rows, vocab, scale,
-                               dlogprob, dentropy, dlse, out, ostride)
-    return out
+    index = logits.get_device()
+    f32 = (torch.float32,)
+    at_stats = _check_like(stats, "stats", (rows, 2), f32, index)
+    at_targets = None if targets is None else _check_like(targets, "targets", (rows,), _INTS, index)
+    at_rows = [None if t is None else _check_like(t, name, (rows,), f32, index)
+               for t, name in ((entropy, "entropy"), (dlogprob, "dlogprob"),
+                               (dentropy, "dentropy"), (dlse, "dlse"))]
+    lib = _load()
+
+    def call(on):
+        to = torch.empty(rows, vocab, dtype=logits.dtype, device=logits.device) if out is None \
+            else out
+        at, ostride = _check_out(to, "logits", rows, vocab, logits.dtype, index)
+        _call("rs_token_logprobs_grad", lib.rs_token_logprobs_grad(
+            et, logits.data_ptr(), stride, at_targets, at_stats, at_rows[0], rows, vocab, scale,
+            *at_rows[1:], at, ostride, on))
+        return to
+
+    return _run_on(index, stream, call)
