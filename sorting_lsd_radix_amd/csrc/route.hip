@@ -84,19 +84,32 @@ struct Candidate {
     uint32_t e;
 };
 
-// The kept groups of the wave's rows, as masks (equal in a row's lanes), from
-// the scores (f32 or 64 bits) in the row's LDS: score [experts], and room for
-// best_of [groups].  Lane l has written its experts' scores.  P = L / (groups,
-// rounded up to a power of two) lanes share a group; the best two of each meet
-// by lane exchanges.  off, rel: how far two groups' scores may be off together;
-// `unclear` tells whether that leaves the row's choice open.
+// The best two scores of the group that `p` lanes share, from each lane's two;
+// then the group's score into the row's LDS, best_of [groups].
+template <class S>
+__device__ __forceinline__ void group_score(const RouteArgs& a, S best, S next, uint32_t sub, uint32_t p, S masked,
+                                            S* best_of) {
+    for (uint32_t o = 1; o < p; o <<= 1) {
+        const S b = __shfl_xor(best, static_cast<int>(o), kWave), n = __shfl_xor(next, static_cast<int>(o), kWave);
+        next = fmax(fmax(next, n), fmin(best, b));
+        best = fmax(best, b);
+    }
+    const uint32_t g = sub / p;
+    if (g < a.groups && sub == g * p) {
+        S sum = a.group_best == 2 && next > masked ? best + next : best;
+        // a sum below f32's range is not a masked group's
+        if (sizeof(S) == 4 && best > masked) sum = fmax(sum, S(-3.402823466e38f));
+        best_of[g] = sum;
+    }
+}
+
+// The same from the scores of all experts in the row's LDS, score [experts]: p =
+// L / (groups, rounded up to a power of two) lanes share a group.
 template <int L, class S>
-__device__ __forceinline__ uint64_t kept_groups(const RouteArgs& a, const S* score, S* best_of, S masked, S off,
-                                                S rel, bool* unclear) {
-    const uint32_t lane = lane_id();
-    const uint32_t sub = lane & (L - 1);
+__device__ __forceinline__ void group_scores(const RouteArgs& a, const S* score, S* best_of, S masked) {
+    const uint32_t sub = lane_id() & (L - 1);
     const uint32_t size = a.experts / a.groups;
-    uint32_t p = L;   // lanes of a group
+    uint32_t p = L;
     while (p * a.groups > L) p >>= 1;
     const uint32_t g = sub / p;
     S best = masked, next = masked;
@@ -108,17 +121,18 @@ __device__ __forceinline__ uint64_t kept_groups(const RouteArgs& a, const S* sco
             best = fmax(best, s);
         }
     }
-    for (uint32_t o = 1; o < p; o <<= 1) {
-        const S b = __shfl_xor(best, o, kWave), n = __shfl_xor(next, o, kWave);
-        next = fmax(fmax(next, n), fmin(best, b));
-        best = fmax(best, b);
-    }
-    if (g < a.groups && (sub & (p - 1)) == 0) {
-        S sum = a.group_best == 2 && next > masked ? best + next : best;
-        // a sum below f32's range is not a masked group's
-        if (sizeof(S) == 4 && best > masked) sum = fmax(sum, S(-3.402823466e38f));
-        best_of[g] = sum;
-    }
+    group_score(a, best, next, sub, p, masked, best_of);
+}
+
+// The kept groups of the wave's rows, as masks (equal in a row's lanes), from
+// the groups' scores best_of [groups] (f32 or 64 bits).  off, rel: how far two
+// scores may be off together; `unclear` tells whether that leaves the row's
+// choice open.
+template <int L, class S>
+__device__ __forceinline__ uint64_t kept_groups(const RouteArgs& a, const S* best_of, S masked, S off, S rel,
+                                                bool* unclear) {
+    const uint32_t lane = lane_id();
+    const uint32_t sub = lane & (L - 1);
     wave_fence();
     bool kept = false, open = false;
     if (sub < a.groups) {   // groups before this one, and groups that may be
@@ -200,16 +214,15 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
             key[j] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[j] * -1.44269504088896341f));
     }
 
-    // What the groups go by, and what the experts go by
-    float* score = reinterpret_cast<float*>(s_groups + slot * (a.experts + a.groups));
+    // What the groups go by (by[]), and what the experts go by (key[])
+    float by[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         if (biased) key[j] += bias[j];
-        const float by = by_p ? key[j] : x[j];
+        by[j] = by_p ? key[j] : x[j];
         const bool masked = !(x[j] > -kInf);
-        const float g = masked || !(by > -kInf) ? -kInf : by;
-        key[j] = static_cast<uint32_t>(j) >= real ? __builtin_nanf("") : biased ? g : masked ? -kInf : x[j];
-        if (a.groups > 1 && static_cast<uint32_t>(j) < real) score[first + j] = g;
+        if (masked || !(by[j] > -kInf)) by[j] = -kInf;
+        key[j] = static_cast<uint32_t>(j) >= real ? __builtin_nanf("") : biased ? by[j] : masked ? -kInf : x[j];
     }
     // The same s in 64 bits
     auto exact = [&](float v, uint32_t e, bool masked) {
@@ -218,9 +231,26 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
     };
 
     if (a.groups > 1) {
-        wave_fence();
+        const uint32_t size = a.experts / a.groups;
+        float* score = reinterpret_cast<float*>(s_groups + slot * (a.experts + a.groups));
+        const uint32_t p = size / V;
+        if (p * V == size && (p & (p - 1)) == 0) {   // whole lanes to a group, a power of two of them
+            float most = by[0], next = -kInf;
+#pragma unroll
+            for (int j = 1; j < V; ++j) {
+                next = fmaxf(next, fminf(most, by[j]));
+                most = fmaxf(most, by[j]);
+            }
+            group_score(a, most, next, sub, p, -kInf, score + a.experts);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (static_cast<uint32_t>(j) < real) score[first + j] = by[j];
+            wave_fence();
+            group_scores<L>(a, score, score + a.experts, -kInf);
+        }
         bool unclear;
-        uint64_t kept = kept_groups<L, float>(a, score, score + a.experts, -kInf, by_p ? 4 * kOff : 0.0f,
+        uint64_t kept = kept_groups<L, float>(a, score + a.experts, -kInf, by_p ? 4 * kOff : 0.0f,
                                               by_p ? 2 * kOffRel : 0.0f, &unclear);
         if (ballot(unclear) != 0) {
             double* wide = s_groups + slot * (a.experts + a.groups);
@@ -236,10 +266,10 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
             }
             wave_fence();
             bool none;
-            const uint64_t sure = kept_groups<L, double>(a, wide, wide + a.experts, kMasked, 0.0, 0.0, &none);
+            group_scores<L>(a, wide, wide + a.experts, kMasked);
+            const uint64_t sure = kept_groups<L, double>(a, wide + a.experts, kMasked, 0.0, 0.0, &none);
             kept = unclear ? sure : kept;
         }
-        const uint32_t size = a.experts / a.groups;
         uint32_t g = first / size, in_group = first - g * size;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -444,21 +474,20 @@ hipError_t route_lanes(const RouteArgs& a, hipStream_t stream) {
     if (a.experts <= L) return route_shape<ELEM, L, 1>(a, stream);
     if (a.experts <= 2 * L) return route_shape<ELEM, L, 2>(a, stream);
     if (a.experts <= 4 * L) return route_shape<ELEM, L, 4>(a, stream);
-    if constexpr (L == kWave)
-        if (a.experts > 8 * L) return route_shape<ELEM, L, 16>(a, stream);
-    return route_shape<ELEM, L, 8>(a, stream);
+    if (a.experts <= 8 * L) return route_shape<ELEM, L, 8>(a, stream);
+    return route_shape<ELEM, L, 16>(a, stream);
 }
 
-// Lanes of a row: enough that every group has one, that a lane has at most 8
-// experts (of 256 and 32 lanes; 16 lanes with 16 each, fewer waves that wait
-// longer: 30 -> 22 us at 16384 rows with groups), and that there are twice
-// top_k: about 1.4 top_k of a row reach the top_k-th of the lanes' bests then,
-// and the list of candidates has a place for each lane.  Experts are spread
-// over all lanes for the same reason.
+// Lanes of a row: enough that every group has one, that a lane has at most 16
+// experts (8 of 16 lanes: 256 experts on 32 lanes take 11.8 us for 16384 rows,
+// 15.8 on 16; 512 on 32 lanes 25 us for 32768 rows, 33 on 64), and that there
+// are twice top_k: about 1.4 top_k of a row reach the top_k-th of the lanes'
+// bests then, and the list of candidates has a place for each lane.  Experts
+// are spread over all lanes for the same reason.
 template <int ELEM>
 hipError_t route_elem(const RouteArgs& a, hipStream_t stream) {
     if (a.experts <= 128 && a.top_k <= 8 && a.groups <= 16) return route_lanes<ELEM, 16>(a, stream);
-    if (a.experts <= 256 && a.top_k <= 16 && a.groups <= 32) return route_lanes<ELEM, 32>(a, stream);
+    if (a.experts <= 512 && a.top_k <= 16 && a.groups <= 32) return route_lanes<ELEM, 32>(a, stream);
     return route_lanes<ELEM, 64>(a, stream);
 }
 
