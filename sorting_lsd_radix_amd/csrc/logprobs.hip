@@ -79,14 +79,12 @@ struct RowVec {
     T v[N];
 };
 
-// A 16-byte vector that may start on any element (2 bytes, the smallest).
-typedef uint32_t AnyVec __attribute__((ext_vector_type(4), aligned(2)));
-
 // STREAM: the data is read once and is not kept in the caches.
 template <bool STREAM, class T>
 __device__ __forceinline__ RowVec<T> load_raw(const T* at) {
-    const AnyVec* p = reinterpret_cast<const AnyVec*>(at);
-    AnyVec v;
+    using V = AnyVec<16>::V;
+    const V* p = reinterpret_cast<const V*>(at);
+    V v;
     if constexpr (STREAM) v = __builtin_nontemporal_load(p);
     else v = *p;
     return __builtin_bit_cast(RowVec<T>, v);
@@ -621,7 +619,8 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_grad_kernel(LogprobsGradArg
             o.v[j] = static_cast<T>(dx);
         }
         if ((v + 1) * N <= p.vocab) {
-            __builtin_memcpy(out + v * N, &o, sizeof(o));
+            using V = AnyVec<16>::V;
+            *reinterpret_cast<V*>(out + v * N) = __builtin_bit_cast(V, o);
         } else {
 #pragma unroll
             for (uint32_t j = 0; j < N; ++j)

@@ -385,36 +385,67 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
     }
 }
 
-// The gradient: every lane has one choice, whose term (summed over the choices
-// of its expert) it puts into the row's LDS copy, which starts as zeros; the
-// lane then writes its V experts, with the softmax's term that reaches them
-// all where the weights are not renormalised.
-template <int ELEM, int L, int V>
+constexpr size_t kGradLds = 32768;   // a block's: five fit a CU
+
+// The gradient.  Every lane has one choice, whose term (summed over the choices
+// of its expert) it puts into the row's LDS copy, which starts as zeros; then
+// the row's lanes write it in 16-byte vectors next to each other, with the
+// softmax's term that reaches every expert where the weights are not
+// renormalised.  As many rows to a wave as top_k allows: the time of a wave is that
+// of its dependent reads, so that 32768 rows of 512 take 23 us at one row a
+// wave.
+template <int ELEM, int L, bool SPREAD>
 __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(RouteGradArgs a) {
     using T = typename Elem<ELEM>::T;
-    constexpr uint32_t R = kWave / L;
-    __shared__ float s_dx[kRouteWaves * R][L * V];
+    constexpr uint32_t N = 16 / sizeof(T);
+    constexpr uint32_t S = 16 / N;      // steps of a row whose scores are read, see grad_elem
+    extern __shared__ float s_rows[];   // [rows of the block][experts, rounded up to whole steps]
     const uint32_t lane = threadIdx.x & (kWave - 1);
     const uint32_t sub = lane & (L - 1);
     const uint32_t slot = threadIdx.x / L;
-    const uint32_t row_or_more = block_id() * (kRouteWaves * R) + slot;
+    const uint32_t row_or_more = block_id() * (blockDim.x / L) + slot;
     const bool active = row_or_more < a.rows;
     const uint32_t row = active ? row_or_more : a.rows - 1;
     const T* in = static_cast<const T*>(a.scores) + row * a.row_stride;
-    const uint32_t first = sub * V;
-    const uint32_t real = first < a.experts ? a.experts - first : 0u;
+    const uint32_t steps = (a.experts + L * N - 1) / (L * N);
+    float* dx = s_rows + slot * (steps * L * N);
 
-    float dx[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) s_dx[slot][first + j] = 0.0f;
     const bool mine = sub < a.top_k;
     const uint64_t at = static_cast<uint64_t>(row) * a.top_k + (mine ? sub : 0u);
     const uint32_t id = mine ? a.ids[at] : 0xFFFFFFFFu;
     const float w = a.weights[at];
     const float dw = a.dweights[at];
+    const float score = a.sigmoid && id < a.experts ? static_cast<float>(in[id]) : 0.0f;
+    for (uint32_t i = sub; i < steps * (L * N); i += L) dx[i] = 0.0f;
+
+    // SPREAD (softmax, not renormalised): every expert's exp(x - m), in registers
+    float p[S][N];
+    float sum = 0.0f;
+    if (SPREAD) {
+        float m = -__builtin_huge_valf();
+#pragma unroll
+        for (uint32_t i = 0; i < S; ++i) {
+            const uint32_t e = (i * L + sub) * N;
+            const bool real = e < a.experts;
+            load_some<N>(in + (real ? e : 0u), real ? a.experts - e : 0u, -__builtin_huge_valf(), p[i]);
+#pragma unroll
+            for (uint32_t j = 0; j < N; ++j) m = fmaxf(m, p[i][j]);
+        }
+        m = lanes_max<L>(m);
+#pragma unroll
+        for (uint32_t i = 0; i < S; ++i)
+#pragma unroll
+            for (uint32_t j = 0; j < N; ++j) {
+                p[i][j] = expf(p[i][j] - m);
+                sum += (i * L + sub) * N + j < a.experts ? p[i][j] : 0.0f;
+            }
+        sum = lanes_sum<L>(sum);
+        if (m == -__builtin_huge_valf()) sum = 0.0f;   // nothing is left: p = 0 (and d = 0, or NaN where the weights are)
+    }
+
     const float d = lanes_sum<L>(mine ? dw * w : 0.0f);
     float part = w * (a.renormalize ? dw - d / a.scale : dw);
-    if (a.sigmoid && id < a.experts) part *= 1.0f / (1.0f + expf(static_cast<float>(in[id])));
+    if (a.sigmoid) part *= 1.0f / (1.0f + expf(score));
     float term = 0.0f;
     for (uint32_t r = 0; r < a.top_k; ++r) {
         const uint32_t e = __shfl(id, static_cast<int>(lane - sub + r), kWave);
@@ -422,30 +453,28 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(RouteGra
         term += e == id ? g : 0.0f;
     }
     wave_fence();
-    if (id < a.experts) s_dx[slot][id] = term;   // the same from every lane of the expert
+    if (id < a.experts) dx[id] = term;   // the same from every lane of the expert
     wave_fence();
-    if (!a.sigmoid && !a.renormalize) {
-        float x[V];
-        load_some<V>(in + (real ? first : 0u), real, -__builtin_huge_valf(), x);
-        float m = x[0];
+
+    T* out = static_cast<T*>(a.dscores) + row * a.dscores_stride;
+    auto write = [&](uint32_t i, const float* pi) {
+        const uint32_t e = (i * L + sub) * N;
+        if (e >= a.experts) return;
+        float v[N];
 #pragma unroll
-        for (int j = 1; j < V; ++j) m = fmaxf(m, x[j]);
-        m = lanes_max<L>(m);
-        const bool empty = m == -__builtin_huge_valf();   // p = 0 (and d = 0, or NaN where the weights are)
-        float sum = 0.0f;
+        for (uint32_t j = 0; j < N; ++j) v[j] = dx[e + j];
+        if (SPREAD) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            dx[j] = expf(x[j] - m);
-            sum += static_cast<uint32_t>(j) < real ? dx[j] : 0.0f;
+            for (uint32_t j = 0; j < N; ++j) v[j] = fmaf(-(sum == 0.0f ? 0.0f : pi[j] / sum), d, v[j]);
         }
-        sum = lanes_sum<L>(sum);
+        if (active) store_some<N>(out + e, a.experts - e, v);
+    };
+    if (SPREAD) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) dx[j] = fmaf(-(empty ? 0.0f : dx[j] / sum), d, s_dx[slot][first + j]);
+        for (uint32_t i = 0; i < S; ++i) write(i, p[i]);
     } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) dx[j] = s_dx[slot][first + j];
+        for (uint32_t i = 0; i < steps; ++i) write(i, nullptr);
     }
-    if (active && real) store_some<V>(static_cast<T*>(a.dscores) + row * a.dscores_stride + first, real, dx);
 }
 
 template <int ELEM, int L, int V>
@@ -459,11 +488,15 @@ hipError_t route_shape(const RouteArgs& a, hipStream_t stream) {
     return e;
 }
 
-template <int ELEM, int L, int V>
-hipError_t grad_shape(const RouteGradArgs& a, hipStream_t stream) {
-    constexpr uint32_t rows = kRouteWaves * kWave / L;
+template <int ELEM, int L, bool SPREAD>
+hipError_t grad_lanes(const RouteGradArgs& a, hipStream_t stream) {
+    constexpr uint32_t step = L * (16 / sizeof(typename Elem<ELEM>::T));
+    const size_t row_lds = (a.experts + step - 1) / step * step * sizeof(float);
+    uint32_t waves = kRouteWaves;
+    while (waves > 1 && waves * (kWave / L) * row_lds > kGradLds) waves /= 2;
+    const uint32_t rows = waves * kWave / L;
     timing_before(stream, RS_KERNEL_ROUTE_GRAD);
-    route_grad_kernel<ELEM, L, V><<<many_blocks((a.rows + rows - 1) / rows), kRouteWaves * kWave, 0, stream>>>(a);
+    route_grad_kernel<ELEM, L, SPREAD><<<many_blocks((a.rows + rows - 1) / rows), waves * kWave, rows * row_lds, stream>>>(a);
     const hipError_t e = hipGetLastError();
     timing_after(stream);
     return e;
@@ -491,17 +524,19 @@ hipError_t route_elem(const RouteArgs& a, hipStream_t stream) {
     return route_lanes<ELEM, 64>(a, stream);
 }
 
-// The gradient has no list: lanes for the choices, and at most 8 experts each
-// up to 512 (32 lanes with 16 each: 30 us against 23 at 32768 rows of 512).
+// A lane for each choice; and where the scores are read, lanes enough that a
+// row's 16-byte vectors are at most 4 of f32 or 2 of 16 bits a lane, which its
+// registers hold.
 template <int ELEM>
 hipError_t grad_elem(const RouteGradArgs& a, hipStream_t stream) {
-    if (a.experts <= 128 && a.top_k <= 16) {
-        if (a.experts <= 64) return grad_shape<ELEM, 16, 4>(a, stream);
-        return grad_shape<ELEM, 16, 8>(a, stream);
+    if (!a.sigmoid && !a.renormalize) {
+        if (a.top_k <= 16 && a.experts <= 128) return grad_lanes<ELEM, 16, true>(a, stream);
+        if (a.top_k <= 32 && a.experts <= 256) return grad_lanes<ELEM, 32, true>(a, stream);
+        return grad_lanes<ELEM, 64, true>(a, stream);
     }
-    if (a.experts <= 256 && a.top_k <= 32) return grad_shape<ELEM, 32, 8>(a, stream);
-    if (a.experts <= 512) return grad_shape<ELEM, 64, 8>(a, stream);
-    return grad_shape<ELEM, 64, 16>(a, stream);
+    if (a.top_k <= 16) return grad_lanes<ELEM, 16, false>(a, stream);
+    if (a.top_k <= 32) return grad_lanes<ELEM, 32, false>(a, stream);
+    return grad_lanes<ELEM, 64, false>(a, stream);
 }
 
 }  // namespace

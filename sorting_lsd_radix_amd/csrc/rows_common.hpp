@@ -47,14 +47,51 @@ __device__ __forceinline__ float value_of_order32(uint32_t o) {
     return o == 1u ? __builtin_nanf("") : __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o);
 }
 
+// Vectors of BYTES (a power of two up to 16) that may start on any element (2
+// bytes, the smallest).  Named types, because copies by memcpy in two branches
+// (whole and by element) are merged into loads and stores of single elements.
+template <int BYTES>
+struct AnyVec;
+template <>
+struct AnyVec<16> {
+    typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
+};
+template <>
+struct AnyVec<8> {
+    typedef uint32_t V __attribute__((ext_vector_type(2), aligned(2)));
+};
+template <>
+struct AnyVec<4> {
+    typedef uint32_t V __attribute__((aligned(2)));
+};
+template <>
+struct AnyVec<2> {
+    typedef uint16_t V;
+};
+
+template <int V, class T>
+struct SomeVec {
+    static constexpr int kBytes = V * sizeof(T) < 16 ? V * sizeof(T) : 16;
+    static constexpr int kParts = V * sizeof(T) / kBytes;
+    static constexpr int kEach = V / kParts;
+    using Part = typename AnyVec<kBytes>::V;
+    struct Elems { T v[kEach]; };
+};
+
 // V consecutive elements at `at`, of which the first `n` exist; `fill` for the others.
 template <int V, class T>
 __device__ __forceinline__ void load_some(const T* at, uint32_t n, float fill, float (&x)[V]) {
+    using S = SomeVec<V, T>;
     if (n >= V) {
-        struct { T v[V]; } r;
-        __builtin_memcpy(&r, at, sizeof(r));   // no alignment beyond the element's
+        typename S::Part r[S::kParts];
 #pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = static_cast<float>(r.v[j]);
+        for (int p = 0; p < S::kParts; ++p) r[p] = *reinterpret_cast<const typename S::Part*>(at + p * S::kEach);
+#pragma unroll
+        for (int p = 0; p < S::kParts; ++p) {
+            const auto e = __builtin_bit_cast(typename S::Elems, r[p]);
+#pragma unroll
+            for (int j = 0; j < S::kEach; ++j) x[p * S::kEach + j] = static_cast<float>(e.v[j]);
+        }
     } else {
 #pragma unroll
         for (uint32_t j = 0; j < V; ++j) x[j] = j < n ? static_cast<float>(at[j]) : fill;
@@ -63,15 +100,19 @@ __device__ __forceinline__ void load_some(const T* at, uint32_t n, float fill, f
 
 template <int V, class T>
 __device__ __forceinline__ void store_some(T* at, uint32_t n, const float (&x)[V]) {
-    struct { T v[V]; } r;
-#pragma unroll
-    for (int j = 0; j < V; ++j) r.v[j] = static_cast<T>(x[j]);
+    using S = SomeVec<V, T>;
     if (n >= V) {
-        __builtin_memcpy(at, &r, sizeof(r));
+#pragma unroll
+        for (int p = 0; p < S::kParts; ++p) {
+            typename S::Elems e;
+#pragma unroll
+            for (int j = 0; j < S::kEach; ++j) e.v[j] = static_cast<T>(x[p * S::kEach + j]);
+            *reinterpret_cast<typename S::Part*>(at + p * S::kEach) = __builtin_bit_cast(typename S::Part, e);
+        }
     } else {
 #pragma unroll
         for (uint32_t j = 0; j < V; ++j)
-            if (j < n) at[j] = r.v[j];
+            if (j < n) at[j] = static_cast<T>(x[j]);
     }
 }
 
