@@ -349,6 +349,14 @@ typedef enum rs_score_fn {
 #define RS_MAX_TOP_K 64       /* experts a row chooses, alternatives of a row */
 
 /*
+ * rs_group_choices and rs_token_logprobs need no temp for some sizes: their
+ * size query then gives RS_NO_TEMP bytes, and the call takes any non-null,
+ * 16-byte aligned d_temp that overlaps none of its buffers and does not touch
+ * it.
+ */
+#define RS_NO_TEMP 16
+
+/*
  * Routing: the top_k experts of every row of scores [rows, experts] and their
  * weights.  p = the score function of the row (softmax over all its experts).
  * An expert is chosen by s = p + bias[e], computed in 64 bits, or without a

@@ -25,7 +25,7 @@ __all__ = [
     "rs_sort_two_keys_u32", "rs_digit_counts", "rs_compact_positive_f32",
     "rs_compact_positive_f32_noalloc", "rs_exclusive_scan_u32", "rs_inclusive_scan_u32",
     "rs_select", "rs_partition", "RS_OP_LT", "RS_OP_LE", "RS_OP_GT", "RS_OP_GE", "RS_OP_EQ",
-    "RS_OP_NE", "RS_ELEM_F32", "RS_ELEM_F16", "RS_ELEM_BF16", "RS_SCORE_SOFTMAX",
+    "RS_OP_NE", "RS_NO_TEMP", "RS_ELEM_F32", "RS_ELEM_F16", "RS_ELEM_BF16", "RS_SCORE_SOFTMAX",
     "RS_SCORE_SIGMOID", "rs_route_topk", "rs_route_topk_grad", "rs_group_choices",
     "rs_token_logprobs", "rs_token_logprobs_grad", "route_topk", "route_topk_grad",
     "group_choices", "token_logprobs", "token_logprobs_grad", "TokenLogprobs", "rs_bitonic_tile", "rs_status_string", "rs_timing_enable", "rs_timing_collect",
@@ -68,6 +68,7 @@ KERNEL_NAMES = {0: "upsweep", 1: "onesweep", 2: "sort_init", 3: "compact_init",
                 14: "route", 15: "route_grad", 16: "group_count", 17: "group_scan",
                 18: "group_place", 19: "logprobs", 20: "logprobs_join", 21: "logprobs_grad"}
 
+RS_NO_TEMP = 16
 RS_ELEM_F32, RS_ELEM_F16, RS_ELEM_BF16 = range(3)
 RS_SCORE_SOFTMAX, RS_SCORE_SIGMOID = range(2)
 _SCORES = {"softmax": RS_SCORE_SOFTMAX, "sigmoid": RS_SCORE_SIGMOID}
@@ -690,8 +691,19 @@ def _run_on(index, stream, call):
         return call(_torch._C._cuda_getCurrentRawStream(index))
 
 
+# A size query that answers RS_NO_TEMP bytes or less says that the call does not touch its temp:
+# it then gets this address, which no allocation has.
+_NO_TEMP_ADDRESS = RS_NO_TEMP
+
+
 def _temp_arg(temp, size, device):
-    return _torch.empty(size.value, dtype=_torch.uint8, device=device) if temp is None else temp
+    """(tensor to keep until the call, its address, its size) of a call's temp."""
+    if temp is not None:
+        return temp, temp.data_ptr(), ctypes.c_size_t(temp.numel() * temp.element_size())
+    if size.value <= RS_NO_TEMP:
+        return None, _NO_TEMP_ADDRESS, size
+    temp = _torch.empty(size.value, dtype=_torch.uint8, device=device)
+    return temp, temp.data_ptr(), size
 
 
 def route_topk(scores, top_k, bias=None, score="softmax", groups=1, top_groups=1, group_best=1,
@@ -776,11 +788,10 @@ def group_choices(ids, experts, align=1, temp=None, stream=None):
         place = torch.empty(shape, dtype=i32, device=dev)
         starts = torch.empty(experts + 1, dtype=i32, device=dev)
         counts = torch.empty(experts, dtype=i32, device=dev)
-        work = _temp_arg(temp, size, dev)
-        have = ctypes.c_size_t(work.numel())
+        _keep, work, have = _temp_arg(temp, size, dev)
         _call("rs_group_choices", lib.rs_group_choices(
             at, n, experts, align, order.data_ptr(), place.data_ptr(), starts.data_ptr(),
-            counts.data_ptr(), work.data_ptr(), ctypes.byref(have), on))
+            counts.data_ptr(), work, ctypes.byref(have), on))
         return order, place, starts, counts
 
     return _run_on(index, stream, call)
@@ -826,12 +837,11 @@ def token_logprobs(logits, targets=None, top_k=0, scale=1.0, temp=None, stream=N
         if top_k:
             top_ids = torch.empty(rows, top_k, dtype=i32, device=dev)
             top_logprobs = torch.empty(rows, top_k, dtype=f32, device=dev)
-        work = _temp_arg(temp, size, dev)
-        have = ctypes.c_size_t(work.numel())
+        _keep, work, have = _temp_arg(temp, size, dev)
         _call("rs_token_logprobs", lib.rs_token_logprobs(
             et, logits.data_ptr(), stride, targets, rows, vocab, scale, top_k, stats.data_ptr(),
             lse.data_ptr(), entropy.data_ptr(), _ptr(logprob), _ptr(rank), _ptr(top_ids),
-            _ptr(top_logprobs), work.data_ptr(), ctypes.byref(have), on))
+            _ptr(top_logprobs), work, ctypes.byref(have), on))
         return TokenLogprobs(logprob, entropy, lse, rank, stats, top_ids, top_logprobs)
 
     return _run_on(index, stream, call)

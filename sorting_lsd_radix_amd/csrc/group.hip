@@ -26,14 +26,13 @@ constexpr int kGroupWaves = kGroupBlock / kWave;
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr uint32_t kShortSum = 1u << 15;
 
-// Choices of a thread.  One tile up to 16384 choices; above, tiles small
-// enough to fill the chip (256 CUs) but no smaller than 1024.
+// Choices of a thread.  One tile up to 4096 choices (16384 in one tile: 22 us,
+// in 16 tiles 11 in two launches); above, tiles of 1024, which fill the chip
+// soonest, and from 2^18 on of 4096 (2^20 in tiles of 16384: 27 us against 19).
 int group_items(uint64_t n) {
-    if (n <= 1024) return 1;
-    if (n <= 4096) return 4;
-    if (n <= 16384) return 16;
-    if (n <= (uint64_t{1} << 18)) return 1;
-    return n <= (uint64_t{1} << 22) ? 4 : 16;
+    if (n <= kGroupBlock) return 1;
+    if (n <= 4 * kGroupBlock) return 4;
+    return n <= (uint64_t{1} << 18) ? 1 : 4;
 }
 
 uint32_t group_tiles(uint64_t n) {
@@ -61,40 +60,51 @@ __global__ __launch_bounds__(kGroupBlock) void group_count_kernel(GroupArgs a, u
     if (tid < a.experts) tile_counts[static_cast<uint64_t>(blockIdx.x) * a.experts + tid] = s_count[tid];
 }
 
-// Block b, experts 64 b .. : tile_counts become the choices of earlier tiles,
-// totals[e] those of all.  Wave w takes a run of tiles: sums it, then, with the
-// sums of earlier runs, writes its offsets.
+// Block b, experts 16 b .. : tile_counts become the choices of earlier tiles,
+// totals[e] those of all.  Thread (r, x) takes run r of 64 of the tiles for
+// expert 16 b + x: sums it, then, with the sums of earlier runs, writes its
+// offsets, eight loads in flight.
+constexpr uint32_t kScanExperts = 16;
+constexpr uint32_t kScanRuns = kGroupBlock / kScanExperts;
+
 __global__ __launch_bounds__(kGroupBlock) void group_scan_kernel(uint32_t experts, uint32_t tiles,
                                                                  uint32_t* __restrict__ tile_counts,
                                                                  uint32_t* __restrict__ totals) {
-    __shared__ uint32_t s_sum[kGroupWaves][kWave];
-    const uint32_t wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
-    const uint32_t e = blockIdx.x * kWave + lane;
+    __shared__ uint32_t s_sum[kScanRuns][kScanExperts];
+    const uint32_t r = threadIdx.x / kScanExperts, x = threadIdx.x % kScanExperts;
+    const uint32_t e = blockIdx.x * kScanExperts + x;
     const bool real = e < experts;
-    const uint32_t run = (tiles + kGroupWaves - 1) / kGroupWaves;
-    const uint32_t begin = wave * run < tiles ? wave * run : tiles;
+    const uint32_t run = (tiles + kScanRuns - 1) / kScanRuns;
+    const uint32_t begin = r * run < tiles ? r * run : tiles;
     const uint32_t end = begin + run < tiles ? begin + run : tiles;
     uint32_t* col = tile_counts + (real ? e : 0u);
+    uint32_t c[8];
+    auto load = [&](uint32_t t0) {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) c[j] = col[static_cast<uint64_t>(t0 + j < end ? t0 + j : t0) * experts];
+    };
     uint32_t sum = 0;
-#pragma unroll 8
-    for (uint32_t t = begin; t < end; ++t) sum += real ? col[static_cast<uint64_t>(t) * experts] : 0u;
-    s_sum[wave][lane] = sum;
+    for (uint32_t t0 = begin; t0 < end; t0 += 8) {
+        load(t0);
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) sum += t0 + j < end ? c[j] : 0u;
+    }
+    s_sum[r][x] = sum;
     __syncthreads();
     uint32_t before = 0, all = 0;
-    for (uint32_t w = 0; w < kGroupWaves; ++w) {
-        const uint32_t s = s_sum[w][lane];
-        before += w < wave ? s : 0u;
+    for (uint32_t i = 0; i < kScanRuns; ++i) {
+        const uint32_t s = s_sum[i][x];
+        before += i < r ? s : 0u;
         all += s;
     }
     if (!real) return;
-    if (wave == 0) totals[e] = all;
-    for (uint32_t t0 = begin; t0 < end; t0 += 8) {   // eight loads at a time, ahead of their stores
-        uint32_t c[8];
-#pragma unroll
-        for (uint32_t j = 0; j < 8; ++j) c[j] = t0 + j < end ? col[static_cast<uint64_t>(t0 + j) * experts] : 0u;
+    if (r == 0) totals[e] = all;
+    for (uint32_t t0 = begin; t0 < end; t0 += 8) {
+        load(t0);
 #pragma unroll
         for (uint32_t j = 0; j < 8; ++j) {
-            if (t0 + j < end) col[static_cast<uint64_t>(t0 + j) * experts] = before;
+            if (t0 + j >= end) break;
+            col[static_cast<uint64_t>(t0 + j) * experts] = before;
             before += c[j];
         }
     }
@@ -136,11 +146,20 @@ __global__ __launch_bounds__(kGroupBlock) void group_place_kernel(GroupArgs a, u
         const uint32_t x = c * kWave + lane;
         uint32_t before = 0, all = 0;
         if (q < slices && x < a.experts) {
-#pragma unroll 8
-            for (uint32_t t = q; t < gridDim.x; t += slices) {
-                const uint32_t n = tile_counts[static_cast<uint64_t>(t) * a.experts + x];
-                all += n;
-                before += t < tile ? n : 0u;
+            constexpr uint32_t kAhead = 8;   // loads in flight: of the last tile again behind the end
+            for (uint32_t t0 = q; t0 < gridDim.x; t0 += kAhead * slices) {
+                uint32_t n[kAhead];
+#pragma unroll
+                for (uint32_t j = 0; j < kAhead; ++j) {
+                    const uint32_t t = t0 + j * slices;
+                    n[j] = tile_counts[static_cast<uint64_t>(t < gridDim.x ? t : gridDim.x - 1) * a.experts + x];
+                }
+#pragma unroll
+                for (uint32_t j = 0; j < kAhead; ++j) {
+                    const uint32_t t = t0 + j * slices;
+                    all += t < gridDim.x ? n[j] : 0u;
+                    before += t < tile ? n[j] : 0u;
+                }
             }
         }
         s_part[0][tid] = before;
@@ -240,7 +259,7 @@ hipError_t group_items_of(const GroupArgs& a, uint32_t tiles, uint32_t* temp, hi
     uint32_t* totals = temp + counts;
     if (tiles > 1 && counts > kShortSum) {
         timing_before(stream, RS_KERNEL_GROUP_SCAN);
-        group_scan_kernel<<<dim3((a.experts + kWave - 1) / kWave), kGroupBlock, 0, stream>>>(a.experts, tiles, temp, totals);
+        group_scan_kernel<<<dim3((a.experts + kScanExperts - 1) / kScanExperts), kGroupBlock, 0, stream>>>(a.experts, tiles, temp, totals);
         e = hipGetLastError();
         timing_after(stream);
         if (e != hipSuccess) return e;
@@ -259,17 +278,14 @@ hipError_t group_items_of(const GroupArgs& a, uint32_t tiles, uint32_t* temp, hi
 
 size_t group_temp_bytes(uint64_t n, uint32_t experts) {
     const uint64_t tiles = group_tiles(n);
-    return tiles > 1 ? (tiles + 1) * experts * sizeof(uint32_t) : 16;
+    return tiles > 1 ? (tiles + 1) * experts * sizeof(uint32_t) : RS_NO_TEMP;
 }
 
 hipError_t launch_group(const GroupArgs& a, void* temp, hipStream_t stream) {
     const uint32_t tiles = group_tiles(a.n);
     uint32_t* words = static_cast<uint32_t*>(temp);
-    switch (group_items(a.n)) {
-    case 1: return group_items_of<1>(a, tiles, words, stream);
-    case 4: return group_items_of<4>(a, tiles, words, stream);
-    default: return group_items_of<16>(a, tiles, words, stream);
-    }
+    return group_items(a.n) == 1 ? group_items_of<1>(a, tiles, words, stream)
+                                 : group_items_of<4>(a, tiles, words, stream);
 }
 
 }  // namespace rs
