@@ -27,9 +27,13 @@ constexpr float kInf = __builtin_huge_valf();
 // powers of two: far below f32's range (sums reach 2^30 * 2^16), and near
 // enough that the rounding of d (16 * 2^-24) stays under a millionth.
 constexpr float kMaxShift = 16.0f;
-// Largest |r a|: above it (logits of some 1e30, as the lowest value of a type
-// that masks a whole row) x a - r a may overflow, and the sums are taken again.
-constexpr float kMaxReference = 1e30f;
+// Largest |r a|: c = -r a is off by up to 2^-24 of it, which has to stay a small
+// shift of the reference (an eighth).  Where a part's largest |x a| is over
+// kMaxLargest (logits of some 7e5 at scale 1, or the lowest value of a type that
+// masks a whole row), its sums are taken again with x - m formed first; below
+// that, what a thread past kMaxReference would add is below 2^-(2^20).
+constexpr float kMaxReference = 0x1p21f;
+constexpr float kMaxLargest = 0x1p20f;
 
 // Where a row's parts begin and end: multiples of 8 elements, so that no
 // 16-byte vector of the row is in two parts.
@@ -235,7 +239,7 @@ struct Running {
     float m = -kInf, c = 0.0f, s = 0.0f, t = 0.0f;
 
     // Called with a new largest m: moves the reference there, unless it is near
-    // enough, or so large (1e30) that x a + c could overflow (slow_sums then).
+    // enough, or too large for c (slow_sums then).
     __device__ __forceinline__ void reference(float a) {
         if (!(fabsf(fmaf(m, a, c)) <= kMaxShift) && fabsf(m * a) <= kMaxReference) {
             const float d = fmaxf(-m * a - c, -1000.0f);
@@ -273,7 +277,7 @@ struct Running {
     }
 };
 
-// Where |largest * a| > kMaxReference: the block's sums again, with x - m formed
+// Where |largest * a| > kMaxLargest: the block's sums again, with x - m formed
 // before the product.  m is finite.
 template <class T>
 __device__ __attribute__((noinline)) Sums slow_sums(const T* in, uint32_t n, float m, float a, Sums* s_sums) {
@@ -521,7 +525,7 @@ __global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LogprobsArgs p, Part
     __syncthreads();
     z = s_sums[0];
     for (uint32_t w = 1; w < kLpWaves; ++w) z = join(z, s_sums[w], a);
-    if (fabsf(z.m) < kInf && fabsf(z.m * a) > kMaxReference) {
+    if (fabsf(z.m) < kInf && fabsf(z.m * a) > kMaxLargest) {
         const uint32_t counted = z.ahead;
         z = slow_sums(in, n, z.m, a, s_sums);
         z.ahead = counted;
@@ -670,7 +674,7 @@ hipError_t grad_elem(const LogprobsGradArgs& p, hipStream_t stream) {
 
 size_t logprobs_temp_bytes(uint64_t rows, uint32_t vocab, uint32_t top_k) {
     const Parts parts = lp_parts(rows, vocab);
-    if (rows == 0 || parts.count == 1) return 16;
+    if (rows == 0 || parts.count == 1) return RS_NO_TEMP;
     return rows * parts.count * (sizeof(Sums) + 8 * static_cast<size_t>(top_k));
 }
 

@@ -317,3 +317,52 @@ def test_no_rows_and_refusals():
         rs.token_logprobs(x, t, top_k=51)
     with pytest.raises(rs.RsError):
         rs.token_logprobs(x, t, scale=0.0)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -60, 1e-4, 300.0, 1e6, 2.0 ** 60])
+@pytest.mark.parametrize("vocab", [50, 9000])
+def test_extreme_scales(scale, vocab):
+    print("logprobs scale %g vocab %d" % (scale, vocab), flush=True)
+    g = np.random.default_rng(15)
+    x = g.standard_normal((5, vocab)) * 3
+    x[1] += 100.0
+    x[2] -= 1000.0
+    x[3, ::3] = -np.inf
+    check(x, [0, 1, 2, 4, vocab - 1], 5, "f32", scale=scale, grad=False)
+
+
+@pytest.mark.parametrize("far", [1e4, 7.2e5, 7.268e5, 7.27e5, 1.4e6, 1.5e6, 1e9, 1e35])
+def test_logits_far_from_zero(far):
+    """Offsets around every limit at which a sum's reference is taken another way (2^20 and 2^21
+    in powers of two are 7.27e5 and 1.45e6); a quarter of the logits lie just past the limit."""
+    print("logprobs around %g" % far, flush=True)
+    g = np.random.default_rng(16)
+    step = np.float64(np.spacing(np.float32(far)))
+    x = np.round(g.standard_normal((6, 20000)) * max(3.0, 2 * step) / step) * step
+    x[0::2] += far
+    x[1::2] -= far
+    x[4, ::4] -= far / 2
+    x[5, ::4] -= far
+    check(x, [3, 30, 300, 3000, 5, 8], 4, "f32", grad=False)
+
+
+def test_one_long_row():
+    vocab = (1 << 28) + 5
+    print("logprobs 2 x (2^28 + 5)", flush=True)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(9)
+    x = torch.randn(2, vocab, generator=g, device=DEV)
+    x[0, -1] = 9.0
+    x[1, 1 << 27] = 9.0
+    t = ids32([vocab - 1, 1 << 27])
+    got = rs.token_logprobs(x, t, top_k=3)
+    for r in range(2):
+        y = x[r].double()
+        lse = torch.logsumexp(y, 0)
+        # 2^28 / 64 / 256 terms a thread, and the bound of rows_reference.logprobs at W = 28
+        es = ref.U * (vocab / 64 / 256 + 8 + 100 + 3 * (28 + 34))
+        assert abs(float(got.lse[r]) - float(lse)) <= es + 4 * ref.U * (abs(float(lse)) + 30)
+        assert abs(float(got.logprob[r]) - float(9.0 - lse)) <= es + 4 * ref.U * (float(lse) + 60)
+        assert int(got.rank[r]) == 0 and int(got.top_ids[r, 0]) == int(t[r])
+        assert got.top_ids[r].tolist() == torch.topk(y, 3).indices.tolist()
+        del y
