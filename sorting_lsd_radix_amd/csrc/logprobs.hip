@@ -374,17 +374,28 @@ __device__ __forceinline__ uint64_t best_of_part(const T* in, uint32_t n, uint32
         __syncthreads();
         for (uint32_t v = tid; v < vecs; v += kLpBlock) collect(v);
     } else {
+        // of 64 groups of four threads' bests while top_k is at most half of
+        // them (one sort in every wave), of all threads' above
         const uint32_t mine = order32(steps.best);
-        uint32_t list = wave_sort_desc(mine);
-#pragma unroll
-        for (uint32_t half = kLpWaves / 2; half > 0; half >>= 1) {
-            if (wave >= half && wave < 2 * half) s.max[wave][lane] = list;
+        uint32_t kth;
+        if (k <= kWave / 2) {
+            const uint32_t of_four = lanes_max<4>(mine);
+            if ((lane & 3) == 0) s.max[0][wave * (kWave / 4) + lane / 4] = of_four;
             __syncthreads();
-            if (wave < half) list = wave_merge_desc(list, s.max[wave + half][lane]);
+            kth = __shfl(wave_sort_desc(s.max[0][lane]), static_cast<int>(k - 1), kWave);
+        } else {
+            uint32_t list = wave_sort_desc(mine);
+#pragma unroll
+            for (uint32_t half = kLpWaves / 2; half > 0; half >>= 1) {
+                if (wave >= half && wave < 2 * half) s.max[wave][lane] = list;
+                __syncthreads();
+                if (wave < half) list = wave_merge_desc(list, s.max[wave + half][lane]);
+            }
+            if (wave == 0 && lane == k - 1) s.tau = list;
+            __syncthreads();
+            kth = s.tau;
         }
-        if (wave == 0 && lane == k - 1) s.tau = list;
-        __syncthreads();
-        tau = s.tau > lowest ? s.tau : lowest + 1;   // never the masked ones
+        tau = kth > lowest ? kth : lowest + 1;   // never the masked ones
         if (mine >= tau) {
             if (order32(steps.next) >= tau) {
                 s.flagged[atomicAdd(&s.flags, 1u)] = tid;
@@ -407,7 +418,16 @@ __device__ __forceinline__ uint64_t best_of_part(const T* in, uint32_t n, uint32
         return wave == 0 ? wave_sort_desc(lane < k ? s.top[lane] : uint64_t{0}) : 0;
     }
     uint64_t key = 0;
-    if (wave == 0) {
+    if (wave == 0 && count <= kWave) {
+        // each lane's candidate goes to the place of as many as are before it
+        const uint64_t own = lane < count ? s.cand[lane] : uint64_t{0};
+        uint32_t place = 0;
+#pragma unroll 8
+        for (uint32_t i = 0; i < count; ++i) place += s.cand[i] > own;
+        if (lane < count) s.top[place] = own;
+        wave_fence();
+        key = lane < count ? s.top[lane] : uint64_t{0};
+    } else if (wave == 0) {
         for (uint32_t i = 0; i < count; i += kWave) {
             const uint64_t next = wave_sort_desc(i + lane < count ? s.cand[i + lane] : uint64_t{0});
             key = i == 0 ? next : wave_merge_desc(key, next);
@@ -580,6 +600,7 @@ __global__ __launch_bounds__(kLpJoinWaves* kWave) void logprobs_join_kernel(Logp
     z = lanes_reduce(z, [&](const Sums& x, const Sums& y) { return join(x, y, a); });
     finish_row(p, row, z, x_target, target < p.vocab, key);
 }
+static_assert(kLpBlock == 4 * kWave, "a threshold of 64 groups of four threads");
 static_assert(kLpMaxParts <= kWave, "the joining wave has a lane for each part");
 
 // Block (part of a row, row): dx = e (c0 + c1 d) with e = 2^d, d = (x - m) a, plus
