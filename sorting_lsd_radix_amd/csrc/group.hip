@@ -14,6 +14,10 @@
 //    tiles itself, which is cheaper than a launch in between.
 //  * Above: a launch in between turns the counts of each expert into the
 //    tiles' offsets and a total.
+//
+// What bounds it: launches and dependent steps.  131072 choices of 256 experts
+// take 2.4 + 8.1 us (the choices and their order are 1.7 MB), 1.3 million of 1000
+// experts 4.4 + 6.3 + 16 us (15.7 MB, the order written in scattered words).
 #include "internal.hpp"
 #include "device_common.hpp"
 
@@ -24,7 +28,7 @@ namespace {
 constexpr int kGroupBlock = 1024;
 constexpr int kGroupWaves = kGroupBlock / kWave;
 constexpr uint32_t kNone = 0xFFFFFFFFu;
-constexpr uint32_t kShortSum = 1u << 15;
+constexpr uint32_t kShortSum = 1u << 15;   // at 2^17 the same times, but more reads of every tile
 
 // Choices of a thread.  One tile up to 4096 choices (16384 in one tile: 22 us,
 // in 16 tiles 11 in two launches); above, tiles of 1024, which fill the chip

@@ -13,6 +13,12 @@
 // unless two scores at the border are too near (then the row's s are all taken
 // in 64 bits).  64-bit arithmetic for every expert cost 45 us of 32768 rows of
 // 512 experts' sigmoids with a bias, against 30 without.
+//
+// What bounds it: 32768 rows of 512 f32 (67 MB), sigmoid with a bias, take 25-28
+// us, 2.4-2.7 TB/s, with the vector units busy in 0.92 of the compute units'
+// cycles (790 instructions for the two rows of a wave); 16384 rows of 256 with
+// groups 16-18 us, where a wave's dependent steps count as much.  Below some
+// 4096 rows the launch is all.
 #include "internal.hpp"
 #include "rows_common.hpp"
 
@@ -392,8 +398,8 @@ constexpr size_t kGradLds = 32768;   // a block's: five fit a CU
 // the row's lanes write it in 16-byte vectors next to each other, with the
 // softmax's term that reaches every expert where the weights are not
 // renormalised.  As many rows to a wave as top_k allows: the time of a wave is that
-// of its dependent reads, so that 32768 rows of 512 take 23 us at one row a
-// wave.
+// of its dependent reads (32768 rows of 512 f32, renormalised softmax: 14.3 us
+// at four rows a wave, 4.7 TB/s written; 23 at one).
 template <int ELEM, int L, bool SPREAD>
 __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(RouteGradArgs a) {
     using T = typename Elem<ELEM>::T;
