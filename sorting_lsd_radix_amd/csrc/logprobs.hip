@@ -139,6 +139,44 @@ struct SelectShared {
     uint64_t top[kWave];
 };
 
+// The first `need` of a part's elements with a pattern, in index order, into
+// s.top[at ..]; fewer if the part has fewer.  Returns how many (everywhere).
+template <class T>
+__device__ uint32_t first_of_pattern(const T* in, uint32_t n, uint32_t base, uint32_t pattern, uint32_t need, uint32_t at,
+                                     SelectShared& s) {
+    constexpr uint32_t N = RowVec<T>::N;
+    const uint32_t tid = threadIdx.x, wave = tid / kWave, lane = tid & (kWave - 1);
+    const uint32_t vecs = (n + N - 1) / N;
+    uint32_t taken = 0;
+    for (uint32_t v0 = 0, it = 0; v0 < vecs && taken < need; v0 += kLpBlock, ++it) {
+        const uint32_t v = v0 + tid;
+        uint32_t mine = 0;
+        if (v < vecs) {
+            float x[N];
+            load_vec(in, v, n, x);
+            for (uint32_t j = 0; j < N; ++j)
+                if (v * N + j < n && order32(x[j]) == pattern) mine |= 1u << j;
+        }
+        const uint32_t own = __popc(mine);
+        const uint32_t incl = wave_inclusive_sum(own);
+        if (lane == kWave - 1) s.wave[it & 1][wave] = incl;
+        __syncthreads();
+        uint32_t rank = taken + incl - own;
+        for (uint32_t w = 0; w < kLpWaves; ++w) {
+            const uint32_t c = s.wave[it & 1][w];
+            if (w < wave) rank += c;
+            taken += c;
+        }
+        for (uint32_t j = 0; j < N; ++j)
+            if ((mine >> j) & 1u) {
+                if (rank < need) s.top[at + rank] = list_key(pattern, base + v * N + j);
+                ++rank;
+            }
+    }
+    __syncthreads();
+    return taken < need ? taken : need;
+}
+
 // The first k (at most n) of a row part's n elements in the row's order,
 // whatever they are, by a radix select on the order patterns: four counts of
 // 8-bit digits find the k-th pattern, then the patterns above it are
@@ -158,8 +196,18 @@ __device__ void radix_select(const T* in, uint32_t n, uint32_t base, uint32_t k,
             load_vec(in, v, n, x);
             for (uint32_t j = 0; j < N; ++j) {
                 const uint32_t o = order32(x[j]);
-                if (v * N + j < n && (shift == 24 || ((o ^ prefix) >> (shift + 8)) == 0))
-                    atomicAdd(&s.bins[(o >> shift) & 255u], 1u);
+                const uint32_t digit = (o >> shift) & 255u;
+                const bool counts = v * N + j < n && (shift == 24 || ((o ^ prefix) >> (shift + 8)) == 0);
+                // ties bring rows here: lanes with one digit count it together
+                const uint64_t all = ballot(counts);
+                if (all == 0) continue;
+                const uint32_t leader = static_cast<uint32_t>(__builtin_ctzll(all));
+                const uint32_t theirs = __shfl(digit, static_cast<int>(leader), kWave);
+                if (ballot(counts && digit == theirs) == all) {
+                    if (lane == leader) atomicAdd(&s.bins[digit], static_cast<uint32_t>(__builtin_popcountll(all)));
+                } else if (counts) {
+                    atomicAdd(&s.bins[digit], 1u);
+                }
             }
         }
         __syncthreads();
@@ -180,41 +228,17 @@ __device__ void radix_select(const T* in, uint32_t n, uint32_t base, uint32_t k,
     }
     if (tid == 0) s.found = 0;
     __syncthreads();
-    for (uint32_t v = tid; v < vecs; v += kLpBlock) {
-        float x[N];
-        load_vec(in, v, n, x);
-        for (uint32_t j = 0; j < N; ++j) {
-            const uint32_t o = order32(x[j]);
-            if (v * N + j < n && o > prefix) s.top[atomicAdd(&s.found, 1u)] = list_key(o, base + v * N + j);
-        }
-    }
-    uint32_t taken = 0;   // equal ones so far, in the order of the row
-    for (uint32_t v0 = 0, it = 0; v0 < vecs && taken < need; v0 += kLpBlock, ++it) {
-        const uint32_t v = v0 + tid;
-        uint32_t mine = 0;
-        if (v < vecs) {
+    if (need < k) {
+        for (uint32_t v = tid; v < vecs; v += kLpBlock) {
             float x[N];
             load_vec(in, v, n, x);
-            for (uint32_t j = 0; j < N; ++j)
-                if (v * N + j < n && order32(x[j]) == prefix) mine |= 1u << j;
-        }
-        const uint32_t own = __popc(mine);
-        const uint32_t incl = wave_inclusive_sum(own);
-        if (lane == kWave - 1) s.wave[it & 1][wave] = incl;
-        __syncthreads();
-        uint32_t at = taken + incl - own;
-        for (uint32_t w = 0; w < kLpWaves; ++w) {
-            const uint32_t c = s.wave[it & 1][w];
-            if (w < wave) at += c;
-            taken += c;
-        }
-        for (uint32_t j = 0; j < N; ++j)
-            if ((mine >> j) & 1u) {
-                if (at < need) s.top[k - need + at] = list_key(prefix, base + v * N + j);
-                ++at;
+            for (uint32_t j = 0; j < N; ++j) {
+                const uint32_t o = order32(x[j]);
+                if (v * N + j < n && o > prefix) s.top[atomicAdd(&s.found, 1u)] = list_key(o, base + v * N + j);
             }
+        }
     }
-    __syncthreads();
+    first_of_pattern(in, n, base, prefix, need, k - need, s);
 }
 
 // Writes a row's results.  Called by one wave; lane i has the i-th list key.
@@ -356,8 +380,8 @@ struct Steps {
 // whole shares in every case cost 20 us of 123 at 2048 rows of 131072 bf16
 // logits.)  What reaches the threshold is collected and sorted by (value,
 // index).  Where more is collected than the list takes (ties, or the best
-// logits crowded in few shares), or where masks leave fewer than k, the radix
-// select reads the part instead.
+// logits crowded in few shares), the radix select reads the part instead; where
+// masks leave fewer than k, the first masked ones follow.
 template <class T>
 __device__ __forceinline__ uint64_t best_of_part(const T* in, uint32_t n, uint32_t base, uint32_t k,
                                                  const Steps& steps, uint32_t full_steps, SelectShared& s) {
@@ -425,7 +449,12 @@ __device__ __forceinline__ uint64_t best_of_part(const T* in, uint32_t n, uint32
     __syncthreads();
     const uint32_t count = s.count;
     if (count > kLpCandidates || count < k) {
-        radix_select(in, n, base, k, s);
+        // fewer than k are not masked: those, and the first masked ones (unless
+        // NaN has to fill up too)
+        const bool few = count < k && first_of_pattern(in, n, base, lowest, k - count, count, s) == k - count;
+        if (!few) radix_select(in, n, base, k, s);
+        if (few && tid < count) s.top[tid] = s.cand[tid];
+        wave_fence();   // count < k: wave 0 wrote them
         return wave == 0 ? wave_sort_desc(lane < k ? s.top[lane] : uint64_t{0}) : 0;
     }
     uint64_t key = 0;
@@ -457,8 +486,10 @@ __device__ __forceinline__ uint64_t best_of_part(const T* in, uint32_t n, uint32
 // target those above it, in front of it those above the next value below it,
 // which are the ones not below it; the vector that holds the target is
 // counted as behind it and its equal logits in front of it added.
+// (96 scalar registers, of which the selects would take more, let 8 waves run on
+// a SIMD; the vector registers do.)
 template <int ELEM, bool TOP, bool STREAM>
-__global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LogprobsArgs p, Parts parts, Sums* __restrict__ sums,
+__global__ __launch_bounds__(kLpBlock) __attribute__((amdgpu_num_sgpr(96))) void logprobs_kernel(LogprobsArgs p, Parts parts, Sums* __restrict__ sums,
                                                             uint64_t* __restrict__ lists) {
     using T = typename Elem<ELEM>::T;
     constexpr uint32_t N = RowVec<T>::N;
