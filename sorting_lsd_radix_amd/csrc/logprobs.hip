@@ -379,9 +379,10 @@ struct Steps {
 // reaches the threshold too, a whole wave reads the thread's share.  (Reading
 // whole shares in every case cost 20 us of 123 at 2048 rows of 131072 bf16
 // logits.)  What reaches the threshold is collected and sorted by (value,
-// index).  Where more is collected than the list takes (ties, or the best
-// logits crowded in few shares), the radix select reads the part instead; where
-// masks leave fewer than k, the first masked ones follow.
+// index).  Where more is collected than the list takes, ties as a rule, only
+// what is above the threshold is collected, and the first ties by index follow
+// (where masks leave fewer than k, the first masked ones); where that is too much
+// too (the best logits crowded in few shares), the radix select reads the part.
 template <class T>
 __device__ __forceinline__ uint64_t best_of_part(const T* in, uint32_t n, uint32_t base, uint32_t k,
                                                  const Steps& steps, uint32_t full_steps, SelectShared& s) {
@@ -431,27 +432,36 @@ __device__ __forceinline__ uint64_t best_of_part(const T* in, uint32_t n, uint32
             kth = s.tau;
         }
         tau = kth > lowest ? kth : lowest + 1;   // never the masked ones
-        if (mine >= tau) {
-            if (order32(steps.next) >= tau) {
-                s.flagged[atomicAdd(&s.flags, 1u)] = tid;
-            } else {
-                const bool whole = steps.at < full_steps;
-                const uint32_t v = tid + kLpBlock * (whole ? steps.at * U : full_steps * U + steps.at - full_steps);
-                for (uint32_t u = 0; u < (whole ? U : 1); ++u) collect(v + u * kLpBlock);
+        for (int attempt = 0;; ++attempt) {
+            if (mine >= tau) {
+                if (order32(steps.next) >= tau) {
+                    s.flagged[atomicAdd(&s.flags, 1u)] = tid;
+                } else {
+                    const bool whole = steps.at < full_steps;
+                    const uint32_t v = tid + kLpBlock * (whole ? steps.at * U : full_steps * U + steps.at - full_steps);
+                    for (uint32_t u = 0; u < (whole ? U : 1); ++u) collect(v + u * kLpBlock);
+                }
             }
-        }
-        __syncthreads();
-        for (uint32_t i = wave; i < s.flags; i += kLpWaves) {
-            if (__hip_atomic_load(&s.count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) > kLpCandidates) break;
-            for (uint32_t v = s.flagged[i] + lane * kLpBlock; v < vecs; v += kWave * kLpBlock) collect(v);
+            __syncthreads();
+            for (uint32_t i = wave; i < s.flags; i += kLpWaves) {
+                if (__hip_atomic_load(&s.count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) > kLpCandidates) break;
+                for (uint32_t v = s.flagged[i] + lane * kLpBlock; v < vecs; v += kWave * kLpBlock) collect(v);
+            }
+            __syncthreads();
+            if (s.count <= kLpCandidates || attempt == 1) break;
+            __syncthreads();   // too many reach the threshold: mostly ties, so only what is above it
+            if (tid == 0) s.flags = s.count = 0;
+            ++tau;
+            __syncthreads();
         }
     }
     __syncthreads();
     const uint32_t count = s.count;
     if (count > kLpCandidates || count < k) {
-        // fewer than k are not masked: those, and the first masked ones (unless
-        // NaN has to fill up too)
-        const bool few = count < k && first_of_pattern(in, n, base, lowest, k - count, count, s) == k - count;
+        // fewer than k reach the threshold where it was raised over ties, or stood
+        // above the masked ones: those, and then the first of the ties or masked
+        // ones (unless NaN has to fill up too)
+        const bool few = count < k && first_of_pattern(in, n, base, tau - 1, k - count, count, s) == k - count;
         if (!few) radix_select(in, n, base, k, s);
         if (few && tid < count) s.top[tid] = s.cand[tid];
         wave_fence();   // count < k: wave 0 wrote them
@@ -486,8 +496,8 @@ __device__ __forceinline__ uint64_t best_of_part(const T* in, uint32_t n, uint32
 // target those above it, in front of it those above the next value below it,
 // which are the ones not below it; the vector that holds the target is
 // counted as behind it and its equal logits in front of it added.
-// (96 scalar registers, of which the selects would take more, let 8 waves run on
-// a SIMD; the vector registers do.)
+// (The selects would take more than 96 scalar registers, which let 8 waves run
+// on a SIMD in f32; in 16 bits the vector registers, 70, let 7.)
 template <int ELEM, bool TOP, bool STREAM>
 __global__ __launch_bounds__(kLpBlock) __attribute__((amdgpu_num_sgpr(96))) void logprobs_kernel(LogprobsArgs p, Parts parts, Sums* __restrict__ sums,
                                                             uint64_t* __restrict__ lists) {
