@@ -451,7 +451,10 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(RouteGra
 
     const float d = lanes_sum<L>(mine ? dw * w : 0.0f);
     float part = w * (a.renormalize ? dw - d / a.scale : dw);
-    if (a.sigmoid) part *= 1.0f / (1.0f + expf(score));
+    if (a.sigmoid) {   // 1 - p, from the exponential that does not overflow
+        const float e = expf(-fabsf(score));
+        part *= (score > 0.0f ? e : 1.0f) / (1.0f + e);
+    }
     float term = 0.0f;
     for (uint32_t r = 0; r < a.top_k; ++r) {
         const uint32_t e = __shfl(id, static_cast<int>(lane - sub + r), kWave);

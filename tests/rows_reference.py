@@ -81,7 +81,8 @@ def route_grad(x, ids, dw, score="softmax", renormalize=True, scale=1.0):
     if score == "sigmoid":
         q = 1.0 / (1.0 + np.exp(np.where(np.isnan(x), 0, x)))[n, ids]
         np.add.at(dx, (n, ids), part * q)
-        np.add.at(bound, (n, ids), off * q)
+        # 1 - p below f32's smallest normal number is a multiple of 2^-149, off by half of that
+        np.add.at(bound, (n, ids), off * q + 2.0 ** -149 * np.abs(part))
     else:
         if not renormalize:
             # p: x - m is rounded once (|x - m| U in the exponent), exp 2 U, the sum of the row

@@ -366,3 +366,22 @@ def test_one_long_row():
         assert int(got.rank[r]) == 0 and int(got.top_ids[r, 0]) == int(t[r])
         assert got.top_ids[r].tolist() == torch.topk(y, 3).indices.tolist()
         del y
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_combinations(seed):
+    g = np.random.default_rng(2000 + seed)
+    vocab = int(np.exp(g.uniform(0, np.log(60000))))
+    rows = int(g.integers(1, max(2, min(60, 400000 // vocab))))
+    k = int(min(vocab, g.integers(0, 65)))
+    x = g.standard_normal((rows, vocab)) * (3.0, 0.5, 10.0)[seed % 3]
+    if seed % 4 == 0:
+        x = np.round(x)                             # ties, past any list of candidates
+    if seed % 5 == 0:
+        x[g.random(x.shape) < g.choice([0.5, 0.99, 0.9999])] = -np.inf
+    if seed % 7 == 0:
+        x[:, : vocab // 3] += 30.0                  # the best crowd in front
+    t = g.integers(-1, vocab, rows)
+    dtype = ("f32", "f16", "bf16")[seed % 3]
+    print("logprobs random", seed, rows, vocab, k, dtype, flush=True)
+    check(x, t if seed % 6 else None, k, dtype, scale=float(g.choice([1.0, 0.7, 1.5, 0.01])), pad=seed % 9, shift=seed % 5)

@@ -266,3 +266,41 @@ def test_wrapper_refusals():
             bad()
     with pytest.raises(rs.RsError):
         rs.route_topk(x, 9)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_extreme_biases(score):
+    """Biases near f32's ends, whose pair sums pass them, and infinite ones, with and without groups."""
+    g = np.random.default_rng(20)
+    x = g.standard_normal((30, 64))
+    for name, bias in (("low", np.where(np.arange(64) % 8 < 6, -3.4e38, 0.1)), ("all low", np.full(64, -3.4e38)),
+                       ("high", np.where(np.arange(64) % 16 < 4, 3.4e38, 0.0)), ("inf", np.where(np.arange(64) % 9 == 0, np.inf, 0.0)),
+                       ("-inf", np.where(np.arange(64) % 2 == 0, -np.inf, 0.0)), ("tiny", np.full(64, 1e-42)),
+                       ("cancelling", -ref.probabilities(x[:1], score)[0])):
+        for kw in (dict(), dict(groups=8, top_groups=3, group_best=2), dict(groups=4, top_groups=2)):
+            print("route bias", name, score, sorted(kw), flush=True)
+            check(x, 8, bias=bias, score=score, **kw)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_combinations(seed):
+    g = np.random.default_rng(1000 + seed)
+    groups = int(g.choice([1, 1, 2, 3, 4, 8, 16, 33, 64]))
+    size = int(g.integers(1, max(2, 1024 // groups + 1)))
+    experts = groups * size
+    top = int(g.integers(1, groups + 1))
+    best = int(g.integers(1, min(2, size) + 1))
+    k = int(g.integers(1, min(64, top * size) + 1))
+    rows = int(g.integers(1, 200))
+    kind = seed % 4
+    x = g.standard_normal((rows, experts)) * (3.0, 1.0, 0.3, 20.0)[kind]
+    if seed % 3 == 0:
+        x = np.round(x * 2) / 2                     # ties
+    if seed % 5 == 0:
+        x[g.random(x.shape) < 0.6] = -np.inf
+    kw = dict(score=("softmax", "sigmoid")[seed % 2], renormalize=bool(g.integers(2)), groups=groups, top_groups=top,
+              group_best=best, scale=float(g.choice([1.0, 0.5, 2.5])))
+    bias = None if g.integers(3) == 0 else np.round(g.standard_normal(experts) * 8) / 64 * g.integers(0, 2)
+    dtype = ("f32", "f16", "bf16")[seed % 3]
+    print("route random", seed, rows, experts, k, dtype, kw, bias is not None, flush=True)
+    check(x, k, dtype, pad=seed % 7, shift=seed % 5, bias=bias, **kw)
