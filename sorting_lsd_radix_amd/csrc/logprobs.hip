@@ -11,8 +11,8 @@
 //
 // What bounds it: at 2048 rows of 131072 bf16 logits with 8 alternatives the
 // vector units (about 10 instructions an element, exp2 among them, busy in all
-// of the compute units' cycles) as much as the memory: 537 MB in 100-106 us,
-// 5.1-5.4 TB/s, where a kernel that only reads the same rows takes 83; in f32
+// of the compute units' cycles) as much as the memory: 537 MB in 101-111 us,
+// 4.8-5.3 TB/s, where a kernel that only reads the same rows takes 83; in f32
 // (1.07 GB) 6.4 TB/s.  The gradient moves 1.07 GB in 172-187 us, 5.8-6.2 TB/s,
 // the rate of an elementwise stream.
 #include "internal.hpp"
@@ -496,10 +496,8 @@ __device__ __forceinline__ uint64_t best_of_part(const T* in, uint32_t n, uint32
 // target those above it, in front of it those above the next value below it,
 // which are the ones not below it; the vector that holds the target is
 // counted as behind it and its equal logits in front of it added.
-// (The selects would take more than 96 scalar registers, which let 8 waves run
-// on a SIMD in f32; in 16 bits the vector registers, 70, let 7.)
 template <int ELEM, bool TOP, bool STREAM>
-__global__ __launch_bounds__(kLpBlock) __attribute__((amdgpu_num_sgpr(96))) void logprobs_kernel(LogprobsArgs p, Parts parts, Sums* __restrict__ sums,
+__global__ __launch_bounds__(kLpBlock) void logprobs_kernel(LogprobsArgs p, Parts parts, Sums* __restrict__ sums,
                                                             uint64_t* __restrict__ lists) {
     using T = typename Elem<ELEM>::T;
     constexpr uint32_t N = RowVec<T>::N;
