@@ -91,7 +91,8 @@ struct Candidate {
 };
 
 // The best two scores of the group that `p` lanes share, from each lane's two;
-// then the group's score into the row's LDS, best_of [groups].
+// then the group's score into the row's LDS, best_of [groups], and in f32 the
+// size of its terms, which its error goes by, behind it.
 template <class S>
 __device__ __forceinline__ void group_score(const RouteArgs& a, S best, S next, uint32_t sub, uint32_t p, S masked,
                                             S* best_of) {
@@ -102,9 +103,13 @@ __device__ __forceinline__ void group_score(const RouteArgs& a, S best, S next, 
     }
     const uint32_t g = sub / p;
     if (g < a.groups && sub == g * p) {
-        S sum = a.group_best == 2 && next > masked ? best + next : best;
-        // a sum below f32's range is not a masked group's
-        if (sizeof(S) == 4 && best > masked) sum = fmax(sum, S(-3.402823466e38f));
+        const bool two = a.group_best == 2 && next > masked;
+        S sum = two ? best + next : best;
+        if (sizeof(S) == 4) {
+            // a sum below f32's range is not a masked group's
+            if (best > masked) sum = fmax(sum, S(-3.402823466e38f));
+            best_of[a.groups + g] = fabs(best) + (two ? fabs(next) : S(0));
+        }
         best_of[g] = sum;
     }
 }
@@ -131,9 +136,9 @@ __device__ __forceinline__ void group_scores(const RouteArgs& a, const S* score,
 }
 
 // The kept groups of the wave's rows, as masks (equal in a row's lanes), from
-// the groups' scores best_of [groups] (f32 or 64 bits).  off, rel: how far two
-// scores may be off together; `unclear` tells whether that leaves the row's
-// choice open.
+// the groups' scores best_of [groups] (f32 or 64 bits).  Two f32 scores may be
+// off by off + rel * (the size of their terms) together; `unclear` tells whether
+// that leaves the row's choice open.
 template <int L, class S>
 __device__ __forceinline__ uint64_t kept_groups(const RouteArgs& a, const S* best_of, S masked, S off, S rel,
                                                 bool* unclear) {
@@ -143,12 +148,13 @@ __device__ __forceinline__ uint64_t kept_groups(const RouteArgs& a, const S* bes
     bool kept = false, open = false;
     if (sub < a.groups) {   // groups before this one, and groups that may be
         const S mine = best_of[sub];
+        const S size = sizeof(S) == 4 ? best_of[a.groups + sub] : S(0);
         uint32_t before = 0, near = 0;
 #pragma unroll 4
         for (uint32_t i = 0; i < a.groups; ++i) {
             const S o = best_of[i];
-            const bool close = i != sub && o != mine && o > masked && mine > masked &&
-                               fabs(o - mine) <= off + rel * (fabs(o) + fabs(mine));
+            const bool close = sizeof(S) == 4 && i != sub && o != mine && o > masked && mine > masked &&
+                               fabs(o - mine) <= off + rel * (size + best_of[a.groups + i]);
             // equal scores are a tie if they are exact, or if nothing is left in both
             const bool tie = i != sub && o == mine && (off == S(0) || mine == masked);
             near += close || (i != sub && o == mine && !tie);
@@ -168,7 +174,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(RouteArgs a) 
     using T = typename Elem<ELEM>::T;
     constexpr uint32_t R = kWave / L;   // rows of a wave
     __shared__ Candidate s_list[kRouteWaves * R][L];
-    extern __shared__ double s_groups[];   // with groups: a row's scores, then its groups' scores
+    extern __shared__ double s_groups[];   // with groups: a row's scores, then its groups' (as f32 in the same place)
     const uint32_t lane = threadIdx.x & (kWave - 1);
     const uint32_t sub = lane & (L - 1);
     const uint32_t slot = threadIdx.x / L;   // the row's place in the block

@@ -282,6 +282,18 @@ def test_extreme_biases(score):
             check(x, 8, bias=bias, score=score, **kw)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [2, 8, 9])
+def test_group_sums_that_cancel(score, size):
+    """Large biases of both signs in a group: their sum is small, the roundings of its terms are not."""
+    g = np.random.default_rng(21)
+    groups = 16
+    for big in (1e3, 1e5, 1e8):
+        bias = np.where(np.arange(groups * size) % size == 0, big, -big)
+        print("route cancelling groups", score, size, big, flush=True)
+        check(g.standard_normal((60, groups * size)), 4, score=score, bias=bias, groups=groups, top_groups=5, group_best=2)
+
+
 @pytest.mark.parametrize("seed", range(40))
 def test_random_combinations(seed):
     g = np.random.default_rng(1000 + seed)
