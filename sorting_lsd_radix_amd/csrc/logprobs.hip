@@ -273,17 +273,26 @@ __device__ __forceinline__ void finish_row(const LogprobsArgs& p, uint32_t row, 
 struct Running {
     float m = -kInf, c = 0.0f, s = 0.0f, t = 0.0f;
 
+    // x - y of the two rounded numbers.  Where the compiler fuses a product into it, the sums so far
+    // are moved by the product before its rounding, which is off by up to 2^-24 |m a| from
+    // where the terms to come are counted from: with logits around -7e5 s was off by a part in 150.
+    static __device__ __forceinline__ float difference(float x, float y) {
+#pragma clang fp contract(off)
+        return x - y;
+    }
+
     // Called with a new largest m: moves the reference there, unless it is near
     // enough, or too large for c (slow_sums then).
     __device__ __forceinline__ void reference(float a) {
         if (!(fabsf(fmaf(m, a, c)) <= kMaxShift) && fabsf(m * a) <= kMaxReference) {
-            const float d = fmaxf(-m * a - c, -1000.0f);
+            const float to = -m * a;
+            const float d = fmaxf(difference(to, c), -1000.0f);
             const float f = __builtin_amdgcn_exp2f(d);
             if (s != 0.0f) {
                 t = (t + s * d) * f;
                 s *= f;
             }
-            c = -m * a;
+            c = to;
         }
     }
 
