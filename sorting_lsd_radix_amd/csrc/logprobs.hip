@@ -253,10 +253,7 @@ __device__ __forceinline__ void finish_row(const LogprobsArgs& p, uint32_t row, 
         p.stats[2ull * row] = z.m;
         p.stats[2ull * row + 1] = z.s;
         if (p.lse) p.lse[row] = empty ? -kInf : z.m * p.scale + ln_s;
-        if (p.entropy) {
-            const float h = empty ? 0.0f : ln_s - kLn2 * (z.t / z.s);
-            p.entropy[row] = h < 0.0f ? 0.0f : h;   // rounding alone makes it negative
-        }
+        if (p.entropy) p.entropy[row] = empty ? 0.0f : ln_s - kLn2 * (z.t / z.s);   // s >= 1, t <= 0
         if (p.logprob) p.logprob[row] = has_target ? ln_p(x_target) : 0.0f;
         if (p.rank) p.rank[row] = has_target && x_target == x_target ? z.ahead : 0xFFFFFFFFu;
     }
@@ -313,11 +310,18 @@ struct Running {
         t += t2[0] + t2[1];
     }
 
+    // The sums with the largest logit as the reference.  Its own term is 1 and adds nothing to t:
+    // what add() took for it is taken out of the sums before they are scaled, so that s is never
+    // below 1 (no probability above 1) and a row with one token left gives s = 1 and t = 0.
     __device__ __forceinline__ Sums relative_to_largest(float a) const {
         if (!(fabsf(m * a) <= kMaxReference)) return Sums{m, s == s ? 0.0f : s, 0.0f, 0u};
         const float d = fmaf(m, a, c);
         const float f = __builtin_amdgcn_exp2f(-d);
-        return Sums{m, s * f, (t - s * d) * f, 0u};
+        const float e = __builtin_amdgcn_exp2f(d);
+        const float rest = s - e;
+        if (rest <= 0.0f) return Sums{m, 1.0f, 0.0f, 0u};   // nothing else, or less than s's roundings
+        const float moved = (t - e * d - rest * d) * f;      // no term of t is above 0
+        return Sums{m, 1.0f + rest * f, moved < 0.0f ? moved : 0.0f, 0u};
     }
 };
 

@@ -42,3 +42,87 @@ def test_terms_of_an_earlier_reference_keep_their_weight(far):
     ln_p = d[np.arange(2), at] - np.log(s)
     close(got.logprob, np.tile(ln_p, 550), np.tile(off + 4 * ref.U * (np.abs(ln_p) + 2 * np.log(s)), 550), "logprob")
     close(got.entropy, np.tile(entropy, 550), np.tile(off * 8 + 8 * ref.U * (np.log(s) + 1), 550), "entropy")
+
+
+LEFT = [(1, "f32", 200), (3, "bf16", 200), (700, "f32", 300), (700, "f16", 300), (9000, "bf16", 300),
+        (9000, "f32", 300), (40009, "f32", 40), (70001, "bf16", 12)]
+
+
+@pytest.mark.parametrize("vocab,dtype,rows", LEFT)
+@pytest.mark.parametrize("spread", [4.0, 11.0, 300.0, 3e4])
+def test_one_token_left(vocab, dtype, rows, spread):
+    """A row with one token left knows its answer: probability 1, no entropy, no gradient, exactly."""
+    g = np.random.default_rng(vocab)
+    x = np.full((rows, vocab), -np.inf)
+    at = g.integers(0, vocab, rows)
+    x[np.arange(rows), at] = g.uniform(-spread, spread, rows)
+    t = matrix(x, dtype)
+    x = values(t)
+    for scale in (1.0, 0.7, 3.0):
+        print("logprobs one left", vocab, dtype, spread, scale, flush=True)
+        c = np.float64(np.float32(scale))
+        got = rs.token_logprobs(t, ids32(at), top_k=1, scale=scale)
+        same(got.logprob, np.zeros(rows), "logprob")
+        same(got.entropy, np.zeros(rows), "entropy")
+        same(got.top_logprobs, np.zeros((rows, 1)), "top_logprobs")
+        same(got.top_ids, at[:, None], "top_ids")
+        same(got.rank, np.zeros(rows), "rank")
+        m = x[np.arange(rows), at]
+        same(got.stats, np.stack([m, np.ones(rows)], 1), "stats")
+        close(got.lse, m * c, 0 * m, "lse")                 # the product, rounded once
+        one = torch.full((rows,), 0.7, device=DEV)
+        dx = rs.token_logprobs_grad(t, got.stats, ids32(at), dlogprob=one, entropy=got.entropy, dentropy=one,
+                                    scale=scale)
+        same(dx, np.zeros((rows, vocab)), "dlogits")
+
+
+@pytest.mark.parametrize("vocab,rows", [(2, 500), (33, 500), (5000, 300), (50021, 40)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_no_probability_is_above_one(vocab, rows, dtype):
+    g = np.random.default_rng(vocab + 1)
+    x = g.standard_normal((rows, vocab)) * 3
+    at = g.integers(0, vocab, rows)
+    x[np.arange(rows), at] += g.uniform(0, 60, rows)        # from flat rows to rows of one token
+    t = matrix(x, dtype, pad=1)
+    for scale in (1.0, 0.3, 2.7):
+        print("logprobs at most 1", vocab, dtype, scale, flush=True)
+        got = rs.token_logprobs(t, ids32(at), top_k=min(vocab, 8), scale=scale)
+        assert (got.stats[:, 1] >= 1).all()
+        assert (got.logprob <= 0).all() and (got.top_logprobs <= 0).all()
+        assert (got.entropy >= 0).all()
+        m = got.stats[:, 0].double() * float(np.float32(scale))
+        assert (got.lse.double() >= m - m.abs() * ref.U).all()
+
+
+@pytest.mark.parametrize("vocab,dtype", [(60, "f32"), (3000, "bf16"), (9000, "f32"), (66000, "f16")])
+def test_few_tokens_left(vocab, dtype):
+    """Bound.  The largest logit's term is 1 exactly.  Another, w powers of two below it: the factor
+    a is off by 2 U, d by its rounding of at most w + 16, the reference's distance by 16, a move by
+    w + 32 (the term is then within 16 of the old reference), exp2 twice or, after a move, three
+    times 2 U, four products, a join's w and exp2 in each of at most 30 joins that it passes, of
+    which only those that it moves in round (at most 5 live logits: 5), the rest exact: U (ln 2 (9 w
+    + 64) + 30) of it.  The sum of L terms rounds L - 1 times, in a thread before its reference's
+    distance is taken off, and the largest is taken out of it: L + 2 times U s."""
+    g = np.random.default_rng(vocab + 2)
+    rows = 400
+    x = np.full((rows, vocab), -np.inf)
+    live = g.integers(2, 7, rows)
+    for r in range(rows):
+        where = g.choice(vocab, live[r], replace=False) if r % 3 else np.arange(live[r]) + g.integers(0, vocab - 6)
+        x[r, where] = g.uniform(-12, 12, live[r])
+    t = matrix(x, dtype)
+    x = values(t)
+    at = x.argmax(1)
+    print("logprobs few left", vocab, dtype, flush=True)
+    got = rs.token_logprobs(t, ids32(at), top_k=2)
+    d = x - x.max(1, keepdims=True)
+    e = np.exp(d)
+    with np.errstate(invalid="ignore"):
+        w = np.where(e > 0, -d / np.log(2), 0.0)
+    s = e.sum(1)
+    rest = np.where(d < 0, e, 0.0)
+    off = ref.U * ((rest * (np.log(2) * (9 * w + 64) + 30)).sum(1) + (live + 2) * s)
+    close(got.stats, np.stack([x.max(1), s], 1), np.stack([0 * s, off], 1), "stats")
+    close(got.logprob, -np.log(s), off / s + 4 * ref.U * np.log(s), "logprob")
+    m = x.max(1)
+    close(got.lse, m + np.log(s), off / s + 2 * ref.U * (np.abs(m) + np.log(s)), "lse")
