@@ -126,3 +126,44 @@ def test_few_tokens_left(vocab, dtype):
     close(got.logprob, -np.log(s), off / s + 4 * ref.U * np.log(s), "logprob")
     m = x.max(1)
     close(got.lse, m + np.log(s), off / s + 2 * ref.U * (np.abs(m) + np.log(s)), "lse")
+
+
+def gradients(x, targets, scale):
+    t = matrix(x, "f32")
+    x = values(t)
+    rows = x.shape[0]
+    got = rs.token_logprobs(t, ids32(targets), scale=scale)
+    g = np.random.default_rng(rows)
+    a, h, q = (g.standard_normal(rows).astype(np.float32) for _ in range(3))
+    for a_, h_, q_ in ((a, None, None), (None, None, q), (a, h, q)):
+        dev = [None if v is None else torch.from_numpy(v).to(DEV) for v in (a_, h_, q_)]
+        dx = rs.token_logprobs_grad(t, got.stats, ids32(targets), dlogprob=dev[0], entropy=got.entropy,
+                                    dentropy=dev[1], dlse=dev[2], scale=scale)
+        want, bound = ref.logprobs_grad(x, np.asarray(targets), np.float32(scale),
+                                        *(None if v is None else v.astype(np.float64) for v in (a_, h_, q_)))
+        close(dx, want, bound, "dlogits")
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -60, 1e-4, 300.0, 1e6, 2.0 ** 60])
+@pytest.mark.parametrize("vocab", [50, 9000])
+def test_gradient_at_extreme_scales(scale, vocab):
+    print("logprobs gradient scale %g vocab %d" % (scale, vocab), flush=True)
+    g = np.random.default_rng(25)
+    x = g.standard_normal((5, vocab)) * 3
+    x[1] += 100.0
+    x[2] -= 1000.0
+    x[3, ::3] = -np.inf
+    gradients(x, [0, 1, 2, 4, vocab - 1], scale)
+
+
+@pytest.mark.parametrize("far", [1e4, 7.2e5, 7.27e5, 1.5e6, 1e9, 1e35, 3.4e38])
+def test_gradient_far_from_zero(far):
+    print("logprobs gradient around %g" % far, flush=True)
+    g = np.random.default_rng(26)
+    step = np.float64(np.spacing(np.float32(far)))
+    x = np.round(g.standard_normal((4, 9000)) * max(3.0, 2 * step) / step) * step
+    x[0::2] += far
+    x[1::2] -= far
+    x = np.clip(x, -3.4028234663852886e38, 3.4028234663852886e38)
+    x[2, ::4] -= far / 2
+    gradients(x, [3, 30, 300, 3000], 1.0)
