@@ -670,8 +670,9 @@ class _On:
         if index != _torch.cuda.current_device():
             self._contexts.append(_torch.cuda.device(index))
         if stream is not None:
-            if isinstance(stream, int):
-                stream = _torch.cuda.ExternalStream(stream, device=index)
+            if isinstance(stream, int):   # of address 0, the default stream's, torch would make a new one
+                stream = _torch.cuda.ExternalStream(stream, device=index) if stream else \
+                    _torch.cuda.default_stream(index)
             self._contexts.append(_torch.cuda.stream(stream))
 
     def __enter__(self):
