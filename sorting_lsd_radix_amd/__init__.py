@@ -667,6 +667,8 @@ class _On:
 
     def __init__(self, index, stream):
         self._contexts = []
+        if stream is not None and not isinstance(stream, int) and stream.device.index != index:
+            raise TypeError("stream must be on cuda:%d, not %s" % (index, stream.device))
         if index != _torch.cuda.current_device():
             self._contexts.append(_torch.cuda.device(index))
         if stream is not None:

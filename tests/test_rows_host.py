@@ -176,6 +176,20 @@ def test_wrappers_refuse_what_is_no_matrix_on_a_gpu():
             call()
 
 
+class StreamOf:
+    """As much of a torch stream as is looked at before it is used."""
+
+    def __init__(self, device):
+        self.device = device
+
+
+def test_a_stream_of_another_device_is_refused():
+    torch = pytest.importorskip("torch")
+    rs._load_torch()
+    with pytest.raises(TypeError, match="cuda:1"):
+        rs._run_on(1, StreamOf(torch.device("cuda:0")), lambda on: pytest.fail("called"))
+
+
 # --- the reference -----------------------------------------------------------------------------------
 
 def differences(f, x, h=1e-5):
