@@ -686,12 +686,20 @@ class _On:
             c.__exit__(*exc)
 
 
-def _run_on(index, stream, call):
-    """call(address of the stream) with the device and the stream as the current ones."""
+def _run_on(index, stream, call, given=()):
+    """call(address of the stream) with the device and the stream as the current ones.  The memory
+    of the tensors `given` to the call (Nones among them) is kept until a stream that is not the
+    current one has run it: their owner may drop them at once."""
     if stream is None and index == _torch.cuda.current_device():
         return call(_torch._C._cuda_getCurrentRawStream(index))
     with _On(index, stream):
-        return call(_torch._C._cuda_getCurrentRawStream(index))
+        result = call(_torch._C._cuda_getCurrentRawStream(index))
+        if stream is not None:
+            on = _torch.cuda.current_stream(index)
+            for t in given:
+                if t is not None:
+                    t.record_stream(on)
+        return result
 
 
 # A size query that answers RS_NO_TEMP bytes or less says that the call does not touch its temp:
@@ -722,8 +730,7 @@ def route_topk(scores, top_k, bias=None, score="softmax", groups=1, top_groups=1
     torch = _load_torch()
     et, rows, experts, stride = _rows(scores, "scores")
     index = scores.get_device()
-    if bias is not None:
-        bias = _check_like(bias, "bias", (experts,), (torch.float32,), index)
+    at_bias = None if bias is None else _check_like(bias, "bias", (experts,), (torch.float32,), index)
     fn = _SCORES[score]
     lib = _load()
 
@@ -731,11 +738,11 @@ def route_topk(scores, top_k, bias=None, score="softmax", groups=1, top_groups=1
         ids = torch.empty(rows, top_k, dtype=torch.int32, device=scores.device)
         weights = torch.empty(rows, top_k, dtype=torch.float32, device=scores.device)
         _call("rs_route_topk", lib.rs_route_topk(
-            et, scores.data_ptr(), stride, bias, rows, experts, top_k, fn, groups, top_groups,
+            et, scores.data_ptr(), stride, at_bias, rows, experts, top_k, fn, groups, top_groups,
             group_best, 1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), on))
         return ids, weights
 
-    return _run_on(index, stream, call)
+    return _run_on(index, stream, call, (scores, bias))
 
 
 def route_topk_grad(scores, ids, weights, dweights, score="softmax", renormalize=True, scale=1.0,
@@ -764,7 +771,7 @@ def route_topk_grad(scores, ids, weights, dweights, score="softmax", renormalize
             1 if renormalize else 0, scale, at, ostride, on))
         return to
 
-    return _run_on(index, stream, call)
+    return _run_on(index, stream, call, (scores, ids, weights, dweights, out))
 
 
 def group_choices(ids, experts, align=1, temp=None, stream=None):
@@ -797,7 +804,7 @@ def group_choices(ids, experts, align=1, temp=None, stream=None):
             counts.data_ptr(), work, ctypes.byref(have), on))
         return order, place, starts, counts
 
-    return _run_on(index, stream, call)
+    return _run_on(index, stream, call, (ids, temp))
 
 
 TokenLogprobs = collections.namedtuple(
@@ -818,9 +825,7 @@ def token_logprobs(logits, targets=None, top_k=0, scale=1.0, temp=None, stream=N
     torch = _load_torch()
     et, rows, vocab, stride = _rows(logits, "logits")
     index = logits.get_device()
-    if targets is not None:
-        given = targets
-        targets = _check_like(given, "targets", (rows,), _INTS, index)
+    at_targets = None if targets is None else _check_like(targets, "targets", (rows,), _INTS, index)
     lib = _load()
     size = ctypes.c_size_t(0)
     _call("rs_token_logprobs", lib.rs_token_logprobs(
@@ -842,12 +847,12 @@ def token_logprobs(logits, targets=None, top_k=0, scale=1.0, temp=None, stream=N
             top_logprobs = torch.empty(rows, top_k, dtype=f32, device=dev)
         _keep, work, have = _temp_arg(temp, size, dev)
         _call("rs_token_logprobs", lib.rs_token_logprobs(
-            et, logits.data_ptr(), stride, targets, rows, vocab, scale, top_k, stats.data_ptr(),
+            et, logits.data_ptr(), stride, at_targets, rows, vocab, scale, top_k, stats.data_ptr(),
             lse.data_ptr(), entropy.data_ptr(), _ptr(logprob), _ptr(rank), _ptr(top_ids),
             _ptr(top_logprobs), work, ctypes.byref(have), on))
         return TokenLogprobs(logprob, entropy, lse, rank, stats, top_ids, top_logprobs)
 
-    return _run_on(index, stream, call)
+    return _run_on(index, stream, call, (logits, targets, temp))
 
 
 def token_logprobs_grad(logits, stats, targets=None, dlogprob=None, entropy=None, dentropy=None,
@@ -876,4 +881,4 @@ def token_logprobs_grad(logits, stats, targets=None, dlogprob=None, entropy=None
             *at_rows[1:], at, ostride, on))
         return to
 
-    return _run_on(index, stream, call)
+    return _run_on(index, stream, call, (logits, stats, targets, entropy, dlogprob, dentropy, dlse, out))

@@ -16,7 +16,7 @@ def busy(stream=None):
     b = torch.empty_like(a)
     torch.cuda.synchronize()
     with torch.cuda.stream(stream or torch.cuda.current_stream()):
-        for _ in range(12):
+        for _ in range(30):
             b.copy_(a)
     return a, b
 
@@ -40,3 +40,71 @@ def test_address_0_is_the_default_stream():
         for g, want in zip(got, ref.group(np.arange(1000) % 7, 7, 1)):
             same(g, want, "stream %d" % address)
         del held
+
+
+def calls(stream, rows=4096, cols=512):
+    """Every wrapper on `stream`, each as (tensors given to it alone, call on them)."""
+    x = torch.randn(rows, cols, device=DEV)
+    b = torch.randn(cols, device=DEV)
+    i = torch.zeros(rows, 8, dtype=torch.int32, device=DEV)
+    w = torch.rand(rows, 8, device=DEV)
+    t = torch.zeros(rows, dtype=torch.int32, device=DEV)
+    r = [torch.rand(rows, device=DEV) for _ in range(4)]
+    st = torch.ones(rows, 2, device=DEV)
+
+    def temp(n):
+        return torch.empty(n, dtype=torch.uint8, device=DEV)
+
+    return [
+        ("route", lambda: ([x.clone(), b.clone()], lambda x, b: rs.route_topk(x, 8, bias=b, stream=stream))),
+        ("route grad", lambda: ([x.clone(), i.clone(), w.clone(), w.clone(), torch.empty_like(x)],
+                                lambda x, i, w, d, o: rs.route_topk_grad(x, i, w, d, out=o, stream=stream))),
+        ("group", lambda: ([i.clone(), temp(1 << 20)],
+                           lambda i, m: rs.group_choices(i, 64, temp=m, stream=stream))),
+        ("logprobs", lambda: ([x.clone(), t.clone(), temp(1 << 20)],
+                              lambda x, t, m: rs.token_logprobs(x, t, top_k=3, temp=m, stream=stream))),
+        ("logprobs grad", lambda: ([x.clone(), st.clone(), t.clone(), *(v.clone() for v in r), torch.empty_like(x)],
+                                   lambda x, s, t, a, e, h, q, o: rs.token_logprobs_grad(
+                                       x, s, t, dlogprob=a, entropy=e, dentropy=h, dlse=q, out=o, stream=stream))),
+    ]
+
+
+@pytest.mark.parametrize("by", ["stream", "address"])
+def test_what_a_call_was_given_may_be_dropped_at_once(by):
+    """While the call waits on another stream, its inputs, `out` and `temp` do not go to the next
+    allocations of their own stream."""
+    side = torch.cuda.Stream()
+    busy(side)
+    torch.cuda.synchronize()
+    for name, make in calls(side if by == "stream" else side.cuda_stream):
+        print("dropped inputs:", name, flush=True)
+        tensors, call = make()
+        torch.cuda.synchronize()
+        held = busy(side)
+        sizes = [(t.numel() * t.element_size(), t.data_ptr()) for t in tensors]
+        result = call(*tensors)
+        del tensors, result, call
+        again = [torch.empty(n, dtype=torch.uint8, device=DEV) for n, _ in sizes for _ in range(2)]
+        assert not side.query(), "the copies in front were to take longer than this"
+        assert not {t.data_ptr() for t in again} & {p for _, p in sizes}, name
+        torch.cuda.synchronize()
+        del held, again
+
+
+def test_captured_calls_on_a_given_stream():
+    """The stream that captures, given by name, is the current one in all but name."""
+    print("capture on a given stream", flush=True)
+    x = torch.randn(300, 64, device=DEV)
+    want = rs.route_topk(x, 4)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        ids, w = rs.route_topk(x + 0.0, 4, stream=side)
+    for _ in range(3):
+        ids.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ids, want[0]) and torch.equal(w, want[1])
+        torch.empty(1 << 22, device=DEV).normal_()
+        torch.cuda.synchronize()
