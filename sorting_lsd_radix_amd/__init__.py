@@ -710,6 +710,8 @@ _NO_TEMP_ADDRESS = RS_NO_TEMP
 def _temp_arg(temp, size, device):
     """(tensor to keep until the call, its address, its size) of a call's temp."""
     if temp is not None:
+        if not temp.is_cuda or temp.device != device or not temp.is_contiguous():
+            raise TypeError("temp must be a contiguous CUDA tensor on %s" % (device,))
         return temp, temp.data_ptr(), ctypes.c_size_t(temp.numel() * temp.element_size())
     if size.value <= RS_NO_TEMP:
         return None, _NO_TEMP_ADDRESS, size

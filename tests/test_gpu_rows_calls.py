@@ -108,3 +108,26 @@ def test_captured_calls_on_a_given_stream():
         assert torch.equal(ids, want[0]) and torch.equal(w, want[1])
         torch.empty(1 << 22, device=DEV).normal_()
         torch.cuda.synchronize()
+
+
+def test_temps():
+    """A temp is memory of the tensors' device, all of it, and as much as the call asks for."""
+    print("temps", flush=True)
+    ids = torch.arange(50000, dtype=torch.int32, device=DEV) % 9
+    x = torch.randn(2, 70000, device=DEV)
+    for call, need in ((lambda m: rs.group_choices(ids, 9, temp=m),
+                        rs.rs_group_choices(None, 50000, 9, 1, *([None] * 5), 0)),
+                       (lambda m: rs.token_logprobs(x, top_k=4, temp=m),
+                        rs.rs_token_logprobs(0, None, 70000, None, 2, 70000, 1.0, 4, *([None] * 8), 0))):
+        assert need > rs.RS_NO_TEMP
+        for bad in (torch.empty(need, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device=DEV).expand(need),
+                    torch.empty(need, 2, dtype=torch.uint8, device=DEV)[:, 0]):
+            with pytest.raises(TypeError):
+                call(bad)
+        with pytest.raises(rs.RsError) as e:
+            call(torch.empty(need - 1, dtype=torch.uint8, device=DEV))
+        assert e.value.status == rs.RS_ERR_TEMP_TOO_SMALL
+        whole = torch.full((need // 4 + 4,), -7, dtype=torch.int32, device=DEV)   # any type, by its bytes
+        for got, want in zip(call(whole[:-4]), call(None)):
+            assert got is want is None or torch.equal(got, want)
+        assert (whole[-4:] == -7).all()

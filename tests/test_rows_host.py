@@ -190,6 +190,14 @@ def test_a_stream_of_another_device_is_refused():
         rs._run_on(1, StreamOf(torch.device("cuda:0")), lambda on: pytest.fail("called"))
 
 
+def test_a_temp_that_is_not_the_devices_own_memory_is_refused():
+    torch = pytest.importorskip("torch")
+    size = ctypes.c_size_t(64)
+    for temp in (torch.empty(64, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8).expand(64)):
+        with pytest.raises(TypeError, match="temp"):
+            rs._temp_arg(temp, size, torch.device("cuda:0"))
+
+
 # --- the reference -----------------------------------------------------------------------------------
 
 def differences(f, x, h=1e-5):
