@@ -334,9 +334,17 @@ def rs_bitonic_tile(keys_in, keys_out, n, tile, begin_bit, end_bit, stream=None)
     _call("rs_bitonic_tile", st)
 
 
+def _check_counts(what, counts):
+    """`counts`, or-ed, are numbers that the C interface takes in 32 bits: past them they would come
+    out as others."""
+    if counts >> 32:   # of a negative one, -1
+        raise RsError(RS_ERR_UNSUPPORTED_SIZE, what)
+
+
 def rs_route_topk(elem_type, scores, row_stride, bias, rows, experts, top_k, score_fn, groups,
                   top_groups, group_best, renormalize, scale, ids, weights, stream=None):
     """C: rs_route_topk."""
+    _check_counts("rs_route_topk", experts | top_k | groups | top_groups | group_best)
     st = _load().rs_route_topk(int(elem_type), _ptr(scores), int(row_stride), _ptr(bias), int(rows),
                                int(experts), int(top_k), int(score_fn), int(groups),
                                int(top_groups), int(group_best), int(bool(renormalize)),
@@ -347,6 +355,7 @@ def rs_route_topk(elem_type, scores, row_stride, bias, rows, experts, top_k, sco
 def rs_route_topk_grad(elem_type, scores, row_stride, ids, weights, dweights, rows, experts, top_k,
                        score_fn, renormalize, scale, dscores, dscores_stride, stream=None):
     """C: rs_route_topk_grad."""
+    _check_counts("rs_route_topk_grad", experts | top_k)
     st = _load().rs_route_topk_grad(int(elem_type), _ptr(scores), int(row_stride), _ptr(ids),
                                     _ptr(weights), _ptr(dweights), int(rows), int(experts),
                                     int(top_k), int(score_fn), int(bool(renormalize)),
@@ -358,6 +367,7 @@ def rs_route_topk_grad(elem_type, scores, row_stride, ids, weights, dweights, ro
 def rs_group_choices(ids, n, experts, align, order, place, starts, counts, d_temp, temp_bytes,
                      stream=None):
     """C: rs_group_choices.  With d_temp None, returns the temp size."""
+    _check_counts("rs_group_choices", experts | align)
     size = ctypes.c_size_t(0 if temp_bytes is None else int(temp_bytes))
     st = _load().rs_group_choices(_ptr(ids), int(n), int(experts), int(align), _ptr(order),
                                   _ptr(place), _ptr(starts), _ptr(counts), _ptr(d_temp),
@@ -371,6 +381,7 @@ def rs_token_logprobs(elem_type, logits, row_stride, targets, rows, vocab, scale
                       entropy, logprob, rank, top_ids, top_logprobs, d_temp, temp_bytes,
                       stream=None):
     """C: rs_token_logprobs.  With d_temp None, returns the temp size."""
+    _check_counts("rs_token_logprobs", vocab | top_k)
     size = ctypes.c_size_t(0 if temp_bytes is None else int(temp_bytes))
     st = _load().rs_token_logprobs(int(elem_type), _ptr(logits), int(row_stride), _ptr(targets),
                                    int(rows), int(vocab), float(scale), int(top_k), _ptr(stats),
@@ -385,6 +396,7 @@ def rs_token_logprobs(elem_type, logits, row_stride, targets, rows, vocab, scale
 def rs_token_logprobs_grad(elem_type, logits, row_stride, targets, stats, entropy, rows, vocab,
                            scale, dlogprob, dentropy, dlse, dlogits, dlogits_stride, stream=None):
     """C: rs_token_logprobs_grad."""
+    _check_counts("rs_token_logprobs_grad", vocab)
     st = _load().rs_token_logprobs_grad(int(elem_type), _ptr(logits), int(row_stride),
                                         _ptr(targets), _ptr(stats), _ptr(entropy), int(rows),
                                         int(vocab), float(scale), _ptr(dlogprob), _ptr(dentropy),
@@ -731,6 +743,7 @@ def route_topk(scores, top_k, bias=None, score="softmax", groups=1, top_groups=1
     chosen p if renormalize."""
     torch = _load_torch()
     et, rows, experts, stride = _rows(scores, "scores")
+    _check_counts("rs_route_topk", experts | top_k | groups | top_groups | group_best)
     index = scores.get_device()
     at_bias = None if bias is None else _check_like(bias, "bias", (experts,), (torch.float32,), index)
     fn = _SCORES[score]
@@ -754,8 +767,9 @@ def route_topk_grad(scores, ids, weights, dweights, score="softmax", renormalize
     scores' type (`out`, if given: a matrix whose rows are contiguous)."""
     torch = _load_torch()
     et, rows, experts, stride = _rows(scores, "scores")
-    index = scores.get_device()
     top_k = ids.shape[-1]
+    _check_counts("rs_route_topk_grad", experts | top_k)
+    index = scores.get_device()
     shape = (rows, top_k)
     f32 = (torch.float32,)
     args = (_check_like(ids, "ids", shape, _INTS, index),
@@ -789,6 +803,7 @@ def group_choices(ids, experts, align=1, temp=None, stream=None):
     index = ids.get_device() if ids.is_cuda else -1
     at = _check_like(ids, "ids", shape, _INTS, index)
     n = ids.numel()
+    _check_counts("rs_group_choices", experts | align)
     lib = _load()
     size = ctypes.c_size_t(0)
     _call("rs_group_choices", lib.rs_group_choices(None, n, experts, align, None, None, None, None,
@@ -826,6 +841,7 @@ def token_logprobs(logits, targets=None, top_k=0, scale=1.0, temp=None, stream=N
     views of one tensor."""
     torch = _load_torch()
     et, rows, vocab, stride = _rows(logits, "logits")
+    _check_counts("rs_token_logprobs", vocab | top_k)
     index = logits.get_device()
     at_targets = None if targets is None else _check_like(targets, "targets", (rows,), _INTS, index)
     lib = _load()
@@ -865,6 +881,7 @@ def token_logprobs_grad(logits, stats, targets=None, dlogprob=None, entropy=None
     whose rows are contiguous; it may be the logits themselves)."""
     torch = _load_torch()
     et, rows, vocab, stride = _rows(logits, "logits")
+    _check_counts("rs_token_logprobs_grad", vocab)
     index = logits.get_device()
     f32 = (torch.float32,)
     at_stats = _check_like(stats, "stats", (rows, 2), f32, index)

@@ -131,3 +131,21 @@ def test_temps():
         for got, want in zip(call(whole[:-4]), call(None)):
             assert got is want is None or torch.equal(got, want)
         assert (whole[-4:] == -7).all()
+
+
+def test_rows_and_counts_past_32_bits():
+    print("counts past 2^32", flush=True)
+    long = torch.empty(1, (1 << 32) + 100, dtype=torch.float16, device=DEV)
+    x = torch.zeros(4, 64, device=DEV)
+    ids = torch.zeros(4, 2, dtype=torch.int32, device=DEV)
+    w = torch.zeros(4, 2, device=DEV)
+    one = torch.zeros(1, device=DEV)
+    stats = torch.ones(1, 2, device=DEV)
+    for call in (lambda: rs.token_logprobs(long), lambda: rs.token_logprobs_grad(long, stats, dlse=one),
+                 lambda: rs.route_topk(long, 8), lambda: rs.route_topk_grad(long, ids[:1], w[:1], w[:1]),
+                 lambda: rs.route_topk(x, (1 << 32) + 2), lambda: rs.route_topk(x, -1),
+                 lambda: rs.route_topk(x, 2, groups=(1 << 32) + 1), lambda: rs.token_logprobs(x, top_k=1 << 32),
+                 lambda: rs.group_choices(ids, (1 << 32) + 8), lambda: rs.group_choices(ids, 8, align=(1 << 32) + 1)):
+        with pytest.raises(rs.RsError) as e:
+            call()
+        assert e.value.status == rs.RS_ERR_UNSUPPORTED_SIZE

@@ -176,6 +176,16 @@ def test_wrappers_refuse_what_is_no_matrix_on_a_gpu():
             call()
 
 
+@pytest.mark.parametrize("call,counts", [
+    (route, ("experts", "k", "groups", "top_groups", "best")), (route_grad, ("experts", "k")),
+    (group, ("experts", "align")), (logprobs, ("vocab", "k")), (logprobs_grad, ("vocab",))])
+def test_counts_past_32_bits_are_refused_as_what_they_are(call, counts):
+    """The C interface has 32 bits for each of these; 2^32 + 8 is not 8, and -1 is no count."""
+    for name in counts:
+        for more in (1 << 32, (1 << 32) + 8, (1 << 33) + 1, 1 << 64, -1, -(1 << 32) + 4):
+            refused(rs.RS_ERR_UNSUPPORTED_SIZE, call, **{name: more})
+
+
 class StreamOf:
     """As much of a torch stream as is looked at before it is used."""
 
