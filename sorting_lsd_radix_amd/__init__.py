@@ -792,7 +792,8 @@ def route_topk_grad(scores, ids, weights, dweights, score="softmax", renormalize
 
 def group_choices(ids, experts, align=1, temp=None, stream=None):
     """The choices `ids` (int32 or uint32, any shape) ordered by expert, stably, each expert's
-    segment padded to a multiple of `align`: (order, place, starts, counts), int32.
+    segment padded to a multiple of `align`: (order, place, starts, counts), int32.  Contiguous ids
+    that begin off a 16-byte boundary (some slices of a batch) are copied first.
 
     order [ids.numel() + experts * (align - 1)]: the flat index of the choice at each position,
     -1 in the padding and behind the last segment.  place (of the ids' shape): each choice's
@@ -816,8 +817,9 @@ def group_choices(ids, experts, align=1, temp=None, stream=None):
         starts = torch.empty(experts + 1, dtype=i32, device=dev)
         counts = torch.empty(experts, dtype=i32, device=dev)
         _keep, work, have = _temp_arg(temp, size, dev)
+        aligned = ids if at % 16 == 0 else ids.clone()   # the library reads from 16-byte boundaries on
         _call("rs_group_choices", lib.rs_group_choices(
-            at, n, experts, align, order.data_ptr(), place.data_ptr(), starts.data_ptr(),
+            aligned.data_ptr(), n, experts, align, order.data_ptr(), place.data_ptr(), starts.data_ptr(),
             counts.data_ptr(), work, ctypes.byref(have), on))
         return order, place, starts, counts
 

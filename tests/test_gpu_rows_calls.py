@@ -149,3 +149,32 @@ def test_rows_and_counts_past_32_bits():
         with pytest.raises(rs.RsError) as e:
             call()
         assert e.value.status == rs.RS_ERR_UNSUPPORTED_SIZE
+
+
+@pytest.mark.parametrize("top_k", [1, 2, 3, 5, 6])
+def test_groups_of_a_slice_of_a_batch(top_k):
+    """The ids of some rows of a batch begin anywhere, on a given stream and in a graph as well."""
+    print("slices of ids, top_k", top_k, flush=True)
+    whole = np.random.default_rng(top_k).integers(-1, 40, (700, top_k)).astype(np.int32)
+    ids = torch.from_numpy(whole).to(DEV)
+    side = torch.cuda.Stream()
+    for first, rows in ((1, 5), (2, 697), (3, 1), (7, 0), (699, 1)):
+        want = ref.group(whole[first:first + rows], 40, 8)
+        torch.cuda.synchronize()
+        for stream in (None, side):
+            got = rs.group_choices(ids[first:first + rows], 40, align=8, stream=stream)
+            torch.cuda.synchronize()
+            assert got[1].shape == (rows, top_k)
+            for g, w in zip(got, want):
+                same(g.reshape(-1), w, "from row %d" % first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = rs.group_choices(ids[1:], 40, align=8)
+    for i in range(4):
+        now = np.roll(whole, i, 0)
+        ids.copy_(torch.from_numpy(now))
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, w, e in zip(got, ref.group(now[1:], 40, 8), rs.group_choices(ids[1:], 40, align=8)):
+            same(g.reshape(-1), w, "replay %d" % i)
+            assert torch.equal(g, e)
