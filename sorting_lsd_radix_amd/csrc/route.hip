@@ -410,7 +410,7 @@ template <int ELEM, int L, bool SPREAD>
 __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(RouteGradArgs a) {
     using T = typename Elem<ELEM>::T;
     constexpr uint32_t N = 16 / sizeof(T);
-    constexpr uint32_t S = 16 / N;      // steps of a row whose scores are read, see grad_elem
+    constexpr uint32_t S = (L == kWave ? 16 : 8) / N;   // steps of a row whose scores are read, see grad_elem
     extern __shared__ float s_rows[];   // [rows of the block][experts, rounded up to whole steps]
     const uint32_t lane = threadIdx.x & (kWave - 1);
     const uint32_t sub = lane & (L - 1);
@@ -522,8 +522,12 @@ hipError_t route_lanes(const RouteArgs& a, hipStream_t stream) {
     if (a.experts <= L) return route_shape<ELEM, L, 1>(a, stream);
     if (a.experts <= 2 * L) return route_shape<ELEM, L, 2>(a, stream);
     if (a.experts <= 4 * L) return route_shape<ELEM, L, 4>(a, stream);
-    if (a.experts <= 8 * L) return route_shape<ELEM, L, 8>(a, stream);
-    return route_shape<ELEM, L, 16>(a, stream);
+    if constexpr (L == 16) {   // at most 128 experts, see route_elem
+        return route_shape<ELEM, L, 8>(a, stream);
+    } else {
+        if (a.experts <= 8 * L) return route_shape<ELEM, L, 8>(a, stream);
+        return route_shape<ELEM, L, 16>(a, stream);
+    }
 }
 
 // Lanes of a row: enough that every group has one, that a lane has at most 16
@@ -540,8 +544,7 @@ hipError_t route_elem(const RouteArgs& a, hipStream_t stream) {
 }
 
 // A lane for each choice; and where the scores are read, lanes enough that a
-// row's 16-byte vectors are at most 4 of f32 or 2 of 16 bits a lane, which its
-// registers hold.
+// lane's registers hold its share: 8 elements of 16 or 32 lanes, 16 of 64.
 template <int ELEM>
 hipError_t grad_elem(const RouteGradArgs& a, hipStream_t stream) {
     if (!a.sigmoid && !a.renormalize) {

@@ -316,3 +316,12 @@ def test_random_combinations(seed):
     dtype = ("f32", "f16", "bf16")[seed % 3]
     print("route random", seed, rows, experts, k, dtype, kw, bias is not None, flush=True)
     check(x, k, dtype, pad=seed % 7, shift=seed % 5, bias=bias, **kw)
+
+
+@pytest.mark.parametrize("experts", [64, 127, 128, 129, 255, 256, 257, 1024])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_gradient_of_plain_weights_at_the_borders_of_its_lanes(experts, dtype):
+    g = np.random.default_rng(experts)
+    for k in (1, 16, 17, 32, 33, 64):
+        print("route gradient of plain weights", experts, k, dtype, flush=True)
+        check(g.standard_normal((9, experts)) * 2, k, dtype, pad=k % 3, renormalize=False, scale=1.5)
