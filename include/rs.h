@@ -323,12 +323,13 @@ rs_status rs_bitonic_tile(const uint32_t *keys_in, uint32_t *keys_out, uint64_t 
  * A matrix of rows is a device pointer, a row stride in elements and an
  * element type; its rows hold `experts` or `vocab` elements next to each
  * other.  Matrices need only the alignment of their elements, and other
- * arrays of these calls that of theirs (4 bytes); rows that start on 16-byte
- * boundaries are read fastest.  An input's row stride may be any number (0
- * repeats one row); a written matrix's must be at least its row length, and
- * elements between its rows are left as they are.  Scores, logits and
- * gradients are converted to f32 when read; gradients are rounded to their
- * matrix's type once, when stored (to nearest, ties to even).
+ * arrays of these calls that of theirs (4 bytes; rs_group_choices asks for 16
+ * of some); rows that start on 16-byte boundaries are read fastest.  An
+ * input's row stride may be any number (0 repeats one row); a written matrix's
+ * must be at least its row length, and elements between its rows are left as
+ * they are.  Scores, logits and gradients are converted to f32 when read;
+ * gradients are rounded to their matrix's type once, when stored (to nearest,
+ * ties to even).
  *
  * Order within a row: by value, larger first; equal values (and -0.0 and
  * +0.0 are equal) by index, lower first; a NaN comes after -inf.
@@ -439,6 +440,9 @@ rs_status rs_group_choices(const uint32_t *ids, uint64_t n, uint32_t experts, ui
  *            target's logit is NaN
  *   top_ids [rows, top_k] u32, top_logprobs [rows, top_k] f32: the first
  *            top_k logits in the row's order and their ln p.
+ * No s of a row with a logit above -inf is below 1, and no ln p above 0: the
+ * largest logit's own term is 1 exactly, and the only one left has ln p = 0
+ * and entropy 0.
  * targets [rows]: a target of `vocab` or above means none.  A row of nothing
  * but -inf has m = -inf, s = 0, lse = -inf, entropy 0, and -inf for every ln
  * p; a NaN or +inf in a row makes its lse, entropy, s and ln p NaN.
@@ -461,11 +465,13 @@ rs_status rs_token_logprobs(rs_elem_type elem_type, const void *logits, uint64_t
  *                   - dentropy p_i (ln p_i + entropy) )
  * with the stats (and, with dentropy, the entropy) that rs_token_logprobs
  * gave for the same logits and scale.  A row without target has no gradient
- * through logprob, a row of nothing but -inf none at all, and a logit of
- * -inf none.  Every element of dlogits [rows, vocab] (of elem_type, as the
- * logits) is written; dlogits may be the logits themselves (with the same
- * stride), otherwise the two must not overlap.  targets must be given with
- * dlogprob.  At least one of the three gradients must be given.
+ * through logprob, and a row of nothing but -inf none at all.  A logit of -inf
+ * has p = 0, and so none, but for a target's own term, c * dlogprob, which a
+ * target of -inf gets in a row that has other logits.  Every element of
+ * dlogits [rows, vocab] (of elem_type, as the logits) is written; dlogits may
+ * be the logits themselves (with the same stride), otherwise the two must not
+ * overlap.  targets must be given with dlogprob.  At least one of the three
+ * gradients must be given.
  */
 rs_status rs_token_logprobs_grad(rs_elem_type elem_type, const void *logits, uint64_t row_stride,
                                  const uint32_t *targets, const float *stats, const float *entropy,

@@ -167,3 +167,16 @@ def test_gradient_far_from_zero(far):
     x = np.clip(x, -3.4028234663852886e38, 3.4028234663852886e38)
     x[2, ::4] -= far / 2
     gradients(x, [3, 30, 300, 3000], 1.0)
+
+
+def test_a_masked_target_has_its_own_term():
+    """A target of -inf among other logits: p = 0, but logprob's derivative is c there."""
+    print("logprobs gradient of a masked target", flush=True)
+    x = np.array([[1.0, -np.inf, 2.0, -np.inf], [-np.inf] * 4])
+    t = matrix(x, "f32")
+    got = rs.token_logprobs(t, ids32([1, 1]), scale=0.5)
+    same(got.logprob, np.array([-np.inf, -np.inf]), "logprob")
+    dx = rs.token_logprobs_grad(t, got.stats, ids32([1, 1]), dlogprob=torch.tensor([3.0, 3.0], device=DEV), scale=0.5)
+    p = np.exp([0.5, 0, 1.0, 0]) * [1, 0, 1, 0]
+    want = np.stack([1.5 * (np.array([0, 1, 0, 0]) - p / p.sum()), np.zeros(4)])
+    close(dx, want, np.abs(want) * 64 * ref.U, "dlogits")
