@@ -8,6 +8,17 @@ wrappers below them (``sort_keys_u32`` ...) allocate outputs and temporary
 storage with torch on the tensors' device and launch on torch's current
 stream; torch provides memory and streams only.
 
+The wrappers on rows of scores (``route_topk``, ``route_topk_grad``,
+``group_choices``, ``token_logprobs``, ``token_logprobs_grad``) take `stream`, a
+torch stream of the tensors' device or its address (0: the default stream; None:
+the current one).  Outputs are allocated on that stream, as a torch operation
+under it would, and what a call is given may be dropped at once; to order the
+stream behind what makes the inputs and before what uses the outputs is the
+caller's.  `temp`, a contiguous tensor of at least the size query's bytes on the
+tensors' device, is used by one call at a time.  None of them is part of torch's
+autograd: outputs have no gradient function, whatever the inputs require, and
+``route_topk_grad`` and ``token_logprobs_grad`` compute the gradients.
+
 Loading fails with an error when ``librs.so`` has not been built; there is no
 fallback implementation.  ``use_library(path)`` binds the functions to another
 build of the same sources (the tests use it for the build with the ballot rank
@@ -740,7 +751,7 @@ def route_topk(scores, top_k, bias=None, score="softmax", groups=1, top_groups=1
     probabilities for the choice only.  With groups > 1 the choice is among the experts of the
     top_groups groups whose group_best largest biased probabilities have the largest sum.
     Ties go to the lower expert.  The weights are scale * p, divided by the sum of the row's
-    chosen p if renormalize."""
+    chosen p if renormalize.  No autograd: route_topk_grad gives the scores' gradient."""
     torch = _load_torch()
     et, rows, experts, stride = _rows(scores, "scores")
     _check_counts("rs_route_topk", experts | top_k | groups | top_groups | group_best)
@@ -840,7 +851,7 @@ def token_logprobs(logits, targets=None, top_k=0, scale=1.0, temp=None, stream=N
     [rows, 2], the largest logit and the sum of exp relative to it, which token_logprobs_grad
     takes; top_ids (int32) and top_logprobs [rows, top_k], the largest logits in order, ties to
     the lower index, both None with top_k 0.  Floating outputs are float32; those of [rows] are
-    views of one tensor."""
+    views of one tensor.  No autograd: token_logprobs_grad gives the logits' gradient."""
     torch = _load_torch()
     et, rows, vocab, stride = _rows(logits, "logits")
     _check_counts("rs_token_logprobs", vocab | top_k)

@@ -15,9 +15,10 @@
 //  * Above: a launch in between turns the counts of each expert into the
 //    tiles' offsets and a total.
 //
-// What bounds it: launches and dependent steps.  131072 choices of 256 experts
-// take 2.4 + 8.1 us (the choices and their order are 1.7 MB), 1.3 million of 1000
-// experts 4.4 + 6.3 + 16 us (15.7 MB, the order written in scattered words).
+// What bounds it: launches and dependent steps where choices are few; 131072 of
+// 256 experts take 2.4 + 8.1 us (the choices and their order are 1.7 MB, but every
+// block reads the 128 KB of counts), 1.3 million of 1000 experts 4.4 + 6.3 + 16 us
+// (15.7 MB, the order written in scattered words).
 #include "internal.hpp"
 #include "device_common.hpp"
 
@@ -28,11 +29,16 @@ namespace {
 constexpr int kGroupBlock = 1024;
 constexpr int kGroupWaves = kGroupBlock / kWave;
 constexpr uint32_t kNone = 0xFFFFFFFFu;
-constexpr uint32_t kShortSum = 1u << 15;   // at 2^17 the same times, but more reads of every tile
+// Calls in a captured graph, two launches against three: 2^14 counts 8.0 us
+// against 10.9, 2^15 9.7 against 11.4, 2^16 12.7 against 11.9, 2^17 19.0 against 13.0.
+constexpr uint32_t kShortSum = 1u << 15;
 
-// Choices of a thread.  One tile up to 4096 choices (16384 in one tile: 22 us,
-// in 16 tiles 11 in two launches); above, tiles of 1024, which fill the chip
-// soonest, and from 2^18 on of 4096 (2^20 in tiles of 16384: 27 us against 19).
+// Choices of a thread.  One tile up to 4096 choices: a launch less, which few
+// experts gain by (2048 of 64: 5.4 us in one tile, 6.2 in two of 1024; 4096 of
+// 1000: 15.7 in one, 10.0 in four).  Above, tiles of 1024, which fill the chip
+// soonest (131072 of 64: 7.2 us, in tiles of 4096 9.6), and above 2^18 of 4096
+// (2^20 of 256: 18.4 us, in tiles of 1024 22.6, of 16384 27; at 2^18 itself the
+// two are within 1.5 us of each other, either way by the experts).
 int group_items(uint64_t n) {
     if (n <= kGroupBlock) return 1;
     if (n <= 4 * kGroupBlock) return 4;

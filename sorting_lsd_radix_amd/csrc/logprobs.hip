@@ -36,7 +36,9 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kInf = __builtin_huge_valf();
 // A sum's reference moves when the largest x is further than this from it, in
 // powers of two: far below f32's range (sums reach 2^30 * 2^16), and near
-// enough that the rounding of d (16 * 2^-24) stays under a millionth.
+// enough that the rounding of d (16 * 2^-24) stays under a millionth.  That is
+// the price of one fused multiply-add for d: a difference from the row's own
+// largest would be off by the rounding of its own size only.
 constexpr float kMaxShift = 16.0f;
 // Largest |r a|: c = -r a is off by up to 2^-24 of it, which has to stay a small
 // shift of the reference (an eighth).  Where a part's largest |x a| is over

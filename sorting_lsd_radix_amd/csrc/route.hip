@@ -12,13 +12,21 @@
 // expert that cannot be among the first, and decides which groups are kept
 // unless two scores at the border are too near (then the row's s are all taken
 // in 64 bits).  64-bit arithmetic for every expert cost 45 us of 32768 rows of
-// 512 experts' sigmoids with a bias, against 30 without.
+// 512 experts' sigmoids with a bias, against 30 without.  A softmax whose sum is
+// needed (with a bias, groups by pairs or weights that stay p) still takes the
+// exponential of every expert in 64 bits.
 //
 // What bounds it: 32768 rows of 512 f32 (67 MB), sigmoid with a bias, take 25-28
 // us, 2.4-2.7 TB/s, with the vector units busy in 0.92 of the compute units'
-// cycles (790 instructions for the two rows of a wave); 16384 rows of 256 with
-// groups 16-18 us, where a wave's dependent steps count as much.  Below some
-// 4096 rows the launch is all.
+// cycles (790 instructions for the two rows of a wave), softmax with a bias 35;
+// 16384 rows of 256 with groups 16-20 us, where a wave's dependent steps count as
+// much.  Below some 4096 rows the launch is all.
+//
+// Slower rows: those with more candidates than a row has lanes, whose choices are
+// taken one after the other (equal scores, a mask that leaves fewer lanes than
+// top_k, kept groups on fewer lanes than that: 32768 rows of 512, sigmoid with a
+// bias, 77, 58 and 90 us), and those whose groups f32 cannot tell apart (equal
+// scores in groups by pairs: 139 us, 16384 rows of 256 42).
 #include "internal.hpp"
 #include "rows_common.hpp"
 
@@ -40,6 +48,10 @@ constexpr double kMasked = -1.7976931348623157e308;
 // 4 roundings' worth, 2^-22 (exp2's argument is off by 2^-24 |x log2 e|, which
 // moves p by less than p (1 - p) |x| 2^-24 < 2^-26; exp2 and the reciprocal are
 // off by 2^-23 relative, the sum by 2^-24); adding the bias 2^-24 |s|.  Twice that.
+// A softmax's p has three roundings relative to it, which is less; of a peaked row
+// the small p are so taken for nearer to each other than they are, and more
+// groups compared in 64 bits (32768 rows of 512 in groups by pairs, scores spread
+// by 12 instead of 1.5: 74 us for 53).
 constexpr float kOff = 0x1p-21f;
 constexpr float kOffRel = 0x1p-23f;
 
@@ -535,7 +547,9 @@ hipError_t route_lanes(const RouteArgs& a, hipStream_t stream) {
 // 15.8 on 16; 512 on 32 lanes 25 us for 32768 rows, 33 on 64), and that there
 // are twice top_k: about 1.4 top_k of a row reach the top_k-th of the lanes'
 // bests then, and the list of candidates has a place for each lane.  Experts
-// are spread over all lanes for the same reason.
+// are spread over all lanes for the same reason; kept groups may leave fewer
+// lanes than top_k with one (one group of 64 of 512 experts is 4 lanes), and the
+// row then goes the slow way.
 template <int ELEM>
 hipError_t route_elem(const RouteArgs& a, hipStream_t stream) {
     if (a.experts <= 128 && a.top_k <= 8 && a.groups <= 16) return route_lanes<ELEM, 16>(a, stream);
