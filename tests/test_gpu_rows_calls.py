@@ -11,12 +11,12 @@ pytestmark = pytest.mark.gpu
 
 
 def busy(stream=None):
-    """Some milliseconds of copies on a stream."""
+    """Some fifty milliseconds of copies on a stream."""
     a = torch.empty(1 << 28, device=DEV)
     b = torch.empty_like(a)
     torch.cuda.synchronize()
     with torch.cuda.stream(stream or torch.cuda.current_stream()):
-        for _ in range(30):
+        for _ in range(120):
             b.copy_(a)
     return a, b
 
