@@ -22,6 +22,13 @@
  *   rs_group_choices        choices ordered by expert, stably, padded segments
  *   rs_token_logprobs       log probability, entropy, rank, top alternatives
  *   rs_token_logprobs_grad  gradient of those for the logits
+ *   rs_gather_choices       rows brought into the order of a grouping
+ *   rs_gather_choices_grad  gradients of that for the rows and the weights
+ *   rs_combine_choices      rows of a grouping summed back by their weights
+ *   rs_combine_choices_grad gradients of that
+ *   rs_embed_tokens         rows of a table by token, scaled
+ *   rs_embed_tokens_grad    the table's gradient, by sorted tokens
+ *   rs_adjust_logits        penalties of repeated tokens, biases, masks
  *   rs_status_string        text of a status code
  *
  * Common rules.
@@ -479,6 +486,139 @@ rs_status rs_token_logprobs_grad(rs_elem_type elem_type, const void *logits, uin
                                  const float *dentropy, const float *dlse, void *dlogits,
                                  uint64_t dlogits_stride, hipStream_t stream);
 
+/*
+ * Rows moved by index: a router's tokens to the order of their experts and
+ * back, and an embedding table's rows to their tokens and back.  Matrices are
+ * those of the calls on rows of scores; a row is `width` elements.  Sums and
+ * products of elements are f32 (or their fused multiply-add), rounded once to
+ * a matrix's type when stored; a sum's order depends on sizes and indexes
+ * only, so equal calls give equal bits.
+ *
+ * order [room] and place [rows, top_k] are those that rs_group_choices gave
+ * for ids [rows, top_k]: order_i is the choice at position i and place_c the
+ * position of choice c, each 0xFFFFFFFF (or anything that is no choice, or no
+ * position below room) where there is none.  order may end early: its first
+ * `room` elements alone make a call on the positions below room.  A call
+ * reads no row of y behind a position that place does not name, and what it
+ * writes by position is given by order alone, whatever place holds: rows
+ * without a choice are written as zeros.  (Where place does not name a
+ * choice's position in order, that row takes a slower way.)
+ */
+
+/*
+ * Gathering: y_i = w_c x_t for every position i < room, where c = order_i is
+ * a choice of row t = c / top_k; w_c = weights[c], or without weights (NULL) y_i
+ * is a copy.  Zeros where order_i is no choice.  x [rows, width], y [room,
+ * width], weights [rows, top_k] f32.
+ * 1 <= top_k <= RS_MAX_TOP_K, rows * top_k < 2^30, room < 2^30, 1 <= width <
+ * 2^30 and at most 2^40 elements in any matrix.  No temp.
+ */
+rs_status rs_gather_choices(rs_elem_type elem_type, const void *x, uint64_t x_stride,
+                            const uint32_t *order, uint64_t room, const uint32_t *place,
+                            const float *weights, uint64_t rows, uint32_t top_k, uint32_t width,
+                            void *y, uint64_t y_stride, hipStream_t stream);
+
+/*
+ * Gradients of rs_gather_choices with weights, of dy [room, width]:
+ *   dx_t  = sum over j of w_tj dy_(place_tj)      [rows, width]
+ *   dw_tj = the product of x_t and dy_(place_tj)  [rows, top_k] f32
+ * without the choices that have no place (their dw is 0).  Without weights
+ * the gradient is rs_combine_choices of dy without weights.
+ */
+rs_status rs_gather_choices_grad(rs_elem_type elem_type, const void *dy, uint64_t dy_stride,
+                                 uint64_t room, const void *x, uint64_t x_stride,
+                                 const uint32_t *place, const float *weights, uint64_t rows,
+                                 uint32_t top_k, uint32_t width, void *dx, uint64_t dx_stride,
+                                 float *dweights, hipStream_t stream);
+
+/*
+ * Combining: out_t = sum over j = 0, 1, ... of w_tj y_(place_tj), or without
+ * weights (NULL) of the rows themselves, without the choices that have no
+ * place; zeros for a row without any.  y [room, width], out [rows, width].
+ * Limits as for rs_gather_choices.  No temp.
+ */
+rs_status rs_combine_choices(rs_elem_type elem_type, const void *y, uint64_t y_stride, uint64_t room,
+                             const uint32_t *place, const float *weights, uint64_t rows,
+                             uint32_t top_k, uint32_t width, void *out, uint64_t out_stride,
+                             hipStream_t stream);
+
+/*
+ * Gradients of rs_combine_choices with weights, of dout [rows, width]:
+ *   dy_i  = w_c dout_t for the choice c = order_i of row t, zeros where there
+ *           is none                                [room, width]
+ *   dw_tj = the product of dout_t and y_(place_tj) [rows, top_k] f32, 0 for
+ *           a choice without place
+ * Without weights the gradient is rs_gather_choices of dout without weights.
+ */
+rs_status rs_combine_choices_grad(rs_elem_type elem_type, const void *dout, uint64_t dout_stride,
+                                  const void *y, uint64_t y_stride, const uint32_t *order,
+                                  uint64_t room, const uint32_t *place, const float *weights,
+                                  uint64_t rows, uint32_t top_k, uint32_t width, void *dy,
+                                  uint64_t dy_stride, float *dweights, hipStream_t stream);
+
+/*
+ * Embedding: out_i = scale * table[id_i] for i < n, zeros where id_i is
+ * `vocab` or above.  table [vocab, width], out [n, width].  With scale 1 the
+ * rows are copies.  vocab < 2^30, n < 2^30, scale finite; limits on width as
+ * for rs_gather_choices.  No temp.
+ */
+rs_status rs_embed_tokens(rs_elem_type elem_type, const void *table, uint64_t table_stride,
+                          const uint32_t *ids, uint64_t n, uint32_t vocab, uint32_t width,
+                          float scale, void *out, uint64_t out_stride, hipStream_t stream);
+
+/*
+ * Gradient of rs_embed_tokens for the table: dtable_v = scale * (the sum of
+ * dout_i over the i with id_i = v), plus with accumulate != 0 what dtable_v
+ * holds; rounded to table_type once.  The tokens are sorted (stably, by this
+ * library's sort) and the rows of each are summed in f32: runs of positions
+ * in order, then the runs.  dout [n, width] of elem_type (stride 0: one row
+ * for all); dtable [vocab, width] of table_type, which is elem_type or
+ * RS_ELEM_F32.  Without accumulate every element of dtable is written; with
+ * it the rows that have no token are left as they are.
+ * Temp with the query idiom; the size depends on n, vocab and width.
+ */
+rs_status rs_embed_tokens_grad(rs_elem_type elem_type, const void *dout, uint64_t dout_stride,
+                               const uint32_t *ids, uint64_t n, uint32_t vocab, uint32_t width,
+                               float scale, int accumulate, rs_elem_type table_type, void *dtable,
+                               uint64_t dtable_stride, void *d_temp, size_t *temp_bytes,
+                               hipStream_t stream);
+
+/*
+ * Adjusting logits before a token is chosen of them (or rs_token_logprobs
+ * scores them).  For the logit l of token v in row r, in f32, in this order:
+ *   if v occurs in the row's history: l / repetition[r] if l > 0, otherwise
+ *     l * repetition[r];
+ *   if it occurs c > 0 times behind the prompt: l - (frequency[r] * c +
+ *     presence[r]);
+ *   if the row's bias lists v: l + its bias, of the last entry that names v;
+ *   if the mask has v's bit clear: -inf, whatever l is.
+ * out gets l rounded to out_type once.
+ *   history [rows, history_len] tokens of row r, the first lengths[r] of them
+ *     (NULL: all; below 0 is 0, above history_len history_len), of which the
+ *     first prompt_lengths[r] (NULL: none) are the prompt; tokens of `vocab` or
+ *     above are passed over.  history, mask and the bias arrays have row
+ *     strides in elements, which may be any number (0: one row for all).
+ *   repetition (NULL: 1), presence, frequency (NULL: 0) [rows] f32, used as
+ *     they are.  Without history (NULL, with history_len 0) they and the
+ *     lengths are not read.
+ *   bias_ids, bias [rows, bias_len] (both NULL, with bias_len 0, or both
+ *     given): entries whose id is `vocab` or above are passed over.
+ *   mask [rows, (vocab + 31) / 32], or NULL: bit v % 32 of word v / 32, set
+ *     where v is allowed.
+ * out_type is elem_type or RS_ELEM_F32; out may be the logits themselves (with
+ * the same type and stride), otherwise the two must not overlap.  1 <= vocab <
+ * 2^30, rows, history_len and bias_len < 2^30.  No temp.
+ */
+rs_status rs_adjust_logits(rs_elem_type elem_type, const void *logits, uint64_t row_stride,
+                           uint64_t rows, uint32_t vocab, const uint32_t *history,
+                           uint64_t history_stride, uint64_t history_len, const int32_t *lengths,
+                           const int32_t *prompt_lengths, const float *repetition,
+                           const float *presence, const float *frequency, const uint32_t *bias_ids,
+                           uint64_t bias_ids_stride, const float *bias, uint64_t bias_stride,
+                           uint64_t bias_len, const uint32_t *mask, uint64_t mask_stride,
+                           rs_elem_type out_type, void *out, uint64_t out_stride,
+                           hipStream_t stream);
+
 /* Static text for a status code (never NULL). */
 const char *rs_status_string(rs_status status);
 
@@ -518,7 +658,14 @@ typedef enum rs_kernel_id {
     RS_KERNEL_GROUP_PLACE = 18, /* grouping: choices to their places */
     RS_KERNEL_LOGPROBS = 19,    /* one read of the logits: sums, rank, top alternatives */
     RS_KERNEL_LOGPROBS_JOIN = 20, /* joins the parts of rows that were split */
-    RS_KERNEL_LOGPROBS_GRAD = 21  /* the logits' gradient */
+    RS_KERNEL_LOGPROBS_GRAD = 21, /* the logits' gradient */
+    RS_KERNEL_GATHER = 22,      /* rows to the positions of a grouping */
+    RS_KERNEL_COMBINE = 23,     /* rows of a grouping summed by row, products for the weights */
+    RS_KERNEL_EMBED = 24,       /* rows of a table by token */
+    RS_KERNEL_EMBED_KEYS = 25,  /* tokens as sort keys, with their positions */
+    RS_KERNEL_EMBED_SUM = 26,   /* sums of rows by runs of sorted tokens */
+    RS_KERNEL_EMBED_JOIN = 27,  /* joins the sums of tokens in several runs */
+    RS_KERNEL_ADJUST = 28       /* penalties, biases and masks on logits */
 } rs_kernel_id;
 
 rs_status rs_timing_enable(int enable);

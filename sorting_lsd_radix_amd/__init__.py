@@ -9,15 +9,17 @@ storage with torch on the tensors' device and launch on torch's current
 stream; torch provides memory and streams only.
 
 The wrappers on rows of scores (``route_topk``, ``route_topk_grad``,
-``group_choices``, ``token_logprobs``, ``token_logprobs_grad``) take `stream`, a
-torch stream of the tensors' device or its address (0: the default stream; None:
-the current one).  Outputs are allocated on that stream, as a torch operation
+``group_choices``, ``token_logprobs``, ``token_logprobs_grad``, ``adjust_logits``)
+and on rows moved by index (``gather_choices``, ``combine_choices``,
+``embed_tokens`` and their ``_grad``) take `stream`, a torch stream of the
+tensors' device or its address (0: the default stream; None: the current one).
+Outputs are allocated on that stream, as a torch operation
 under it would, and what a call is given may be dropped at once; to order the
 stream behind what makes the inputs and before what uses the outputs is the
 caller's.  `temp`, a contiguous tensor of at least the size query's bytes on the
 tensors' device, is used by one call at a time.  None of them is part of torch's
 autograd: outputs have no gradient function, whatever the inputs require, and
-``route_topk_grad`` and ``token_logprobs_grad`` compute the gradients.
+the calls named ``_grad`` compute the gradients.
 
 Loading fails with an error when ``librs.so`` has not been built; there is no
 fallback implementation.  ``use_library(path)`` binds the functions to another
@@ -39,7 +41,11 @@ __all__ = [
     "RS_OP_NE", "RS_NO_TEMP", "RS_ELEM_F32", "RS_ELEM_F16", "RS_ELEM_BF16", "RS_SCORE_SOFTMAX",
     "RS_SCORE_SIGMOID", "rs_route_topk", "rs_route_topk_grad", "rs_group_choices",
     "rs_token_logprobs", "rs_token_logprobs_grad", "route_topk", "route_topk_grad",
-    "group_choices", "token_logprobs", "token_logprobs_grad", "TokenLogprobs", "rs_bitonic_tile", "rs_status_string", "rs_timing_enable", "rs_timing_collect",
+    "group_choices", "token_logprobs", "token_logprobs_grad", "TokenLogprobs",
+    "rs_gather_choices", "rs_gather_choices_grad", "rs_combine_choices", "rs_combine_choices_grad",
+    "rs_embed_tokens", "rs_embed_tokens_grad", "rs_adjust_logits", "gather_choices",
+    "gather_choices_grad", "combine_choices", "combine_choices_grad", "embed_tokens",
+    "embed_tokens_grad", "adjust_logits", "rs_bitonic_tile", "rs_status_string", "rs_timing_enable", "rs_timing_collect",
     "exclusive_scan_u32", "inclusive_scan_u32", "select", "partition",
     "sort_keys_u32", "sort_pairs_u32", "sort_pairs_f32", "sort_keys", "sort_pairs",
     "sort_two_keys_u32", "digit_counts", "compact_positive_f32", "bitonic_tile",
@@ -77,7 +83,9 @@ KERNEL_NAMES = {0: "upsweep", 1: "onesweep", 2: "sort_init", 3: "compact_init",
                 4: "compact", 5: "bitonic", 6: "copy", 7: "tile_sort", 8: "bucket_sort",
                 9: "scan_init", 10: "scan", 11: "select_init", 12: "select_count", 13: "select",
                 14: "route", 15: "route_grad", 16: "group_count", 17: "group_scan",
-                18: "group_place", 19: "logprobs", 20: "logprobs_join", 21: "logprobs_grad"}
+                18: "group_place", 19: "logprobs", 20: "logprobs_join", 21: "logprobs_grad",
+                22: "gather", 23: "combine", 24: "embed", 25: "embed_keys", 26: "embed_sum",
+                27: "embed_join", 28: "adjust"}
 
 RS_NO_TEMP = 16
 RS_ELEM_F32, RS_ELEM_F16, RS_ELEM_BF16 = range(3)
@@ -93,7 +101,10 @@ EXPORTED_SYMBOLS = ["rs_sort_keys_u32", "rs_sort_pairs_u32", "rs_sort_pairs_f32"
                     "rs_compact_positive_f32", "rs_compact_positive_f32_noalloc",
                     "rs_exclusive_scan_u32", "rs_inclusive_scan_u32", "rs_select", "rs_partition",
                     "rs_bitonic_tile", "rs_route_topk", "rs_route_topk_grad", "rs_group_choices",
-                    "rs_token_logprobs", "rs_token_logprobs_grad", "rs_status_string",
+                    "rs_token_logprobs", "rs_token_logprobs_grad", "rs_gather_choices",
+                    "rs_gather_choices_grad", "rs_combine_choices", "rs_combine_choices_grad",
+                    "rs_embed_tokens", "rs_embed_tokens_grad", "rs_adjust_logits",
+                    "rs_status_string",
                     "rs_timing_enable", "rs_timing_collect"]
 
 _lib = None
@@ -162,8 +173,21 @@ def _load():
                                       vp, vp, szp, vp]
     lib.rs_token_logprobs_grad.argtypes = [i32, vp, u64, vp, vp, vp, u64, u32, f32, vp, vp, vp, vp,
                                            u64, vp]
+    lib.rs_gather_choices.argtypes = [i32, vp, u64, vp, u64, vp, vp, u64, u32, u32, vp, u64, vp]
+    lib.rs_gather_choices_grad.argtypes = [i32, vp, u64, u64, vp, u64, vp, vp, u64, u32, u32, vp,
+                                           u64, vp, vp]
+    lib.rs_combine_choices.argtypes = [i32, vp, u64, u64, vp, vp, u64, u32, u32, vp, u64, vp]
+    lib.rs_combine_choices_grad.argtypes = [i32, vp, u64, vp, u64, vp, u64, vp, vp, u64, u32, u32,
+                                            vp, u64, vp, vp]
+    lib.rs_embed_tokens.argtypes = [i32, vp, u64, vp, u64, u32, u32, f32, vp, u64, vp]
+    lib.rs_embed_tokens_grad.argtypes = [i32, vp, u64, vp, u64, u32, u32, f32, i32, i32, vp, u64,
+                                         vp, szp, vp]
+    lib.rs_adjust_logits.argtypes = [i32, vp, u64, u64, u32, vp, u64, u64, vp, vp, vp, vp, vp, vp,
+                                     u64, vp, u64, u64, vp, u64, i32, vp, u64, vp]
     for f in (lib.rs_route_topk, lib.rs_route_topk_grad, lib.rs_group_choices,
-              lib.rs_token_logprobs, lib.rs_token_logprobs_grad):
+              lib.rs_token_logprobs, lib.rs_token_logprobs_grad, lib.rs_gather_choices,
+              lib.rs_gather_choices_grad, lib.rs_combine_choices, lib.rs_combine_choices_grad,
+              lib.rs_embed_tokens, lib.rs_embed_tokens_grad, lib.rs_adjust_logits):
         f.restype = i32
     lib.rs_status_string.argtypes = [i32]
     lib.rs_status_string.restype = ctypes.c_char_p
@@ -414,6 +438,87 @@ def rs_token_logprobs_grad(elem_type, logits, row_stride, targets, stats, entrop
                                         _ptr(dlse), _ptr(dlogits), int(dlogits_stride),
                                         _stream(stream))
     _call("rs_token_logprobs_grad", st)
+
+
+def rs_gather_choices(elem_type, x, x_stride, order, room, place, weights, rows, top_k, width, y,
+                      y_stride, stream=None):
+    """C: rs_gather_choices."""
+    _check_counts("rs_gather_choices", top_k | width)
+    st = _load().rs_gather_choices(int(elem_type), _ptr(x), int(x_stride), _ptr(order), int(room),
+                                   _ptr(place), _ptr(weights), int(rows), int(top_k), int(width),
+                                   _ptr(y), int(y_stride), _stream(stream))
+    _call("rs_gather_choices", st)
+
+
+def rs_gather_choices_grad(elem_type, dy, dy_stride, room, x, x_stride, place, weights, rows, top_k,
+                           width, dx, dx_stride, dweights, stream=None):
+    """C: rs_gather_choices_grad."""
+    _check_counts("rs_gather_choices_grad", top_k | width)
+    st = _load().rs_gather_choices_grad(int(elem_type), _ptr(dy), int(dy_stride), int(room), _ptr(x),
+                                        int(x_stride), _ptr(place), _ptr(weights), int(rows),
+                                        int(top_k), int(width), _ptr(dx), int(dx_stride),
+                                        _ptr(dweights), _stream(stream))
+    _call("rs_gather_choices_grad", st)
+
+
+def rs_combine_choices(elem_type, y, y_stride, room, place, weights, rows, top_k, width, out,
+                       out_stride, stream=None):
+    """C: rs_combine_choices."""
+    _check_counts("rs_combine_choices", top_k | width)
+    st = _load().rs_combine_choices(int(elem_type), _ptr(y), int(y_stride), int(room), _ptr(place),
+                                    _ptr(weights), int(rows), int(top_k), int(width), _ptr(out),
+                                    int(out_stride), _stream(stream))
+    _call("rs_combine_choices", st)
+
+
+def rs_combine_choices_grad(elem_type, dout, dout_stride, y, y_stride, order, room, place, weights,
+                            rows, top_k, width, dy, dy_stride, dweights, stream=None):
+    """C: rs_combine_choices_grad."""
+    _check_counts("rs_combine_choices_grad", top_k | width)
+    st = _load().rs_combine_choices_grad(int(elem_type), _ptr(dout), int(dout_stride), _ptr(y),
+                                         int(y_stride), _ptr(order), int(room), _ptr(place),
+                                         _ptr(weights), int(rows), int(top_k), int(width), _ptr(dy),
+                                         int(dy_stride), _ptr(dweights), _stream(stream))
+    _call("rs_combine_choices_grad", st)
+
+
+def rs_embed_tokens(elem_type, table, table_stride, ids, n, vocab, width, scale, out, out_stride,
+                    stream=None):
+    """C: rs_embed_tokens."""
+    _check_counts("rs_embed_tokens", vocab | width)
+    st = _load().rs_embed_tokens(int(elem_type), _ptr(table), int(table_stride), _ptr(ids), int(n),
+                                 int(vocab), int(width), float(scale), _ptr(out), int(out_stride),
+                                 _stream(stream))
+    _call("rs_embed_tokens", st)
+
+
+def rs_embed_tokens_grad(elem_type, dout, dout_stride, ids, n, vocab, width, scale, accumulate,
+                         table_type, dtable, dtable_stride, d_temp, temp_bytes, stream=None):
+    """C: rs_embed_tokens_grad.  With d_temp None, returns the temp size."""
+    _check_counts("rs_embed_tokens_grad", vocab | width)
+    size = ctypes.c_size_t(0 if temp_bytes is None else int(temp_bytes))
+    st = _load().rs_embed_tokens_grad(int(elem_type), _ptr(dout), int(dout_stride), _ptr(ids), int(n),
+                                      int(vocab), int(width), float(scale), int(bool(accumulate)),
+                                      int(table_type), _ptr(dtable), int(dtable_stride),
+                                      _ptr(d_temp), ctypes.byref(size),
+                                      _stream(stream) if d_temp is not None else None)
+    _call("rs_embed_tokens_grad", st)
+    return size.value if d_temp is None else None
+
+
+def rs_adjust_logits(elem_type, logits, row_stride, rows, vocab, history, history_stride, history_len,
+                     lengths, prompt_lengths, repetition, presence, frequency, bias_ids,
+                     bias_ids_stride, bias, bias_stride, bias_len, mask, mask_stride, out_type, out,
+                     out_stride, stream=None):
+    """C: rs_adjust_logits."""
+    _check_counts("rs_adjust_logits", vocab)
+    st = _load().rs_adjust_logits(int(elem_type), _ptr(logits), int(row_stride), int(rows), int(vocab),
+                                  _ptr(history), int(history_stride), int(history_len), _ptr(lengths),
+                                  _ptr(prompt_lengths), _ptr(repetition), _ptr(presence),
+                                  _ptr(frequency), _ptr(bias_ids), int(bias_ids_stride), _ptr(bias),
+                                  int(bias_stride), int(bias_len), _ptr(mask), int(mask_stride),
+                                  int(out_type), _ptr(out), int(out_stride), _stream(stream))
+    _call("rs_adjust_logits", st)
 
 
 def rs_timing_enable(enable):
@@ -914,3 +1019,270 @@ def token_logprobs_grad(logits, stats, targets=None, dlogprob=None, entropy=None
         return to
 
     return _run_on(index, stream, call, (logits, stats, targets, entropy, dlogprob, dentropy, dlse, out))
+
+
+# --- rows moved by index --------------------------------------------------------------
+
+def _choices(place, name, rows, index):
+    """(address, top_k) of a [rows, top_k] array of positions."""
+    if len(place.shape) != 2:
+        raise TypeError("%s must be of shape [rows, top_k]" % name)
+    return _check_like(place, name, (rows, place.shape[1]), _INTS, index), place.shape[1]
+
+
+def _order(order, index):
+    """(address, positions) of an order."""
+    return _check_like(order, "order", (order.numel(),), _INTS, index), order.numel()
+
+
+def _on_device(t, name, index):
+    if t.get_device() != index:
+        raise TypeError("%s must be on cuda:%d" % (name, index))
+
+
+def gather_choices(x, order, place, weights=None, out=None, stream=None):
+    """Rows of x [rows, width] (float32, float16 or bfloat16) in the order of a grouping: y [room,
+    width] of x's type with y[i] = x[order[i] // top_k], times weights.view(-1)[order[i]] with
+    weights (float32 [rows, top_k]), and zeros where order[i] is no choice (the padding).
+
+    order [room] and place [rows, top_k] are group_choices' (of the first positions alone, if order
+    is a slice of them).  `out`: a matrix whose rows are contiguous, to be written instead of a new
+    one.  No autograd: the gradient of a gathering without weights is combine_choices of dy, with
+    weights gather_choices_grad."""
+    torch = _load_torch()
+    et, rows, width, stride = _rows(x, "x")
+    index = x.get_device()
+    at_place, top_k = _choices(place, "place", rows, index)
+    at_order, room = _order(order, index)
+    _check_counts("rs_gather_choices", top_k | width)
+    at_w = None if weights is None else _check_like(weights, "weights", place.shape, (torch.float32,), index)
+    lib = _load()
+
+    def call(on):
+        to = torch.empty(room, width, dtype=x.dtype, device=x.device) if out is None else out
+        at, ostride = _check_out(to, "result", room, width, x.dtype, index)
+        _call("rs_gather_choices", lib.rs_gather_choices(
+            et, x.data_ptr(), stride, at_order, room, at_place, at_w, rows, top_k, width, at, ostride, on))
+        return to
+
+    return _run_on(index, stream, call, (x, order, place, weights, out))
+
+
+def gather_choices_grad(dy, x, place, weights, out=None, stream=None):
+    """Gradients of gather_choices with weights, of dy [room, width] of x's type: (dx [rows, width]
+    of x's type (`out`, if given), dweights float32 [rows, top_k])."""
+    torch = _load_torch()
+    et, rows, width, stride = _rows(x, "x")
+    index = x.get_device()
+    _, room, wide, dstride = _rows(dy, "dy", x.dtype)
+    _on_device(dy, "dy", index)
+    if wide != width:
+        raise TypeError("dy must have rows of %d elements, as x" % width)
+    at_place, top_k = _choices(place, "place", rows, index)
+    _check_counts("rs_gather_choices_grad", top_k | width)
+    at_w = _check_like(weights, "weights", place.shape, (torch.float32,), index)
+    lib = _load()
+
+    def call(on):
+        to = torch.empty(rows, width, dtype=x.dtype, device=x.device) if out is None else out
+        at, ostride = _check_out(to, "x", rows, width, x.dtype, index)
+        dw = torch.empty(rows, top_k, dtype=torch.float32, device=x.device)
+        _call("rs_gather_choices_grad", lib.rs_gather_choices_grad(
+            et, dy.data_ptr(), dstride, room, x.data_ptr(), stride, at_place, at_w, rows, top_k, width,
+            at, ostride, dw.data_ptr(), on))
+        return to, dw
+
+    return _run_on(index, stream, call, (dy, x, place, weights, out))
+
+
+def combine_choices(y, place, weights=None, out=None, stream=None):
+    """The rows of a grouping's y [room, width] summed back: out [rows, width] of y's type with
+    out[t] = the sum over j of y[place[t, j]], times weights[t, j] with weights (float32 [rows,
+    top_k]); choices without a place (-1, or no row of y) are left out.  Sums are float32.  `out`: a
+    matrix whose rows are contiguous.  No autograd: the gradient without weights is
+    gather_choices of dout, with weights combine_choices_grad."""
+    torch = _load_torch()
+    et, room, width, stride = _rows(y, "y")
+    index = y.get_device()
+    at_place, top_k = _choices(place, "place", place.shape[0] if len(place.shape) else 0, index)
+    rows = place.shape[0]
+    _check_counts("rs_combine_choices", top_k | width)
+    at_w = None if weights is None else _check_like(weights, "weights", place.shape, (torch.float32,), index)
+    lib = _load()
+
+    def call(on):
+        to = torch.empty(rows, width, dtype=y.dtype, device=y.device) if out is None else out
+        at, ostride = _check_out(to, "result", rows, width, y.dtype, index)
+        _call("rs_combine_choices", lib.rs_combine_choices(
+            et, y.data_ptr(), stride, room, at_place, at_w, rows, top_k, width, at, ostride, on))
+        return to
+
+    return _run_on(index, stream, call, (y, place, weights, out))
+
+
+def combine_choices_grad(dout, y, order, place, weights, out=None, stream=None):
+    """Gradients of combine_choices with weights, of dout [rows, width] of y's type: (dy [room,
+    width] of y's type, zeros where order has no choice (`out`, if given), dweights float32 [rows,
+    top_k], 0 for a choice without place)."""
+    torch = _load_torch()
+    et, room, width, stride = _rows(y, "y")
+    index = y.get_device()
+    _, rows, wide, dstride = _rows(dout, "dout", y.dtype)
+    _on_device(dout, "dout", index)
+    if wide != width:
+        raise TypeError("dout must have rows of %d elements, as y" % width)
+    at_place, top_k = _choices(place, "place", rows, index)
+    at_order = _check_like(order, "order", (room,), _INTS, index)
+    _check_counts("rs_combine_choices_grad", top_k | width)
+    at_w = _check_like(weights, "weights", place.shape, (torch.float32,), index)
+    lib = _load()
+
+    def call(on):
+        to = torch.empty(room, width, dtype=y.dtype, device=y.device) if out is None else out
+        at, ostride = _check_out(to, "y", room, width, y.dtype, index)
+        dw = torch.empty(rows, top_k, dtype=torch.float32, device=y.device)
+        _call("rs_combine_choices_grad", lib.rs_combine_choices_grad(
+            et, dout.data_ptr(), dstride, y.data_ptr(), stride, at_order, room, at_place, at_w, rows,
+            top_k, width, at, ostride, dw.data_ptr(), on))
+        return to, dw
+
+    return _run_on(index, stream, call, (dout, y, order, place, weights, out))
+
+
+def embed_tokens(table, ids, scale=1.0, out=None, stream=None):
+    """scale * table[ids] for a table [vocab, width] (float32, float16 or bfloat16) and ids (int32 or
+    uint32, any shape): [*ids.shape, width] of the table's type, zeros for ids outside the table
+    (-1).  `out`: a matrix [ids.numel(), width] whose rows are contiguous, to be written and
+    returned instead.  No autograd: embed_tokens_grad gives the table's gradient."""
+    torch = _load_torch()
+    et, vocab, width, stride = _rows(table, "table")
+    _check_counts("rs_embed_tokens", vocab | width)
+    index = table.get_device()
+    at_ids = _check_like(ids, "ids", ids.shape, _INTS, index)
+    n = ids.numel()
+    lib = _load()
+
+    def call(on):
+        to = torch.empty(*ids.shape, width, dtype=table.dtype, device=table.device) if out is None else out
+        at, ostride = (to.data_ptr(), width) if out is None else \
+            _check_out(to, "result", n, width, table.dtype, index)
+        _call("rs_embed_tokens", lib.rs_embed_tokens(
+            et, table.data_ptr(), stride, at_ids, n, vocab, width, scale, at, ostride, on))
+        return to
+
+    return _run_on(index, stream, call, (table, ids, out))
+
+
+def embed_tokens_grad(dout, ids, vocab, scale=1.0, dtype=None, accumulate=False, out=None, temp=None,
+                      stream=None):
+    """Gradient of embed_tokens for a table of `vocab` rows, of dout [*ids.shape, width] (or [ids.numel(),
+    width], as any view of one row stride): dtable [vocab, width], whose row v is scale times the sum
+    of the rows of dout whose id is v, in float32, rounded once to dtype (dout's, by default, or
+    float32); ids outside the table add nothing.  `out`: a matrix of that type whose rows are
+    contiguous, to be written and returned; with accumulate the gradient is added to what it holds."""
+    torch = _load_torch()
+    if dout.dim() != 2:
+        if dout.dim() != ids.dim() + 1:
+            raise TypeError("dout must be of shape [*ids.shape, width] or [ids.numel(), width]")
+        try:
+            dout = dout.view(ids.numel(), dout.shape[-1])
+        except RuntimeError:
+            raise TypeError("dout's rows must be one stride apart") from None
+    et, n, width, stride = _rows(dout, "dout")
+    _check_counts("rs_embed_tokens_grad", vocab | width)
+    index = dout.get_device()
+    if n != ids.numel():
+        raise TypeError("dout must have a row for each id")
+    at_ids = _check_like(ids, "ids", ids.shape, _INTS, index)
+    if dtype is None:
+        dtype = dout.dtype if out is None else out.dtype
+    if dtype not in (dout.dtype, torch.float32):
+        raise TypeError("the gradient must be of dout's type or float32")
+    if accumulate and out is None:
+        raise TypeError("accumulate adds to `out`, which must be given")
+    tt = _ELEMS[dtype]
+    lib = _load()
+    size = ctypes.c_size_t(0)
+    _call("rs_embed_tokens_grad", lib.rs_embed_tokens_grad(
+        et, None, stride, None, n, vocab, width, scale, 0, tt, None, 0, None, ctypes.byref(size), None))
+
+    def call(on):
+        to = torch.empty(vocab, width, dtype=dtype, device=dout.device) if out is None else out
+        at, ostride = _check_out(to, "table", vocab, width, dtype, index)
+        _keep, work, have = _temp_arg(temp, size, dout.device)
+        _call("rs_embed_tokens_grad", lib.rs_embed_tokens_grad(
+            et, dout.data_ptr(), stride, at_ids, n, vocab, width, scale, 1 if accumulate else 0, tt, at,
+            ostride, work, ctypes.byref(have), on))
+        return to
+
+    return _run_on(index, stream, call, (dout, ids, out, temp))
+
+
+def _lists(t, name, rows, cols, dtypes, index):
+    """(address, row stride) of a row's list of each row, whose elements are next to each other."""
+    if t.dtype not in dtypes or len(t.shape) != 2 or t.shape[0] != rows or \
+            (cols is not None and t.shape[1] != cols) or t.get_device() != index or \
+            (t.stride(1) != 1 and t.shape[1] > 1):
+        raise TypeError("%s must be a 2-D tensor of %d rows%s of %s on cuda:%d whose rows are contiguous"
+                        % (name, rows, "" if cols is None else " and %d columns" % cols,
+                           " or ".join(str(d) for d in dtypes), index))
+    return t.data_ptr(), t.stride(0)
+
+
+def adjust_logits(logits, history=None, lengths=None, prompt_lengths=None, repetition=None,
+                  presence=None, frequency=None, bias_ids=None, bias=None, mask=None, dtype=None,
+                  out=None, stream=None):
+    """Penalties, biases and masks on logits [rows, vocab] (float32, float16 or bfloat16), computed in
+    float32: [rows, vocab] of dtype (the logits' by default, or float32).
+
+    history (int32 or uint32 [rows, n]): each row's tokens so far, the first lengths (int32 [rows];
+    None: all) of them, of which the first prompt_lengths (int32 [rows]; None: none) are the prompt;
+    tokens outside the vocabulary (-1) are passed over.  A token of the history has its logit
+    divided (if positive) or multiplied by repetition (float32 [rows]); one that occurs c > 0 times
+    behind the prompt loses frequency * c + presence (float32 [rows] each).  Then bias (float32
+    [rows, m]) is added to the logits of bias_ids (int32 or uint32 [rows, m]; -1: none; of entries of
+    one token the last counts).  Last, tokens whose bit in mask (int32 or uint32 [rows, ceil(vocab /
+    32)], bit v % 32 of word v // 32) is clear get -inf.  The rows of history, bias_ids, bias and
+    mask may be any stride apart.  `out`: a matrix whose rows are contiguous, which may be the
+    logits themselves."""
+    torch = _load_torch()
+    et, rows, vocab, stride = _rows(logits, "logits")
+    _check_counts("rs_adjust_logits", vocab)
+    index = logits.get_device()
+    f32 = (torch.float32,)
+    at_history = at_ids = at_bias = at_mask = None
+    hstride = hlen = istride = bstride = blen = mstride = 0
+    if history is not None:
+        at_history, hstride = _lists(history, "history", rows, None, _INTS, index)
+        hlen = history.shape[1]
+    if (bias_ids is None) != (bias is None):
+        raise TypeError("bias_ids and bias must both be given")
+    if bias is not None:
+        at_ids, istride = _lists(bias_ids, "bias_ids", rows, None, _INTS, index)
+        blen = bias_ids.shape[1]
+        at_bias, bstride = _lists(bias, "bias", rows, blen, f32, index)
+    if mask is not None:
+        at_mask, mstride = _lists(mask, "mask", rows, (vocab + 31) // 32, _INTS, index)
+    at_rows = [None if t is None else _check_like(t, name, (rows,), of, index)
+               for t, name, of in ((lengths, "lengths", (torch.int32,)),
+                                   (prompt_lengths, "prompt_lengths", (torch.int32,)),
+                                   (repetition, "repetition", f32), (presence, "presence", f32),
+                                   (frequency, "frequency", f32))]
+    if history is None and at_rows != [None] * 5:
+        raise TypeError("lengths and penalties need a history")
+    if dtype is None:
+        dtype = logits.dtype if out is None else out.dtype
+    if dtype not in (logits.dtype, torch.float32):
+        raise TypeError("the result must be of the logits' type or float32")
+    lib = _load()
+
+    def call(on):
+        to = torch.empty(rows, vocab, dtype=dtype, device=logits.device) if out is None else out
+        at, ostride = _check_out(to, "logits", rows, vocab, dtype, index)
+        _call("rs_adjust_logits", lib.rs_adjust_logits(
+            et, logits.data_ptr(), stride, rows, vocab, at_history, hstride, hlen, *at_rows, at_ids,
+            istride, at_bias, bstride, blen, at_mask, mstride, _ELEMS[dtype], at, ostride, on))
+        return to
+
+    return _run_on(index, stream, call, (logits, history, lengths, prompt_lengths, repetition, presence,
+                                         frequency, bias_ids, bias, mask, out))

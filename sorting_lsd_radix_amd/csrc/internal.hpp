@@ -1,6 +1,6 @@
 // internal.hpp -- host-side interfaces between the C ABI (rs_api.cpp) and the
 // kernel launchers (radix.hip, compact.hip, scan.hip, bitonic.hip, route.hip,
-// group.hip, logprobs.hip).
+// group.hip, logprobs.hip, choices.hip, embed.hip, adjust.hip).
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -181,5 +181,84 @@ struct LogprobsGradArgs {
     uint64_t dlogits_stride;
 };
 hipError_t launch_logprobs_grad(int elem_type, const LogprobsGradArgs& a, hipStream_t stream);
+
+// ---- rows moved by index ----------------------------------------------------------
+
+// Arguments of the calls that move rows by index, as in rs.h; already validated.
+struct GatherArgs {
+    const void* x;
+    uint64_t x_stride;
+    const uint32_t* order;
+    const uint32_t* place;
+    const float* weights;   // or null
+    uint32_t room, rows, top_k, width;
+    void* y;
+    uint64_t y_stride;
+};
+hipError_t launch_gather(int elem_type, const GatherArgs& a, hipStream_t stream);
+
+// out_t = sum of w y (out not null), dots_tj = the product of x_t and y_(place_tj) (dots not null).
+struct CombineArgs {
+    const void* y;
+    uint64_t y_stride;
+    const void* x;
+    uint64_t x_stride;
+    const uint32_t* place;
+    const float* weights;   // or null
+    uint32_t room, rows, top_k, width;
+    void* out;
+    uint64_t out_stride;
+    float* dots;
+};
+hipError_t launch_combine(int elem_type, const CombineArgs& a, hipStream_t stream);
+
+struct EmbedArgs {
+    const void* table;
+    uint64_t table_stride;
+    const uint32_t* ids;
+    uint32_t n, vocab, width;
+    float scale;
+    void* out;
+    uint64_t out_stride;
+};
+hipError_t launch_embed(int elem_type, const EmbedArgs& a, hipStream_t stream);
+
+struct EmbedGradArgs {
+    const void* dout;
+    uint64_t dout_stride;
+    const uint32_t* ids;
+    uint32_t n, vocab, width;
+    float scale;
+    bool accumulate;
+    void* dtable;
+    uint64_t dtable_stride;
+};
+size_t embed_grad_temp_bytes(uint64_t n, uint32_t vocab, uint32_t width);
+hipError_t launch_embed_grad(int elem_type, int table_type, const EmbedGradArgs& a, void* temp,
+                             hipStream_t stream);
+
+struct AdjustArgs {
+    const void* logits;
+    uint64_t row_stride;
+    uint32_t rows, vocab;
+    const uint32_t* history;
+    uint64_t history_stride;
+    uint32_t history_len;
+    const int32_t* lengths;
+    const int32_t* prompt_lengths;
+    const float* repetition;
+    const float* presence;
+    const float* frequency;
+    const uint32_t* bias_ids;
+    uint64_t bias_ids_stride;
+    const float* bias;
+    uint64_t bias_stride;
+    uint32_t bias_len;
+    const uint32_t* mask;
+    uint64_t mask_stride;
+    void* out;
+    uint64_t out_stride;
+};
+hipError_t launch_adjust(int elem_type, int out_type, const AdjustArgs& a, hipStream_t stream);
 
 }  // namespace rs

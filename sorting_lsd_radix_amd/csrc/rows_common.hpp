@@ -1,5 +1,5 @@
 // rows_common.hpp -- loads, stores, order patterns and wave reductions shared
-// by the kernels on rows of scores (route.hip, logprobs.hip).
+// by the kernels on rows of scores and on rows moved by index.
 #pragma once
 
 #include "device_common.hpp"
@@ -113,6 +113,26 @@ __device__ __forceinline__ void store_some(T* at, uint32_t n, const float (&x)[V
 #pragma unroll
         for (uint32_t j = 0; j < V; ++j)
             if (j < n) at[j] = static_cast<T>(x[j]);
+    }
+}
+
+// V consecutive elements from `from` to `to`, of which the first `n` exist, bit
+// by bit; zeros if not `real`.
+template <int V, class T>
+__device__ __forceinline__ void copy_some(const T* from, bool real, T* to, uint32_t n) {
+    using S = SomeVec<V, T>;
+    if (n >= V) {
+        typename S::Part r[S::kParts] = {};
+        if (real) {
+#pragma unroll
+            for (int p = 0; p < S::kParts; ++p) r[p] = *reinterpret_cast<const typename S::Part*>(from + p * S::kEach);
+        }
+#pragma unroll
+        for (int p = 0; p < S::kParts; ++p) *reinterpret_cast<typename S::Part*>(to + p * S::kEach) = r[p];
+    } else {
+#pragma unroll
+        for (uint32_t j = 0; j < V; ++j)
+            if (j < n) to[j] = real ? from[j] : static_cast<T>(0.0f);
     }
 }
 

@@ -638,6 +638,261 @@ rs_status rs_token_logprobs_grad(rs_elem_type elem_type, const void* logits, uin
     return launch_logprobs_grad(elem_type, a, stream) == hipSuccess ? RS_OK : RS_ERR_HIP;
 }
 
+// ---- rows moved by index ----------------------------------------------------------
+
+extern "C++" {   // templates
+namespace rs {
+namespace {
+
+// A matrix of a call: its type, first element, stride and size.
+struct Matrix {
+    int elem_type;
+    const void* p;
+    uint64_t stride, rows;
+    uint32_t cols;
+    bool written;
+};
+
+// What every call on such matrices refuses; on RS_OK, bytes[i] from each one's
+// first element to behind its last.
+template <size_t N>
+rs_status check_matrices(const Matrix (&m)[N], uint64_t (&bytes)[N]) {
+    for (size_t i = 0; i < N; ++i) {
+        if (m[i].rows * m[i].cols > (uint64_t{1} << 40)) return RS_ERR_UNSUPPORTED_SIZE;
+        if (m[i].written && m[i].stride < m[i].cols && m[i].rows > 1) return RS_ERR_INVALID_VALUE;
+        if (!matrix_bytes(m[i].elem_type, m[i].rows, m[i].stride, m[i].cols, &bytes[i])) return RS_ERR_INVALID_VALUE;
+        if (m[i].rows > 0 && m[i].p == nullptr) return RS_ERR_INVALID_VALUE;
+    }
+    for (size_t i = 0; i < N; ++i)
+        if (m[i].rows > 0 && !matrix_aligned(m[i].elem_type, m[i].p)) return RS_ERR_MISALIGNED;
+    return RS_OK;
+}
+
+struct Part {
+    const void* p;
+    uint64_t bytes;
+};
+
+// Whether what a call writes meets what it reads or writes otherwise; inputs may share memory.
+template <size_t W, size_t R>
+bool written_overlap(const Part (&written)[W], const Part (&read)[R]) {
+    for (const Part& r : read) {
+        Buffers b;
+        for (const Part& w : written) b.add(w.p, w.bytes);
+        b.add(r.p, r.bytes);
+        if (b.overlap()) return true;
+    }
+    return false;
+}
+
+rs_status check_choices(int elem_type, uint64_t room, uint64_t rows, uint32_t top_k, uint32_t width) {
+    if (!elem_ok(elem_type)) return RS_ERR_INVALID_VALUE;
+    if (room >= RS_MAX_N || rows >= RS_MAX_N || top_k > RS_MAX_TOP_K || width >= RS_MAX_N ||
+        rows * top_k >= RS_MAX_N)
+        return RS_ERR_UNSUPPORTED_SIZE;
+    return top_k == 0 || width == 0 ? RS_ERR_INVALID_VALUE : RS_OK;
+}
+
+rs_status hip_status(hipError_t e) { return e == hipSuccess ? RS_OK : RS_ERR_HIP; }
+
+}  // namespace
+}  // namespace rs
+}  // extern "C++"
+
+rs_status rs_gather_choices(rs_elem_type elem_type, const void* x, uint64_t x_stride,
+                            const uint32_t* order, uint64_t room, const uint32_t* place,
+                            const float* weights, uint64_t rows, uint32_t top_k, uint32_t width,
+                            void* y, uint64_t y_stride, hipStream_t stream) {
+    using namespace rs;
+    rs_status st = check_choices(elem_type, room, rows, top_k, width);
+    if (st != RS_OK) return st;
+    const Matrix m[] = {{elem_type, x, x_stride, rows, width, false}, {elem_type, y, y_stride, room, width, true}};
+    uint64_t bytes[2];
+    st = check_matrices(m, bytes);
+    if (st != RS_OK) return st;
+    if ((room > 0 && order == nullptr) || (rows > 0 && place == nullptr)) return RS_ERR_INVALID_VALUE;
+    if (!aligned4(order) || !aligned4(place) || !aligned4(weights)) return RS_ERR_MISALIGNED;
+    const Part written[] = {{y, bytes[1]}};
+    const Part read[] = {{x, bytes[0]}, {order, room * 4}, {place, rows * top_k * 4}, {weights, rows * top_k * 4}};
+    if (written_overlap(written, read)) return RS_ERR_OVERLAP;
+    const GatherArgs a{x, x_stride, order, place, weights, static_cast<uint32_t>(room), static_cast<uint32_t>(rows),
+                       top_k, width, y, y_stride};
+    return hip_status(launch_gather(elem_type, a, stream));
+}
+
+rs_status rs_gather_choices_grad(rs_elem_type elem_type, const void* dy, uint64_t dy_stride,
+                                 uint64_t room, const void* x, uint64_t x_stride,
+                                 const uint32_t* place, const float* weights, uint64_t rows,
+                                 uint32_t top_k, uint32_t width, void* dx, uint64_t dx_stride,
+                                 float* dweights, hipStream_t stream) {
+    using namespace rs;
+    rs_status st = check_choices(elem_type, room, rows, top_k, width);
+    if (st != RS_OK) return st;
+    const Matrix m[] = {{elem_type, dy, dy_stride, room, width, false},
+                        {elem_type, x, x_stride, rows, width, false},
+                        {elem_type, dx, dx_stride, rows, width, true}};
+    uint64_t bytes[3];
+    st = check_matrices(m, bytes);
+    if (st != RS_OK) return st;
+    if (rows > 0 && (!place || !weights || !dweights)) return RS_ERR_INVALID_VALUE;
+    if (!aligned4(place) || !aligned4(weights) || !aligned4(dweights)) return RS_ERR_MISALIGNED;
+    const uint64_t choices = rows * top_k * 4;
+    const Part written[] = {{dx, bytes[2]}, {dweights, choices}};
+    const Part read[] = {{dy, bytes[0]}, {x, bytes[1]}, {place, choices}, {weights, choices}};
+    if (written_overlap(written, read)) return RS_ERR_OVERLAP;
+    const CombineArgs a{dy, dy_stride, x, x_stride, place, weights, static_cast<uint32_t>(room),
+                        static_cast<uint32_t>(rows), top_k, width, dx, dx_stride, dweights};
+    return hip_status(launch_combine(elem_type, a, stream));
+}
+
+rs_status rs_combine_choices(rs_elem_type elem_type, const void* y, uint64_t y_stride, uint64_t room,
+                             const uint32_t* place, const float* weights, uint64_t rows,
+                             uint32_t top_k, uint32_t width, void* out, uint64_t out_stride,
+                             hipStream_t stream) {
+    using namespace rs;
+    rs_status st = check_choices(elem_type, room, rows, top_k, width);
+    if (st != RS_OK) return st;
+    const Matrix m[] = {{elem_type, y, y_stride, room, width, false}, {elem_type, out, out_stride, rows, width, true}};
+    uint64_t bytes[2];
+    st = check_matrices(m, bytes);
+    if (st != RS_OK) return st;
+    if (rows > 0 && place == nullptr) return RS_ERR_INVALID_VALUE;
+    if (!aligned4(place) || !aligned4(weights)) return RS_ERR_MISALIGNED;
+    const Part written[] = {{out, bytes[1]}};
+    const Part read[] = {{y, bytes[0]}, {place, rows * top_k * 4}, {weights, rows * top_k * 4}};
+    if (written_overlap(written, read)) return RS_ERR_OVERLAP;
+    const CombineArgs a{y, y_stride, nullptr, 0, place, weights, static_cast<uint32_t>(room),
+                        static_cast<uint32_t>(rows), top_k, width, out, out_stride, nullptr};
+    return hip_status(launch_combine(elem_type, a, stream));
+}
+
+rs_status rs_combine_choices_grad(rs_elem_type elem_type, const void* dout, uint64_t dout_stride,
+                                  const void* y, uint64_t y_stride, const uint32_t* order,
+                                  uint64_t room, const uint32_t* place, const float* weights,
+                                  uint64_t rows, uint32_t top_k, uint32_t width, void* dy,
+                                  uint64_t dy_stride, float* dweights, hipStream_t stream) {
+    using namespace rs;
+    rs_status st = check_choices(elem_type, room, rows, top_k, width);
+    if (st != RS_OK) return st;
+    const Matrix m[] = {{elem_type, dout, dout_stride, rows, width, false},
+                        {elem_type, y, y_stride, room, width, false},
+                        {elem_type, dy, dy_stride, room, width, true}};
+    uint64_t bytes[3];
+    st = check_matrices(m, bytes);
+    if (st != RS_OK) return st;
+    if ((rows > 0 && (!place || !weights || !dweights)) || (room > 0 && !order)) return RS_ERR_INVALID_VALUE;
+    if (!aligned4(order) || !aligned4(place) || !aligned4(weights) || !aligned4(dweights)) return RS_ERR_MISALIGNED;
+    const uint64_t choices = rows * top_k * 4;
+    const Part written[] = {{dy, bytes[2]}, {dweights, choices}};
+    const Part read[] = {{dout, bytes[0]}, {y, bytes[1]}, {order, room * 4}, {place, choices}, {weights, choices}};
+    if (written_overlap(written, read)) return RS_ERR_OVERLAP;
+    const GatherArgs g{dout, dout_stride, order, place, weights, static_cast<uint32_t>(room),
+                       static_cast<uint32_t>(rows), top_k, width, dy, dy_stride};
+    const CombineArgs c{y, y_stride, dout, dout_stride, place, weights, static_cast<uint32_t>(room),
+                        static_cast<uint32_t>(rows), top_k, width, nullptr, 0, dweights};
+    const hipError_t e = launch_gather(elem_type, g, stream);
+    return hip_status(e == hipSuccess ? launch_combine(elem_type, c, stream) : e);
+}
+
+rs_status rs_embed_tokens(rs_elem_type elem_type, const void* table, uint64_t table_stride,
+                          const uint32_t* ids, uint64_t n, uint32_t vocab, uint32_t width,
+                          float scale, void* out, uint64_t out_stride, hipStream_t stream) {
+    using namespace rs;
+    if (!elem_ok(elem_type)) return RS_ERR_INVALID_VALUE;
+    if (n >= RS_MAX_N || vocab >= RS_MAX_N || width >= RS_MAX_N) return RS_ERR_UNSUPPORTED_SIZE;
+    if (vocab == 0 || width == 0 || !(scale - scale == 0.0f)) return RS_ERR_INVALID_VALUE;
+    const Matrix m[] = {{elem_type, table, table_stride, n > 0 ? vocab : 0u, width, false},
+                        {elem_type, out, out_stride, n, width, true}};
+    uint64_t bytes[2];
+    const rs_status st = check_matrices(m, bytes);
+    if (st != RS_OK) return st;
+    if (n == 0) return RS_OK;
+    if (ids == nullptr) return RS_ERR_INVALID_VALUE;
+    if (!aligned4(ids)) return RS_ERR_MISALIGNED;
+    const Part written[] = {{out, bytes[1]}};
+    const Part read[] = {{table, bytes[0]}, {ids, n * 4}};
+    if (written_overlap(written, read)) return RS_ERR_OVERLAP;
+    const EmbedArgs a{table, table_stride, ids, static_cast<uint32_t>(n), vocab, width, scale, out, out_stride};
+    return hip_status(launch_embed(elem_type, a, stream));
+}
+
+rs_status rs_embed_tokens_grad(rs_elem_type elem_type, const void* dout, uint64_t dout_stride,
+                               const uint32_t* ids, uint64_t n, uint32_t vocab, uint32_t width,
+                               float scale, int accumulate, rs_elem_type table_type, void* dtable,
+                               uint64_t dtable_stride, void* d_temp, size_t* temp_bytes,
+                               hipStream_t stream) {
+    using namespace rs;
+    if (temp_bytes == nullptr || !elem_ok(elem_type)) return RS_ERR_INVALID_VALUE;
+    if (table_type != elem_type && table_type != RS_ELEM_F32) return RS_ERR_INVALID_VALUE;
+    if (n >= RS_MAX_N || vocab >= RS_MAX_N || width >= RS_MAX_N || n * width > (uint64_t{1} << 40))
+        return RS_ERR_UNSUPPORTED_SIZE;
+    if (vocab == 0 || width == 0 || !(scale - scale == 0.0f)) return RS_ERR_INVALID_VALUE;
+    const size_t need = embed_grad_temp_bytes(n, vocab, width);
+    if (d_temp == nullptr) {
+        *temp_bytes = need;
+        return RS_OK;
+    }
+    const Matrix m[] = {{elem_type, dout, dout_stride, n, width, false},
+                        {table_type, dtable, dtable_stride, vocab, width, true}};
+    uint64_t bytes[2];
+    const rs_status st = check_matrices(m, bytes);
+    if (st != RS_OK) return st;
+    if (n > 0 && ids == nullptr) return RS_ERR_INVALID_VALUE;
+    if (!aligned4(ids) || !aligned16(d_temp)) return RS_ERR_MISALIGNED;
+    if (*temp_bytes < need) return RS_ERR_TEMP_TOO_SMALL;
+    const Part written[] = {{dtable, bytes[1]}, {d_temp, need}};
+    const Part read[] = {{dout, bytes[0]}, {ids, n * 4}};
+    if (written_overlap(written, read)) return RS_ERR_OVERLAP;
+    const EmbedGradArgs a{dout, dout_stride, ids, static_cast<uint32_t>(n), vocab, width, scale, accumulate != 0,
+                          dtable, dtable_stride};
+    return hip_status(launch_embed_grad(elem_type, table_type, a, d_temp, stream));
+}
+
+rs_status rs_adjust_logits(rs_elem_type elem_type, const void* logits, uint64_t row_stride,
+                           uint64_t rows, uint32_t vocab, const uint32_t* history,
+                           uint64_t history_stride, uint64_t history_len, const int32_t* lengths,
+                           const int32_t* prompt_lengths, const float* repetition,
+                           const float* presence, const float* frequency, const uint32_t* bias_ids,
+                           uint64_t bias_ids_stride, const float* bias, uint64_t bias_stride,
+                           uint64_t bias_len, const uint32_t* mask, uint64_t mask_stride,
+                           rs_elem_type out_type, void* out, uint64_t out_stride,
+                           hipStream_t stream) {
+    using namespace rs;
+    if (!elem_ok(elem_type) || (out_type != elem_type && out_type != RS_ELEM_F32)) return RS_ERR_INVALID_VALUE;
+    if (rows >= RS_MAX_N || vocab >= RS_MAX_N || history_len >= RS_MAX_N || bias_len >= RS_MAX_N)
+        return RS_ERR_UNSUPPORTED_SIZE;
+    if (vocab == 0) return RS_ERR_INVALID_VALUE;
+    if (!history && history_len > 0) return RS_ERR_INVALID_VALUE;
+    if ((bias_ids == nullptr) != (bias == nullptr) || (!bias && bias_len > 0)) return RS_ERR_INVALID_VALUE;
+    const Matrix m[] = {{elem_type, logits, row_stride, rows, vocab, false},
+                        {out_type, out, out_stride, rows, vocab, true}};
+    uint64_t bytes[2], lists[4];
+    const rs_status st = check_matrices(m, bytes);
+    if (st != RS_OK) return st;
+    const uint32_t words = (vocab + 31) / 32;
+    if (!matrix_bytes(RS_ELEM_F32, history ? rows : 0, history_stride, static_cast<uint32_t>(history_len), &lists[0]) ||
+        !matrix_bytes(RS_ELEM_F32, bias ? rows : 0, bias_ids_stride, static_cast<uint32_t>(bias_len), &lists[1]) ||
+        !matrix_bytes(RS_ELEM_F32, bias ? rows : 0, bias_stride, static_cast<uint32_t>(bias_len), &lists[2]) ||
+        !matrix_bytes(RS_ELEM_F32, mask ? rows : 0, mask_stride, words, &lists[3]))
+        return RS_ERR_INVALID_VALUE;
+    if (rows == 0) return RS_OK;
+    if (!aligned4(history) || !aligned4(lengths) || !aligned4(prompt_lengths) || !aligned4(repetition) ||
+        !aligned4(presence) || !aligned4(frequency) || !aligned4(bias_ids) || !aligned4(bias) || !aligned4(mask))
+        return RS_ERR_MISALIGNED;
+    const bool in_place = logits == out && elem_type == out_type && (row_stride == out_stride || rows == 1);
+    const Part written[] = {{out, bytes[1]}};
+    const Part read[] = {{in_place ? nullptr : logits, bytes[0]}, {history, lists[0]}, {lengths, rows * 4},
+                         {prompt_lengths, rows * 4}, {repetition, rows * 4}, {presence, rows * 4},
+                         {frequency, rows * 4}, {bias_ids, lists[1]}, {bias, lists[2]}, {mask, lists[3]}};
+    if (written_overlap(written, read)) return RS_ERR_OVERLAP;
+    const AdjustArgs a{logits, row_stride, static_cast<uint32_t>(rows), vocab,
+                       history, history_stride, static_cast<uint32_t>(history_len), lengths, prompt_lengths,
+                       repetition, presence, frequency,
+                       bias_ids, bias_ids_stride, bias, bias_stride, static_cast<uint32_t>(bias_len),
+                       mask, mask_stride, out, out_stride};
+    return hip_status(launch_adjust(elem_type, out_type, a, stream));
+}
+
 const char* rs_status_string(rs_status status) {
     switch (status) {
         case RS_OK: return "RS_OK: success";
