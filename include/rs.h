@@ -511,7 +511,7 @@ rs_status rs_token_logprobs_grad(rs_elem_type elem_type, const void *logits, uin
  * is a copy.  Zeros where order_i is no choice.  x [rows, width], y [room,
  * width], weights [rows, top_k] f32.
  * 1 <= top_k <= RS_MAX_TOP_K, rows * top_k < 2^30, room < 2^30, 1 <= width <
- * 2^30 and at most 2^40 elements in any matrix.  No temp.
+ * 2^30 and at most 2^38 elements in any matrix.  No temp.
  */
 rs_status rs_gather_choices(rs_elem_type elem_type, const void *x, uint64_t x_stride,
                             const uint32_t *order, uint64_t room, const uint32_t *place,

@@ -1,139 +1,455 @@
 // choices.hip -- a router's rows brought into the order of their experts, and
 // summed back by their weights, with the gradients of both.
-//
-// A wave moves a chunk of 64 vectors of 16 bytes of one row.
 #include "internal.hpp"
-#include "rows_common.hpp"
+#include "move_common.hpp"
 
 namespace rs {
 
 namespace {
 
-constexpr int kMoveBlock = 256;
-constexpr int kMoveWaves = kMoveBlock / kWave;
+// Rows of up to kNarrow vectors share a wave.
+constexpr uint32_t kNarrow = 32;
 
-// Elements of a 16-byte vector.
-template <class T>
-constexpr int kVec = 16 / sizeof(T);
+// ---- wide rows --------------------------------------------------------------------
 
-// y_i = w_c x_t, c = order_i, t = c / top_k: a wave for each chunk of a position's row.
-template <class T, bool WEIGHTS>
-__global__ __launch_bounds__(kMoveBlock) void gather_kernel(GatherArgs a, uint32_t chunks) {
-    constexpr int V = kVec<T>;
-    const uint64_t unit = static_cast<uint64_t>(block_id()) * kMoveWaves + threadIdx.x / kWave;
-    const uint64_t i = unit / chunks;
-    const uint32_t col = static_cast<uint32_t>(unit % chunks) * (kWave * V) + lane_id() * V;
-    if (i >= a.room || col >= a.width) return;
-    const uint32_t c = a.order[i];
-    const uint32_t left = a.width - col;
+// The rows of positions that the wave of their choice does not write: zeros
+// where there is no choice, and the row itself where place has another position.
+template <class T, int U, bool WEIGHTS, bool ONCE>
+__device__ __forceinline__ void fill_rows(const GatherArgs& a, uint32_t unit, uint32_t parts, uint32_t each) {
+    const uint32_t lane = lane_id();
+    const uint32_t part = unit % parts;
+    const uint32_t i = unit / parts * each + lane;
+    const bool here = lane < each && i < a.room;
+    const uint32_t c = here ? a.order[i] : 0u;
     const bool real = c < a.rows * a.top_k;
-    const T* from = static_cast<const T*>(a.x) + (real ? c / a.top_k : 0u) * a.x_stride + col;
-    T* to = static_cast<T*>(a.y) + i * a.y_stride + col;
-    if (WEIGHTS) {
-        float v[V] = {};
-        if (real) {
-            load_some<V>(from, left, 0.0f, v);
-            const float w = a.weights[c];
+    uint64_t todo = ballot(here && !(real && a.place[c] == i));
+    const RowPart<T, U> row(part, a.width);
+    while (todo) {
+        const uint32_t l = __builtin_ctzll(todo);
+        todo &= todo - 1;
+        const uint32_t cl = lane_value(c, l);
+        typename RowPart<T, U>::Vec r[U] = {};
+        if (cl < a.rows * a.top_k) {
+            row.load(static_cast<const T*>(a.x) + cl / a.top_k * a.x_stride, r);
+            if (WEIGHTS) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[j] *= w;
+                for (int u = 0; u < U; ++u) r[u] = scaled<T>(r[u], a.weights[cl]);
+            }
         }
-        store_some<V>(to, left, v);
-    } else {
-        copy_some<V>(from, real, to, left);
+        row.template store<ONCE>(static_cast<T*>(a.y) + (unit / parts * each + l) * a.y_stride, r);
     }
 }
 
-// A block for each row: out_t = sum of w y over the row's choices, dots_tj = x_t y.
-template <class T, bool WEIGHTS, bool OUT, bool DOTS>
-__global__ __launch_bounds__(kMoveBlock) void combine_kernel(CombineArgs a) {
+// A choice's position, and whether the order has it there.
+__device__ __forceinline__ bool owns(const uint32_t* order, uint32_t room, uint32_t p, uint32_t c) {
+    return p < room && order[p] == c;
+}
+
+// A wave for each part of a row, which it reads once and writes to all its
+// choices' positions; the first `fill` waves write the other positions, `each` a wave.
+template <class T, int U, bool WEIGHTS, bool ONCE>
+__global__ __launch_bounds__(kMoveBlock) void gather_kernel(GatherArgs a, uint32_t parts, uint32_t fill,
+                                                            uint32_t each) {
+    const uint32_t unit = block_id() * kMoveWaves + threadIdx.x / kWave;
+    if (unit < fill) return fill_rows<T, U, WEIGHTS, ONCE>(a, unit, parts, each);
+    const uint32_t t = (unit - fill) / parts, part = (unit - fill) % parts;
+    if (t >= a.rows) return;
+    const uint32_t lane = lane_id();
+    const uint32_t c = t * a.top_k + lane;
+    const RowPart<T, U> row(part, a.width);
+    typename RowPart<T, U>::Vec x[U];
+    row.load(static_cast<const T*>(a.x) + t * a.x_stride, x);
+    const uint32_t p = lane < a.top_k ? a.place[c] : ~0u;
+    const float w = WEIGHTS && lane < a.top_k ? a.weights[c] : 0.0f;
+    uint64_t todo = ballot(owns(a.order, a.room, p, c));
+    while (todo) {
+        const uint32_t l = __builtin_ctzll(todo);
+        todo &= todo - 1;
+        T* to = static_cast<T*>(a.y) + lane_value(p, l) * a.y_stride;
+        if (WEIGHTS) {
+            typename RowPart<T, U>::Vec r[U];
+            const float wl = lane_value(w, l);
+#pragma unroll
+            for (int u = 0; u < U; ++u) r[u] = scaled<T>(x[u], wl);
+            row.template store<ONCE>(to, r);
+        } else {
+            row.template store<ONCE>(to, x);
+        }
+    }
+}
+
+constexpr int kBatch = 8;   // choices whose rows are in flight together
+
+// A wave for each 64 vectors of a row: the sum of its choices' rows there.
+template <class T, bool WEIGHTS, bool ONCE>
+__global__ __launch_bounds__(kMoveBlock) void combine_kernel(CombineArgs a, uint32_t parts) {
+    using Row = RowPart<T, 1>;
+    constexpr int V = kVec<T>;
+    const uint32_t unit = block_id() * kMoveWaves + threadIdx.x / kWave;
+    const uint32_t t = unit / parts;
+    if (t >= a.rows) return;
+    const uint32_t lane = lane_id();
+    const Row row(unit % parts, a.width);
+    const uint32_t p = lane < a.top_k ? a.place[t * a.top_k + lane] : ~0u;
+    const float w = WEIGHTS && lane < a.top_k ? a.weights[t * a.top_k + lane] : 1.0f;
+    float sum[V] = {};
+    for (uint64_t todo = ballot(p < a.room); todo != 0;) {
+        typename Row::Vec r[kBatch][1];
+        float wl[kBatch];
+        uint32_t n = 0;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (todo == 0) break;
+            const uint32_t l = __builtin_ctzll(todo);
+            todo &= todo - 1;
+            wl[b] = lane_value(w, l);
+            row.template load<ONCE>(static_cast<const T*>(a.y) + lane_value(p, l) * a.y_stride, r[b]);
+            ++n;
+        }
+#pragma unroll
+        for (uint32_t b = 0; b < kBatch; ++b) {
+            if (b >= n) break;
+            float y[V];
+            widen<T>(r[b][0], y);
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[e] = WEIGHTS ? fmaf(wl[b], y[e], sum[e]) : sum[e] + y[e];
+        }
+    }
+    const typename Row::Vec out[1] = {narrow<T>(sum)};
+    row.store(static_cast<T*>(a.out) + t * a.out_stride, out);
+}
+
+// Gradients, WAVES waves a row: the products of x_t with the rows of y at its
+// choices, and beside them the sum of those rows by their weights (SUM), or x_t
+// times each weight at its choices' positions in g.y.
+template <class T, int WAVES, bool SUM, bool ONCE>
+__global__ __launch_bounds__(kMoveBlock, 4) void products_kernel(CombineArgs a, GatherArgs g, uint32_t fill,
+                                                                 uint32_t fill_parts, uint32_t each) {
+    using Row = RowPart<T, 1>;
     constexpr int V = kVec<T>;
     __shared__ float s_dots[kMoveWaves][RS_MAX_TOP_K];
-    const uint32_t t = block_id();
-    if (t >= a.rows) return;
     const uint32_t wave = threadIdx.x / kWave, lane = lane_id();
-    if (DOTS) {
-        s_dots[wave][lane] = 0.0f;
-        wave_fence();
+    if (!SUM && block_id() < fill) return fill_rows<T, 1, true, false>(g, block_id() * kMoveWaves + wave, fill_parts, each);
+    const uint32_t t = ((block_id() - fill) * kMoveWaves + wave) / WAVES;
+    const bool real = t < a.rows;
+    s_dots[wave][lane] = 0.0f;
+    wave_fence();
+    if (real) {
+        const uint32_t c = t * a.top_k + lane;
+        const uint32_t p = lane < a.top_k ? a.place[c] : ~0u;
+        const float w = lane < a.top_k ? a.weights[c] : 0.0f;
+        const uint64_t valid = ballot(p < a.room);
+        const uint64_t owned = SUM ? 0 : ballot(owns(g.order, g.room, p, c));
+        const uint32_t steps = (a.width + kWave * V - 1) / (kWave * V);
+        const T* x_row = static_cast<const T*>(a.x) + t * a.x_stride;
+        float dot[kBatch] = {};   // of the valid choices, in order
+        for (uint32_t s = wave % WAVES; s < steps; s += WAVES) {
+            const Row row(s, a.width);
+            const typename Row::Vec own = row.own_bits(s, 0);
+            typename Row::Vec xr[1];
+            row.load(x_row, xr);
+            float x[V], sum[V] = {};
+            for (uint64_t todo = valid; todo != 0;) {
+                typename Row::Vec r[kBatch][1];
+                uint32_t l[kBatch], n = 0;
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    if (todo == 0) break;
+                    l[b] = __builtin_ctzll(todo);
+                    todo &= todo - 1;
+                    row.template load<ONCE>(static_cast<const T*>(a.y) + lane_value(p, l[b]) * a.y_stride, r[b]);
+                    ++n;
+                }
+                widen<T>(xr[0] & own, x);
+#pragma unroll
+                for (uint32_t b = 0; b < kBatch; ++b) {
+                    if (b >= n) break;
+                    float y[V];
+                    const float wl = lane_value(w, l[b]);
+                    if (SUM) {
+                        widen<T>(r[b][0], y);
+#pragma unroll
+                        for (uint32_t e = 0; e < V; ++e) sum[e] = fmaf(wl, y[e], sum[e]);
+                    }
+                    widen<T>(r[b][0] & own, y);
+#pragma unroll
+                    for (uint32_t e = 0; e < V; ++e) dot[b] = fmaf(x[e], y[e], dot[b]);
+                }
+                if (a.top_k > kBatch) {
+#pragma unroll
+                    for (uint32_t b = 0; b < kBatch; ++b) {
+                        if (b >= n) break;
+                        const float d = lanes_sum(dot[b]);
+                        if (lane == 0) s_dots[wave][l[b]] += d;
+                        dot[b] = 0.0f;
+                    }
+                }
+            }
+            if (SUM) {
+                const typename Row::Vec v[1] = {narrow<T>(sum)};
+                row.store(static_cast<T*>(a.out) + t * a.out_stride, v);
+            } else {
+                for (uint64_t todo = owned; todo != 0; todo &= todo - 1) {
+                    const uint32_t b = __builtin_ctzll(todo);
+                    const typename Row::Vec v[1] = {scaled<T>(xr[0], lane_value(w, b))};
+                    row.store(static_cast<T*>(g.y) + lane_value(p, b) * g.y_stride, v);
+                }
+            }
+        }
+        if (a.top_k <= kBatch) {
+            uint64_t todo = valid;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (todo == 0) break;
+                const float d = lanes_sum(dot[b]);
+                if (lane == 0) s_dots[wave][__builtin_ctzll(todo)] = d;
+                todo &= todo - 1;
+            }
+        }
     }
-    const uint32_t* place = a.place + static_cast<uint64_t>(t) * a.top_k;
-    for (uint32_t col = threadIdx.x * V; col - lane * V < a.width; col += kMoveBlock * V) {
-        const uint32_t left = col < a.width ? a.width - col : 0u;
-        float sum[V], x[V];
+    if (WAVES > 1) __syncthreads();
+    else wave_fence();
+    if (real && wave % WAVES == 0 && lane < a.top_k) {
+        float d = 0.0f;
 #pragma unroll
-        for (int e = 0; e < V; ++e) sum[e] = x[e] = 0.0f;
-        if (DOTS) load_some<V>(static_cast<const T*>(a.x) + t * a.x_stride + col, left, 0.0f, x);
-        for (uint32_t j = 0; j < a.top_k; ++j) {
-            const uint32_t p = place[j];
-            if (p >= a.room) continue;
-            float y[V];
-            load_some<V>(static_cast<const T*>(a.y) + p * a.y_stride + col, left, 0.0f, y);
-            if (OUT) {
-                const float w = WEIGHTS ? a.weights[static_cast<uint64_t>(t) * a.top_k + j] : 1.0f;
+        for (int v = 0; v < WAVES; ++v) d += s_dots[wave + v][lane];
+        a.dots[t * a.top_k + lane] = d;
+    }
+}
+
+// ---- narrow rows: L lanes a row -----------------------------------------------------
+
+constexpr int kRowsEach = 4;   // positions of a group of lanes
+
+template <class T, int L, bool WEIGHTS>
+__device__ __forceinline__ void gather_narrow(const GatherArgs& a, uint32_t block) {
+    constexpr int V = kVec<T>;
+    constexpr uint32_t kGroups = kMoveBlock / L;
+    const uint32_t col = threadIdx.x % L * V;
+    if (col >= a.width) return;
+    const uint32_t left = a.width - col;
+    uint32_t c[kRowsEach];
+    uint64_t i = static_cast<uint64_t>(block) * (kGroups * kRowsEach) + threadIdx.x / L;
 #pragma unroll
-                for (int e = 0; e < V; ++e) sum[e] = WEIGHTS ? fmaf(w, y[e], sum[e]) : sum[e] + y[e];
+    for (int u = 0; u < kRowsEach; ++u) c[u] = i + u * kGroups < a.room ? a.order[i + u * kGroups] : ~0u;
+    float v[kRowsEach][V];
+#pragma unroll
+    for (int u = 0; u < kRowsEach; ++u, i += kGroups) {
+        if (i >= a.room) return;
+        const bool real = c[u] < a.rows * a.top_k;
+        const T* from = static_cast<const T*>(a.x) + (real ? c[u] / a.top_k : 0u) * a.x_stride + col;
+        T* to = static_cast<T*>(a.y) + i * a.y_stride + col;
+        if (WEIGHTS) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[u][e] = 0.0f;
+            if (real) {
+                load_some<V>(from, left, 0.0f, v[u]);
+                const float w = a.weights[c[u]];
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[u][e] *= w;
+            }
+            store_some<V>(to, left, v[u]);
+        } else {
+            copy_some<V>(from, real, to, left);
+        }
+    }
+}
+
+template <class T, int L, bool WEIGHTS, bool OUT, bool DOTS>
+__device__ __forceinline__ void combine_narrow(const CombineArgs& a, uint32_t block) {
+    constexpr int V = kVec<T>;
+    constexpr uint32_t kEach = 4;   // choices in flight
+    const uint32_t t = block * (kMoveBlock / L) + threadIdx.x / L;
+    if (t >= a.rows) return;
+    const uint32_t col = threadIdx.x % L * V;
+    const uint32_t left = col < a.width ? a.width - col : 0u;
+    float sum[V] = {}, x[V];
+    if (DOTS) load_some<V>(static_cast<const T*>(a.x) + t * a.x_stride + col, left, 0.0f, x);
+    for (uint32_t j0 = 0; j0 < a.top_k; j0 += kEach) {
+        uint32_t p[kEach];
+        float w[kEach], y[kEach][V];
+#pragma unroll
+        for (uint32_t b = 0; b < kEach; ++b) {
+            p[b] = j0 + b < a.top_k ? a.place[t * a.top_k + j0 + b] : ~0u;
+            w[b] = WEIGHTS && j0 + b < a.top_k ? a.weights[t * a.top_k + j0 + b] : 1.0f;
+        }
+#pragma unroll
+        for (uint32_t b = 0; b < kEach; ++b)
+            if (p[b] < a.room) load_some<V>(static_cast<const T*>(a.y) + p[b] * a.y_stride + col, left, 0.0f, y[b]);
+#pragma unroll
+        for (uint32_t b = 0; b < kEach; ++b) {
+            float dot = 0.0f;
+            if (p[b] < a.room) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    if (OUT) sum[e] = WEIGHTS ? fmaf(w[b], y[b][e], sum[e]) : sum[e] + y[b][e];
+                    if (DOTS) dot = fmaf(x[e], y[b][e], dot);
+                }
             }
             if (DOTS) {
-                float dot = 0.0f;
-#pragma unroll
-                for (int e = 0; e < V; ++e) dot = fmaf(x[e], y[e], dot);
-                dot = lanes_sum(dot);
-                if (lane == 0) s_dots[wave][j] += dot;
+                dot = lanes_sum<L>(dot);
+                if (threadIdx.x % L == 0 && j0 + b < a.top_k) a.dots[t * a.top_k + j0 + b] = dot;
             }
         }
-        if (OUT) store_some<V>(static_cast<T*>(a.out) + t * a.out_stride + col, left, sum);
     }
-    if (DOTS) {
-        __syncthreads();
-        if (threadIdx.x < a.top_k) {
-            float dot = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kMoveWaves; ++w) dot += s_dots[w][threadIdx.x];
-            a.dots[static_cast<uint64_t>(t) * a.top_k + threadIdx.x] = dot;
-        }
-    }
+    if (OUT) store_some<V>(static_cast<T*>(a.out) + t * a.out_stride + col, left, sum);
 }
 
+template <class T, int L, bool WEIGHTS>
+__global__ __launch_bounds__(kMoveBlock) void gather_narrow_kernel(GatherArgs a) {
+    gather_narrow<T, L, WEIGHTS>(a, block_id());
+}
+template <class T, int L, bool WEIGHTS>
+__global__ __launch_bounds__(kMoveBlock) void combine_narrow_kernel(CombineArgs a) {
+    combine_narrow<T, L, WEIGHTS, true, false>(a, block_id());
+}
+template <class T, int L, bool SUM>
+__global__ __launch_bounds__(kMoveBlock) void products_narrow_kernel(CombineArgs a, GatherArgs g, uint32_t fill) {
+    if (!SUM && block_id() < fill) gather_narrow<T, L, true>(g, block_id());
+    else combine_narrow<T, L, true, SUM, true>(a, block_id() - fill);
+}
+
+// ---- launches ---------------------------------------------------------------------
+
+template <class Launch>
+hipError_t timed(int id, hipStream_t stream, Launch launch) {
+    timing_before(stream, id);
+    launch();
+    const hipError_t e = hipGetLastError();
+    timing_after(stream);
+    return e;
+}
+
+// call(whether) as a constant.
+template <class Call>
+void pick(bool whether, Call call) {
+    if (whether) call(std::true_type{});
+    else call(std::false_type{});
+}
+
+uint64_t up(uint64_t n, uint64_t d) { return (n + d - 1) / d; }
+
+// Positions that a wave fills.  2176 positions of 4096 bf16 elements, most of
+// them padding: 5.5 us with 4, 6.7 with 16; 15005 of 1001 f32, none padding, 13.9
+// with 4, 13.0 with 16, the limit between them by the waves that it takes.
+uint32_t fill_each(uint64_t room, uint32_t parts) { return up(room, 16) * parts >= 2048 ? 16 : 4; }
+
 template <class T>
+uint64_t matrix_size(uint64_t rows, uint32_t width) {
+    return rows * width * sizeof(T);
+}
+
+// call(lanes a row) of a narrow row.
+template <class Call>
+hipError_t by_lanes(uint32_t vectors, Call call) {
+    if (vectors <= 4) return call(std::integral_constant<int, 4>{});
+    if (vectors <= 16) return call(std::integral_constant<int, 16>{});
+    return call(std::integral_constant<int, 32>{});
+}
+
+template <class T, bool WEIGHTS>
 hipError_t gather_of(const GatherArgs& a, hipStream_t stream) {
-    const uint32_t chunks = (a.width + kWave * kVec<T> - 1) / (kWave * kVec<T>);
-    const dim3 grid = many_blocks((static_cast<uint64_t>(a.room) * chunks + kMoveWaves - 1) / kMoveWaves);
-    timing_before(stream, RS_KERNEL_GATHER);
-    if (a.weights) gather_kernel<T, true><<<grid, kMoveBlock, 0, stream>>>(a, chunks);
-    else gather_kernel<T, false><<<grid, kMoveBlock, 0, stream>>>(a, chunks);
-    const hipError_t e = hipGetLastError();
-    timing_after(stream);
-    return e;
+    const uint32_t vectors = static_cast<uint32_t>(up(a.width, kVec<T>));
+    if (vectors <= kNarrow)
+        return by_lanes(vectors, [&](auto lanes) {
+            constexpr int L = decltype(lanes)::value;
+            return timed(RS_KERNEL_GATHER, stream, [&] {
+                gather_narrow_kernel<T, L, WEIGHTS><<<many_blocks(up(a.room, kMoveBlock / L * kRowsEach)), kMoveBlock, 0, stream>>>(a);
+            });
+        });
+    const Split s = split_rows(vectors, a.rows);
+    const uint32_t each = fill_each(a.room, s.parts);
+    const uint32_t fill = static_cast<uint32_t>(up(a.room, each) * s.parts);
+    const dim3 grid = many_blocks(up(fill + static_cast<uint64_t>(a.rows) * s.parts, kMoveWaves));
+    return timed(RS_KERNEL_GATHER, stream, [&] {
+        pick(large(matrix_size<T>(static_cast<uint64_t>(a.rows) * a.top_k, a.width)), [&](auto once) {
+            constexpr bool ONCE = decltype(once)::value;
+            const auto kernel = s.unroll == 1 ? gather_kernel<T, 1, WEIGHTS, ONCE> : s.unroll == 2 ? gather_kernel<T, 2, WEIGHTS, ONCE>
+                                                  : gather_kernel<T, 4, WEIGHTS, ONCE>;
+            kernel<<<grid, kMoveBlock, 0, stream>>>(a, s.parts, fill, each);
+        });
+    });
+}
+
+template <class T, bool WEIGHTS>
+hipError_t combine_of(const CombineArgs& a, hipStream_t stream) {
+    const uint32_t vectors = static_cast<uint32_t>(up(a.width, kVec<T>));
+    if (vectors <= kNarrow)
+        return by_lanes(vectors, [&](auto lanes) {
+            constexpr int L = decltype(lanes)::value;
+            return timed(RS_KERNEL_COMBINE, stream, [&] {
+                combine_narrow_kernel<T, L, WEIGHTS><<<many_blocks(up(a.rows, kMoveBlock / L)), kMoveBlock, 0, stream>>>(a);
+            });
+        });
+    const uint32_t parts = static_cast<uint32_t>(up(vectors, kWave));
+    return timed(RS_KERNEL_COMBINE, stream, [&] {
+        pick(large(matrix_size<T>(static_cast<uint64_t>(a.rows) * a.top_k, a.width)), [&](auto once) {
+            constexpr bool ONCE = decltype(once)::value;
+            combine_kernel<T, WEIGHTS, ONCE><<<many_blocks(up(static_cast<uint64_t>(a.rows) * parts, kMoveWaves)), kMoveBlock, 0,
+                                               stream>>>(a, parts);
+        });
+    });
+}
+
+template <class T, bool SUM>
+hipError_t products_of(const CombineArgs& a, const GatherArgs& g, hipStream_t stream) {
+    const uint32_t vectors = static_cast<uint32_t>(up(a.width, kVec<T>));
+    if (vectors <= kNarrow)
+        return by_lanes(vectors, [&](auto lanes) {
+            constexpr int L = decltype(lanes)::value;
+            const uint32_t fill = SUM ? 0 : static_cast<uint32_t>(up(g.room, kMoveBlock / L * kRowsEach));
+            return timed(RS_KERNEL_COMBINE, stream, [&] {
+                products_narrow_kernel<T, L, SUM><<<many_blocks(fill + up(a.rows, kMoveBlock / L)), kMoveBlock, 0, stream>>>(a, g, fill);
+            });
+        });
+    const uint32_t parts = static_cast<uint32_t>(up(vectors, kWave));
+    const uint32_t each = fill_each(g.room, parts);
+    const uint32_t fill = SUM ? 0 : static_cast<uint32_t>(up(up(g.room, each) * parts, kMoveWaves));
+    return timed(RS_KERNEL_COMBINE, stream, [&] {
+        pick(large(matrix_size<T>(static_cast<uint64_t>(a.rows) * a.top_k, a.width)), [&](auto once) {
+            constexpr bool ONCE = decltype(once)::value;
+            if (a.rows >= 16384)
+                products_kernel<T, 1, SUM, ONCE><<<many_blocks(fill + up(a.rows, kMoveWaves)), kMoveBlock, 0, stream>>>(a, g, fill, parts, each);
+            else
+                products_kernel<T, kMoveWaves, SUM, ONCE><<<many_blocks(fill + uint64_t{a.rows}), kMoveBlock, 0, stream>>>(a, g, fill, parts, each);
+        });
+    });
 }
 
 template <class T>
-hipError_t combine_of(const CombineArgs& a, hipStream_t stream) {
-    const auto kernel = !a.dots ? (a.weights ? combine_kernel<T, true, true, false> : combine_kernel<T, false, true, false>)
-                        : a.out ? combine_kernel<T, true, true, true>
-                                : combine_kernel<T, true, false, true>;
-    timing_before(stream, RS_KERNEL_COMBINE);
-    kernel<<<many_blocks(a.rows), kMoveBlock, 0, stream>>>(a);
-    const hipError_t e = hipGetLastError();
-    timing_after(stream);
-    return e;
+hipError_t combine_any(const CombineArgs& a, hipStream_t stream) {
+    if (a.dots) return products_of<T, true>(a, GatherArgs{}, stream);
+    return a.weights ? combine_of<T, true>(a, stream) : combine_of<T, false>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_gather(int elem_type, const GatherArgs& a, hipStream_t stream) {
     if (a.room == 0) return hipSuccess;
+    // without weights the rows are copied bit by bit, whatever they hold
+    if (!a.weights) return elem_type == RS_ELEM_F32 ? gather_of<float, false>(a, stream) : gather_of<_Float16, false>(a, stream);
     switch (elem_type) {
-        case RS_ELEM_F32: return gather_of<float>(a, stream);
-        case RS_ELEM_F16: return gather_of<_Float16>(a, stream);
-        default: return gather_of<__bf16>(a, stream);
+        case RS_ELEM_F32: return gather_of<float, true>(a, stream);
+        case RS_ELEM_F16: return gather_of<_Float16, true>(a, stream);
+        default: return gather_of<__bf16, true>(a, stream);
     }
 }
 
 hipError_t launch_combine(int elem_type, const CombineArgs& a, hipStream_t stream) {
     if (a.rows == 0) return hipSuccess;
     switch (elem_type) {
-        case RS_ELEM_F32: return combine_of<float>(a, stream);
-        case RS_ELEM_F16: return combine_of<_Float16>(a, stream);
-        default: return combine_of<__bf16>(a, stream);
+        case RS_ELEM_F32: return combine_any<float>(a, stream);
+        case RS_ELEM_F16: return combine_any<_Float16>(a, stream);
+        default: return combine_any<__bf16>(a, stream);
+    }
+}
+
+hipError_t launch_combine_grad(int elem_type, const CombineArgs& a, const GatherArgs& g, hipStream_t stream) {
+    if (a.rows == 0 && g.room == 0) return hipSuccess;
+    switch (elem_type) {
+        case RS_ELEM_F32: return products_of<float, false>(a, g, stream);
+        case RS_ELEM_F16: return products_of<_Float16, false>(a, g, stream);
+        default: return products_of<__bf16, false>(a, g, stream);
     }
 }
 

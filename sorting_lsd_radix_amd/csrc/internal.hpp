@@ -197,7 +197,7 @@ struct GatherArgs {
 };
 hipError_t launch_gather(int elem_type, const GatherArgs& a, hipStream_t stream);
 
-// out_t = sum of w y (out not null), dots_tj = the product of x_t and y_(place_tj) (dots not null).
+// out_t = sum of w y, and dots_tj = the product of x_t and y_(place_tj) (dots not null).
 struct CombineArgs {
     const void* y;
     uint64_t y_stride;
@@ -211,6 +211,9 @@ struct CombineArgs {
     float* dots;
 };
 hipError_t launch_combine(int elem_type, const CombineArgs& a, hipStream_t stream);
+
+// The products of `a`, and g: the rows of g.x, a.x again, to the positions of g.order.
+hipError_t launch_combine_grad(int elem_type, const CombineArgs& a, const GatherArgs& g, hipStream_t stream);
 
 struct EmbedArgs {
     const void* table;

@@ -1,0 +1,120 @@
+// move_common.hpp -- parts of rows in registers, shared by the kernels that
+// move rows by index (choices.hip, embed.hip).
+#pragma once
+
+#include "rows_common.hpp"
+
+namespace rs {
+
+constexpr int kMoveBlock = 256;
+constexpr int kMoveWaves = kMoveBlock / kWave;
+
+// Elements of a 16-byte vector.
+template <class T>
+constexpr int kVec = 16 / sizeof(T);
+
+// The value of lane `from`, the same lane for the whole wave.
+__device__ __forceinline__ uint32_t lane_value(uint32_t x, uint32_t from) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), static_cast<int>(from)));
+}
+__device__ __forceinline__ float lane_value(float x, uint32_t from) {
+    return __uint_as_float(lane_value(__float_as_uint(x), from));
+}
+
+// A lane's U vectors of a row of at least one vector, 64 vectors apart.  The
+// row's last vector begins where the row has a whole one left, so it may hold
+// elements of the one before it: those are moved twice, with the same values.
+template <class T, int U>
+struct RowPart {
+    static constexpr int V = kVec<T>;
+    using Vec = AnyVec<16>::V;
+    uint32_t at[U];     // first element
+    bool real[U];       // whether the row has this vector
+
+    __device__ __forceinline__ RowPart(uint32_t part, uint32_t width) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t c = ((part * U + u) * kWave + lane_id()) * V;
+            real[u] = c < width;
+            at[u] = c < width - V ? c : width - V;
+        }
+    }
+    // Bits of vector u's elements that are its own, and not of the one before it
+    // as well; none where the row has no such vector.
+    __device__ __forceinline__ Vec own_bits(uint32_t part, int u) const {
+        const uint32_t twice = real[u] ? ((part * U + u) * kWave + lane_id()) * V - at[u] : V;
+        Vec m;
+#pragma unroll
+        for (uint32_t d = 0; d < 4; ++d) {
+            if constexpr (sizeof(T) == 4) m[d] = d < twice ? 0u : ~0u;
+            else m[d] = 2 * d + 1 < twice ? 0u : 2 * d < twice ? 0xFFFF0000u : ~0u;
+        }
+        return m;
+    }
+    // ONCE: past the caches, for what is too large to be found there again.
+    template <bool ONCE = false>
+    __device__ __forceinline__ void load(const T* row, Vec (&r)[U]) const {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!real[u]) continue;
+            const Vec* from = reinterpret_cast<const Vec*>(row + at[u]);
+            r[u] = ONCE ? __builtin_nontemporal_load(from) : *from;
+        }
+    }
+    template <bool ONCE = false>
+    __device__ __forceinline__ void store(T* row, const Vec (&r)[U]) const {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!real[u]) continue;
+            Vec* to = reinterpret_cast<Vec*>(row + at[u]);
+            if (ONCE) __builtin_nontemporal_store(r[u], to);
+            else *to = r[u];
+        }
+    }
+};
+
+// A vector's elements as f32, and back.
+template <class T>
+__device__ __forceinline__ void widen(AnyVec<16>::V r, float (&x)[kVec<T>]) {
+    const auto e = __builtin_bit_cast(typename SomeVec<kVec<T>, T>::Elems, r);
+#pragma unroll
+    for (int j = 0; j < kVec<T>; ++j) x[j] = static_cast<float>(e.v[j]);
+}
+template <class T>
+__device__ __forceinline__ AnyVec<16>::V narrow(const float (&x)[kVec<T>]) {
+    typename SomeVec<kVec<T>, T>::Elems e;
+#pragma unroll
+    for (int j = 0; j < kVec<T>; ++j) e.v[j] = static_cast<T>(x[j]);
+    return __builtin_bit_cast(AnyVec<16>::V, e);
+}
+// A vector times w, rounded.
+template <class T>
+__device__ __forceinline__ AnyVec<16>::V scaled(AnyVec<16>::V r, float w) {
+    float x[kVec<T>];
+    widen<T>(r, x);
+#pragma unroll
+    for (int j = 0; j < kVec<T>; ++j) x[j] *= w;
+    return narrow<T>(x);
+}
+
+// Whether the rows moved by position are read or written past the caches: the
+// 256 MB on-package cache would not hold them until they are used, nor what else is
+// used meanwhile.  A router's rows gathered, passed through an elementwise kernel
+// and combined: 128 MB take 89.5 us by the caches and 91.2 past them, 256 MB 196 and
+// 188, 512 MB 426 and 388; 192 MB combined with their gradients, other rows in
+// between, 142 and 120.
+inline bool large(uint64_t bytes) { return bytes > (uint64_t{128} << 20); }
+
+// How rows are split among waves: vectors of a lane (1, 2 or 4, so many that the
+// parts still fill the chip: 8192 waves), and parts of a row.
+struct Split {
+    uint32_t unroll, parts;
+};
+inline Split split_rows(uint32_t vectors, uint64_t rows) {
+    const uint32_t each = (vectors + kWave - 1) / kWave;   // vectors of a lane, were a row one wave's
+    uint32_t u = 1;
+    while (u < 4 && u < each && rows * ((each + 2 * u - 1) / (2 * u)) >= 8192) u *= 2;
+    return Split{u, (each + u - 1) / u};
+}
+
+}  // namespace rs

@@ -658,7 +658,7 @@ struct Matrix {
 template <size_t N>
 rs_status check_matrices(const Matrix (&m)[N], uint64_t (&bytes)[N]) {
     for (size_t i = 0; i < N; ++i) {
-        if (m[i].rows * m[i].cols > (uint64_t{1} << 40)) return RS_ERR_UNSUPPORTED_SIZE;
+        if (m[i].rows * m[i].cols > (uint64_t{1} << 38)) return RS_ERR_UNSUPPORTED_SIZE;
         if (m[i].written && m[i].stride < m[i].cols && m[i].rows > 1) return RS_ERR_INVALID_VALUE;
         if (!matrix_bytes(m[i].elem_type, m[i].rows, m[i].stride, m[i].cols, &bytes[i])) return RS_ERR_INVALID_VALUE;
         if (m[i].rows > 0 && m[i].p == nullptr) return RS_ERR_INVALID_VALUE;
@@ -790,8 +790,7 @@ rs_status rs_combine_choices_grad(rs_elem_type elem_type, const void* dout, uint
                        static_cast<uint32_t>(rows), top_k, width, dy, dy_stride};
     const CombineArgs c{y, y_stride, dout, dout_stride, place, weights, static_cast<uint32_t>(room),
                         static_cast<uint32_t>(rows), top_k, width, nullptr, 0, dweights};
-    const hipError_t e = launch_gather(elem_type, g, stream);
-    return hip_status(e == hipSuccess ? launch_combine(elem_type, c, stream) : e);
+    return hip_status(launch_combine_grad(elem_type, c, g, stream));
 }
 
 rs_status rs_embed_tokens(rs_elem_type elem_type, const void* table, uint64_t table_stride,
@@ -824,7 +823,7 @@ rs_status rs_embed_tokens_grad(rs_elem_type elem_type, const void* dout, uint64_
     using namespace rs;
     if (temp_bytes == nullptr || !elem_ok(elem_type)) return RS_ERR_INVALID_VALUE;
     if (table_type != elem_type && table_type != RS_ELEM_F32) return RS_ERR_INVALID_VALUE;
-    if (n >= RS_MAX_N || vocab >= RS_MAX_N || width >= RS_MAX_N || n * width > (uint64_t{1} << 40))
+    if (n >= RS_MAX_N || vocab >= RS_MAX_N || width >= RS_MAX_N || n * width > (uint64_t{1} << 38))
         return RS_ERR_UNSUPPORTED_SIZE;
     if (vocab == 0 || width == 0 || !(scale - scale == 0.0f)) return RS_ERR_INVALID_VALUE;
     const size_t need = embed_grad_temp_bytes(n, vocab, width);
