@@ -14,7 +14,7 @@ constexpr uint32_t kNarrow = 32;
 
 // The rows of positions that the wave of their choice does not write: zeros
 // where there is no choice, and the row itself where place has another position.
-template <class T, int U, bool WEIGHTS, bool ONCE>
+template <class T, int U, bool WEIGHTS>
 __device__ __forceinline__ void fill_rows(const GatherArgs& a, uint32_t unit, uint32_t parts, uint32_t each) {
     const uint32_t lane = lane_id();
     const uint32_t part = unit % parts;
@@ -36,7 +36,7 @@ __device__ __forceinline__ void fill_rows(const GatherArgs& a, uint32_t unit, ui
                 for (int u = 0; u < U; ++u) r[u] = scaled<T>(r[u], a.weights[cl]);
             }
         }
-        row.template store<ONCE>(static_cast<T*>(a.y) + (unit / parts * each + l) * a.y_stride, r);
+        row.store(static_cast<T*>(a.y) + (unit / parts * each + l) * a.y_stride, r);
     }
 }
 
@@ -47,11 +47,11 @@ __device__ __forceinline__ bool owns(const uint32_t* order, uint32_t room, uint3
 
 // A wave for each part of a row, which it reads once and writes to all its
 // choices' positions; the first `fill` waves write the other positions, `each` a wave.
-template <class T, int U, bool WEIGHTS, bool ONCE>
+template <class T, int U, bool WEIGHTS>
 __global__ __launch_bounds__(kMoveBlock) void gather_kernel(GatherArgs a, uint32_t parts, uint32_t fill,
                                                             uint32_t each) {
     const uint32_t unit = block_id() * kMoveWaves + threadIdx.x / kWave;
-    if (unit < fill) return fill_rows<T, U, WEIGHTS, ONCE>(a, unit, parts, each);
+    if (unit < fill) return fill_rows<T, U, WEIGHTS>(a, unit, parts, each);
     const uint32_t t = (unit - fill) / parts, part = (unit - fill) % parts;
     if (t >= a.rows) return;
     const uint32_t lane = lane_id();
@@ -71,9 +71,9 @@ __global__ __launch_bounds__(kMoveBlock) void gather_kernel(GatherArgs a, uint32
             const float wl = lane_value(w, l);
 #pragma unroll
             for (int u = 0; u < U; ++u) r[u] = scaled<T>(x[u], wl);
-            row.template store<ONCE>(to, r);
+            row.store(to, r);
         } else {
-            row.template store<ONCE>(to, x);
+            row.store(to, x);
         }
     }
 }
@@ -122,14 +122,14 @@ __global__ __launch_bounds__(kMoveBlock) void combine_kernel(CombineArgs a, uint
 // Gradients, WAVES waves a row: the products of x_t with the rows of y at its
 // choices, and beside them the sum of those rows by their weights (SUM), or x_t
 // times each weight at its choices' positions in g.y.
-template <class T, int WAVES, bool SUM, bool ONCE>
+template <class T, int WAVES, bool SUM>
 __global__ __launch_bounds__(kMoveBlock, 4) void products_kernel(CombineArgs a, GatherArgs g, uint32_t fill,
                                                                  uint32_t fill_parts, uint32_t each) {
     using Row = RowPart<T, 1>;
     constexpr int V = kVec<T>;
     __shared__ float s_dots[kMoveWaves][RS_MAX_TOP_K];
     const uint32_t wave = threadIdx.x / kWave, lane = lane_id();
-    if (!SUM && block_id() < fill) return fill_rows<T, 1, true, false>(g, block_id() * kMoveWaves + wave, fill_parts, each);
+    if (!SUM && block_id() < fill) return fill_rows<T, 4, true>(g, block_id() * kMoveWaves + wave, fill_parts, each);
     const uint32_t t = ((block_id() - fill) * kMoveWaves + wave) / WAVES;
     const bool real = t < a.rows;
     s_dots[wave][lane] = 0.0f;
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(kMoveBlock, 4) void products_kernel(CombineArgs a, 
                     if (todo == 0) break;
                     l[b] = __builtin_ctzll(todo);
                     todo &= todo - 1;
-                    row.template load<ONCE>(static_cast<const T*>(a.y) + lane_value(p, l[b]) * a.y_stride, r[b]);
+                    row.load(static_cast<const T*>(a.y) + lane_value(p, l[b]) * a.y_stride, r[b]);
                     ++n;
                 }
                 widen<T>(xr[0] & own, x);
@@ -329,15 +329,12 @@ void pick(bool whether, Call call) {
 
 uint64_t up(uint64_t n, uint64_t d) { return (n + d - 1) / d; }
 
-// Positions that a wave fills.  2176 positions of 4096 bf16 elements, most of
-// them padding: 5.5 us with 4, 6.7 with 16; 15005 of 1001 f32, none padding, 13.9
-// with 4, 13.0 with 16, the limit between them by the waves that it takes.
-uint32_t fill_each(uint64_t room, uint32_t parts) { return up(room, 16) * parts >= 2048 ? 16 : 4; }
-
-template <class T>
-uint64_t matrix_size(uint64_t rows, uint32_t width) {
-    return rows * width * sizeof(T);
-}
+// Positions that a wave fills: few where there is padding, which is all that it
+// writes, many where there is none and it only looks.  131072 choices in 163584
+// positions of 4096 bf16 elements: 295 us with 4, 305 with 16; without padding, 15005
+// positions of 1001 f32: 16.8 us with 4, 15.8 with 16; 2176 positions, most of them
+// padding: 5.5 us with 4, 6.7 with 16.
+uint32_t fill_each(uint64_t room, uint64_t choices) { return room > choices + choices / 16 ? 4 : 16; }
 
 // call(lanes a row) of a narrow row.
 template <class Call>
@@ -358,16 +355,13 @@ hipError_t gather_of(const GatherArgs& a, hipStream_t stream) {
             });
         });
     const Split s = split_rows(vectors, a.rows);
-    const uint32_t each = fill_each(a.room, s.parts);
+    const uint32_t each = fill_each(a.room, static_cast<uint64_t>(a.rows) * a.top_k);
     const uint32_t fill = static_cast<uint32_t>(up(a.room, each) * s.parts);
     const dim3 grid = many_blocks(up(fill + static_cast<uint64_t>(a.rows) * s.parts, kMoveWaves));
     return timed(RS_KERNEL_GATHER, stream, [&] {
-        pick(large(matrix_size<T>(static_cast<uint64_t>(a.rows) * a.top_k, a.width)), [&](auto once) {
-            constexpr bool ONCE = decltype(once)::value;
-            const auto kernel = s.unroll == 1 ? gather_kernel<T, 1, WEIGHTS, ONCE> : s.unroll == 2 ? gather_kernel<T, 2, WEIGHTS, ONCE>
-                                                  : gather_kernel<T, 4, WEIGHTS, ONCE>;
-            kernel<<<grid, kMoveBlock, 0, stream>>>(a, s.parts, fill, each);
-        });
+        const auto kernel = s.unroll == 1 ? gather_kernel<T, 1, WEIGHTS> : s.unroll == 2 ? gather_kernel<T, 2, WEIGHTS>
+                                                                                         : gather_kernel<T, 4, WEIGHTS>;
+        kernel<<<grid, kMoveBlock, 0, stream>>>(a, s.parts, fill, each);
     });
 }
 
@@ -383,7 +377,7 @@ hipError_t combine_of(const CombineArgs& a, hipStream_t stream) {
         });
     const uint32_t parts = static_cast<uint32_t>(up(vectors, kWave));
     return timed(RS_KERNEL_COMBINE, stream, [&] {
-        pick(large(matrix_size<T>(static_cast<uint64_t>(a.rows) * a.top_k, a.width)), [&](auto once) {
+        pick(large(static_cast<uint64_t>(a.rows) * a.top_k * a.width * sizeof(T)), [&](auto once) {
             constexpr bool ONCE = decltype(once)::value;
             combine_kernel<T, WEIGHTS, ONCE><<<many_blocks(up(static_cast<uint64_t>(a.rows) * parts, kMoveWaves)), kMoveBlock, 0,
                                                stream>>>(a, parts);
@@ -402,17 +396,14 @@ hipError_t products_of(const CombineArgs& a, const GatherArgs& g, hipStream_t st
                 products_narrow_kernel<T, L, SUM><<<many_blocks(fill + up(a.rows, kMoveBlock / L)), kMoveBlock, 0, stream>>>(a, g, fill);
             });
         });
-    const uint32_t parts = static_cast<uint32_t>(up(vectors, kWave));
-    const uint32_t each = fill_each(g.room, parts);
+    const uint32_t waves = vectors <= kWave ? 1 : vectors <= 2 * kWave ? 2 : 4;   // of a row; 8192 rows of 256 vectors: 146 us with 4, 160 with 1
+    const uint32_t parts = static_cast<uint32_t>(up(vectors, 4 * kWave));
+    const uint32_t each = fill_each(g.room, static_cast<uint64_t>(a.rows) * a.top_k);
     const uint32_t fill = SUM ? 0 : static_cast<uint32_t>(up(up(g.room, each) * parts, kMoveWaves));
     return timed(RS_KERNEL_COMBINE, stream, [&] {
-        pick(large(matrix_size<T>(static_cast<uint64_t>(a.rows) * a.top_k, a.width)), [&](auto once) {
-            constexpr bool ONCE = decltype(once)::value;
-            if (a.rows >= 16384)
-                products_kernel<T, 1, SUM, ONCE><<<many_blocks(fill + up(a.rows, kMoveWaves)), kMoveBlock, 0, stream>>>(a, g, fill, parts, each);
-            else
-                products_kernel<T, kMoveWaves, SUM, ONCE><<<many_blocks(fill + uint64_t{a.rows}), kMoveBlock, 0, stream>>>(a, g, fill, parts, each);
-        });
+        const auto kernel = vectors <= kWave ? products_kernel<T, 1, SUM> : vectors <= 2 * kWave ? products_kernel<T, 2, SUM>
+                                                                                                 : products_kernel<T, 4, SUM>;
+        kernel<<<many_blocks(fill + up(uint64_t{a.rows} * waves, kMoveWaves)), kMoveBlock, 0, stream>>>(a, g, fill, parts, each);
     });
 }
 

@@ -97,13 +97,12 @@ __device__ __forceinline__ AnyVec<16>::V scaled(AnyVec<16>::V r, float w) {
     return narrow<T>(x);
 }
 
-// Whether the rows moved by position are read or written past the caches: the
-// 256 MB on-package cache would not hold them until they are used, nor what else is
-// used meanwhile.  A router's rows gathered, passed through an elementwise kernel
-// and combined: 128 MB take 89.5 us by the caches and 91.2 past them, 256 MB 196 and
-// 188, 512 MB 426 and 388; 192 MB combined with their gradients, other rows in
-// between, 142 and 120.
-inline bool large(uint64_t bytes) { return bytes > (uint64_t{128} << 20); }
+// Whether rows that are read once are read past the caches, which hold 256 MB on
+// the package: combining a router's rows, others in between, takes at 64 MB 12.7 us
+// by the caches and 13.4 past them, at 128 MB 28.9 and 26.8, at 512 MB 120 and 104;
+// rows that the kernel before wrote take 33.0 and 33.5, 66.8 and 62.8, 293 and 272
+// with that kernel.
+inline bool large(uint64_t bytes) { return bytes > (uint64_t{96} << 20); }
 
 // How rows are split among waves: vectors of a lane (1, 2 or 4, so many that the
 // parts still fill the chip: 8192 waves), and parts of a row.
