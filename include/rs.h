@@ -662,9 +662,9 @@ typedef enum rs_kernel_id {
     RS_KERNEL_GATHER = 22,      /* rows to the positions of a grouping */
     RS_KERNEL_COMBINE = 23,     /* rows of a grouping summed by row, products for the weights */
     RS_KERNEL_EMBED = 24,       /* rows of a table by token */
-    RS_KERNEL_EMBED_KEYS = 25,  /* tokens as sort keys, with their positions */
-    RS_KERNEL_EMBED_SUM = 26,   /* sums of rows by runs of sorted tokens */
-    RS_KERNEL_EMBED_JOIN = 27,  /* joins the sums of tokens in several runs */
+    RS_KERNEL_EMBED_SORT = 25,  /* tokens sorted with their positions: counts, places */
+    RS_KERNEL_EMBED_SUM = 26,   /* sums of rows by pieces of sorted tokens, zeros */
+    RS_KERNEL_EMBED_JOIN = 27,  /* joins the sums of tokens in several pieces */
     RS_KERNEL_ADJUST = 28       /* penalties, biases and masks on logits */
 } rs_kernel_id;
 

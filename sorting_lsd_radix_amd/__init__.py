@@ -84,7 +84,7 @@ KERNEL_NAMES = {0: "upsweep", 1: "onesweep", 2: "sort_init", 3: "compact_init",
                 9: "scan_init", 10: "scan", 11: "select_init", 12: "select_count", 13: "select",
                 14: "route", 15: "route_grad", 16: "group_count", 17: "group_scan",
                 18: "group_place", 19: "logprobs", 20: "logprobs_join", 21: "logprobs_grad",
-                22: "gather", 23: "combine", 24: "embed", 25: "embed_keys", 26: "embed_sum",
+                22: "gather", 23: "combine", 24: "embed", 25: "embed_sort", 26: "embed_sum",
                 27: "embed_join", 28: "adjust"}
 
 RS_NO_TEMP = 16

@@ -1,36 +1,63 @@
 // embed.hip -- rows of an embedding table by token, and the table's gradient.
 //
 // The gradient sorts the tokens with their positions (stably) and sums the
-// rows of each token: a wave takes a piece of kPiece sorted positions and a
-// chunk of 64 vectors of 16 bytes.  A token inside one piece is stored at once;
-// of one that goes on, each piece keeps an f32 part, and the piece where the
+// rows of each token: a wave takes a piece of some sorted positions and a chunk
+// of 64 vectors of 16 bytes.  A token inside one piece is stored at once; of one
+// that goes on, each piece keeps an f32 part, and the block of the piece where the
 // token begins joins them in order.  Nothing depends on the order in which
 // blocks run.
+//
+// Rows without a token are zeros.  The sort's launches are short chains of
+// dependent steps, so blocks beside them write zeros meanwhile: to the first rows
+// whatever their tokens, which is made good later, and once it is known which tokens
+// occur, to the others' rows only.  The rows that are left are filled beside
+// the sums.
 #include "internal.hpp"
-#include "rows_common.hpp"
+#include "move_common.hpp"
 
 namespace rs {
 
 namespace {
 
-constexpr int kEmbedBlock = 256;
-constexpr int kEmbedWaves = kEmbedBlock / kWave;
-constexpr uint32_t kPiece = 16;
+#ifndef RIDE
+#define RIDE (24u << 20)
+#endif
 
-template <class T>
-constexpr int kVec = 16 / sizeof(T);
-
-template <class T>
-uint32_t chunks_of(uint32_t width) {
-    return (width + kWave * kVec<T> - 1) / (kWave * kVec<T>);
+hipError_t done(hipStream_t stream) {
+    const hipError_t e = hipGetLastError();
+    timing_after(stream);
+    return e;
 }
 
-template <class T, bool SCALED>
-__global__ __launch_bounds__(kEmbedBlock) void embed_kernel(EmbedArgs a, uint32_t chunks) {
+uint64_t up(uint64_t n, uint64_t d) { return (n + d - 1) / d; }
+
+// ---- rows by token ------------------------------------------------------------------
+
+// A wave for each part of a row of more than 32 vectors.
+template <class T, int U, bool SCALED>
+__global__ __launch_bounds__(kMoveBlock) void embed_kernel(EmbedArgs a, uint32_t parts) {
+    const uint32_t unit = block_id() * kMoveWaves + threadIdx.x / kWave;
+    const uint32_t i = unit / parts;
+    if (i >= a.n) return;
+    const uint32_t id = a.ids[i];
+    const RowPart<T, U> row(unit % parts, a.width);
+    typename RowPart<T, U>::Vec r[U] = {};
+    if (id < a.vocab) {
+        row.load(static_cast<const T*>(a.table) + id * a.table_stride, r);
+        if (SCALED) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) r[u] = scaled<T>(r[u], a.scale);
+        }
+    }
+    row.store(static_cast<T*>(a.out) + i * a.out_stride, r);
+}
+
+// L lanes a row, up to L vectors.
+template <class T, int L, bool SCALED>
+__global__ __launch_bounds__(kMoveBlock) void embed_narrow_kernel(EmbedArgs a) {
     constexpr int V = kVec<T>;
-    const uint64_t unit = static_cast<uint64_t>(block_id()) * kEmbedWaves + threadIdx.x / kWave;
-    const uint64_t i = unit / chunks;
-    const uint32_t col = static_cast<uint32_t>(unit % chunks) * (kWave * V) + lane_id() * V;
+    const uint64_t i = static_cast<uint64_t>(block_id()) * (kMoveBlock / L) + threadIdx.x / L;
+    const uint32_t col = threadIdx.x % L * V;
     if (i >= a.n || col >= a.width) return;
     const uint32_t id = a.ids[i];
     const uint32_t left = a.width - col;
@@ -50,21 +77,226 @@ __global__ __launch_bounds__(kEmbedBlock) void embed_kernel(EmbedArgs a, uint32_
     }
 }
 
-// Sort keys: the tokens, `vocab` for those outside the table; values: positions.
-__global__ __launch_bounds__(kEmbedBlock) void embed_keys_kernel(const uint32_t* __restrict__ ids, uint32_t n,
-                                                                 uint32_t vocab, uint32_t* __restrict__ keys,
-                                                                 uint32_t* __restrict__ at) {
-    const uint64_t i = static_cast<uint64_t>(block_id()) * kEmbedBlock + threadIdx.x;
-    if (i >= n) return;
-    const uint32_t id = ids[i];
-    keys[i] = id < vocab ? id : vocab;
-    at[i] = static_cast<uint32_t>(i);
+template <class T, bool SCALED>
+hipError_t embed_of(const EmbedArgs& a, hipStream_t stream) {
+    const uint32_t vectors = static_cast<uint32_t>(up(a.width, kVec<T>));
+    timing_before(stream, RS_KERNEL_EMBED);
+    if (vectors <= 32) {
+        const uint32_t lanes = vectors <= 4 ? 4 : vectors <= 16 ? 16 : 32;
+        const auto kernel = lanes == 4 ? embed_narrow_kernel<T, 4, SCALED> : lanes == 16 ? embed_narrow_kernel<T, 16, SCALED>
+                                                                                         : embed_narrow_kernel<T, 32, SCALED>;
+        kernel<<<many_blocks(up(a.n, kMoveBlock / lanes)), kMoveBlock, 0, stream>>>(a);
+    } else {
+        const Split s = split_rows(vectors, a.n);
+        const auto kernel = s.unroll == 1 ? embed_kernel<T, 1, SCALED> : s.unroll == 2 ? embed_kernel<T, 2, SCALED>
+                                                                                       : embed_kernel<T, 4, SCALED>;
+        kernel<<<many_blocks(up(static_cast<uint64_t>(a.n) * s.parts, kMoveWaves)), kMoveBlock, 0, stream>>>(a, s.parts);
+    }
+    return done(stream);
 }
 
-template <class T, class O>
-__device__ __forceinline__ void store_row(const EmbedGradArgs& a, uint32_t id, uint32_t col, uint32_t left,
-                                          float (&sum)[kVec<T>]) {
-    constexpr int V = kVec<T>;
+// ---- zeros in rows without a token ------------------------------------------------------
+
+// Rows first .. last of a table, `each` (at most 64) a wave, on 2^lanes_log2
+// lanes a row; those of tokens that occur are left out, where that is known.
+struct Zeros {
+    void* table;
+    uint64_t stride;
+    const uint8_t* occurs;
+    uint32_t first, last, width, each, lanes_log2;
+};
+
+template <class O>
+__device__ __forceinline__ void zero_rows(const Zeros& z, uint64_t wave) {
+    constexpr int V = kVec<O>;
+    const uint32_t lane = lane_id();
+    const uint64_t row0 = z.first + wave * z.each;
+    if (row0 >= z.last) return;
+    const uint32_t n = z.last - row0 < z.each ? z.last - static_cast<uint32_t>(row0) : z.each;
+    const uint64_t rows = ballot(lane < n && !(z.occurs && z.occurs[row0 + lane]));
+    const uint32_t groups = kWave >> z.lanes_log2;
+    const float zero[V] = {};
+    for (uint32_t s = 0; s < n; s += groups) {
+        const uint32_t r = s + (lane >> z.lanes_log2);
+        if (r >= n || !((rows >> r) & 1u)) continue;
+        O* to = static_cast<O*>(z.table) + (row0 + r) * z.stride;
+        for (uint64_t c = (lane & ((1u << z.lanes_log2) - 1)) * V; c < z.width; c += static_cast<uint64_t>(V) << z.lanes_log2)
+            store_some<V>(to + c, z.width - static_cast<uint32_t>(c), zero);
+    }
+}
+
+// ---- the sort -----------------------------------------------------------------------------
+//
+// A stable counting sort by digits of up to 10 bits, lowest first.  A block
+// ranks a tile of keys as group.hip does: wave w holds the w-th run of 64 ITEMS
+// keys, 64 a row, and a key's rank among its digit's in the wave is the count
+// of earlier rows plus the peers in lower lanes, found by a ballot for each bit.
+
+constexpr int kSortBlock = 1024;
+constexpr int kSortWaves = kSortBlock / kWave;
+constexpr uint32_t kMaxBits = 10;
+constexpr uint32_t kMaxTiles = 128;   // each block sums the counts of all tiles
+
+struct Pass {
+    const uint32_t* keys;   // the tokens in the first pass
+    const uint32_t* at;     // their positions, null in the first pass
+    uint32_t* keys_out;
+    uint32_t* at_out;
+    uint32_t* counts;       // [tiles][bins]
+    uint8_t* occurs;        // [vocab], or null
+    uint32_t n, vocab, tiles, shift, bits;
+};
+
+// A key: the token, `vocab` for one outside the table.
+__device__ __forceinline__ uint32_t key_of(const Pass& p, uint64_t i) {
+    const uint32_t k = p.keys[i];
+    return k < p.vocab ? k : p.vocab;
+}
+
+template <class O, int ITEMS>
+__global__ __launch_bounds__(kSortBlock) void embed_count_kernel(Pass p, Zeros z, bool first) {
+    __shared__ uint32_t s_count[1u << kMaxBits];
+    const uint32_t tid = threadIdx.x;
+    if (first && p.occurs) {
+        const uint32_t words = static_cast<uint32_t>((static_cast<uint64_t>(p.vocab) + 3) / 4);
+        for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kSortBlock + tid; i < words; i += static_cast<uint64_t>(gridDim.x) * kSortBlock)
+            reinterpret_cast<uint32_t*>(p.occurs)[i] = 0;
+    }
+    if (blockIdx.x >= p.tiles) return zero_rows<O>(z, static_cast<uint64_t>(blockIdx.x - p.tiles) * kSortWaves + tid / kWave);
+    const uint32_t base = blockIdx.x * (kSortBlock * ITEMS);
+    s_count[tid] = 0;
+    uint32_t d[ITEMS];
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        const uint32_t i = base + j * kSortBlock + tid;
+        d[j] = i < p.n ? (key_of(p, i) >> p.shift) & ((1u << p.bits) - 1) : ~0u;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j)
+        if (d[j] != ~0u) atomicAdd(&s_count[d[j]], 1u);
+    __syncthreads();
+    if (tid < (1u << p.bits)) p.counts[(blockIdx.x << p.bits) + tid] = s_count[tid];
+}
+
+template <class O, int ITEMS>
+__global__ __launch_bounds__(kSortBlock) void embed_place_kernel(Pass p, Zeros z) {
+    __shared__ uint16_t s_count[kSortWaves][1u << kMaxBits];
+    __shared__ uint32_t s_part[2][kSortBlock];
+    __shared__ uint32_t s_base[1u << kMaxBits];
+    __shared__ uint32_t s_wave[kSortWaves];
+    const uint32_t tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+    const uint32_t tile = blockIdx.x;
+    if (tile >= p.tiles) return zero_rows<O>(z, static_cast<uint64_t>(tile - p.tiles) * kSortWaves + wave);
+    const uint32_t bins = 1u << p.bits;
+    const uint32_t base = tile * (kSortBlock * ITEMS) + wave * (kWave * ITEMS) + lane;
+    uint32_t key[ITEMS], at[ITEMS], rank[ITEMS];
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        const uint32_t i = base + j * kWave;
+        key[j] = i < p.n ? key_of(p, i) : ~0u;
+        at[j] = i < p.n && p.at ? p.at[i] : i;
+    }
+    for (uint32_t x = lane; x < bins; x += kWave) s_count[wave][x] = 0;
+    // counts of the tiles: thread (slice q, bin) sums every slices-th tile
+    if (p.tiles > 1) {
+        const uint32_t slices = kSortBlock >> p.bits;
+        const uint32_t bin = tid & (bins - 1), q = tid >> p.bits;
+        constexpr uint32_t kAhead = 8;   // loads in flight: of the last tile again behind the end
+        uint32_t before = 0, all = 0;
+        for (uint32_t t0 = q; t0 < p.tiles; t0 += kAhead * slices) {
+            uint32_t n[kAhead];
+#pragma unroll
+            for (uint32_t j = 0; j < kAhead; ++j) {
+                const uint32_t t = t0 + j * slices;
+                n[j] = p.counts[((t < p.tiles ? t : p.tiles - 1) << p.bits) + bin];
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < kAhead; ++j) {
+                const uint32_t t = t0 + j * slices;
+                all += t < p.tiles ? n[j] : 0u;
+                before += t < tile ? n[j] : 0u;
+            }
+        }
+        s_part[0][tid] = before;
+        s_part[1][tid] = all;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        const bool real = key[j] != ~0u;
+        const uint32_t d = (key[j] >> p.shift) & (bins - 1);
+        uint64_t peers = ballot(real);
+        for (uint32_t b = 0; b < p.bits; ++b) {
+            const uint64_t ones = ballot((d >> b) & 1u);
+            peers &= ((d >> b) & 1u) ? ones : ~ones;
+        }
+        const uint32_t below = count_below(peers);
+        rank[j] = real ? s_count[wave][d] + below : 0u;
+        wave_fence();   // all peers have read before the last of them writes
+        if (real && below + 1 == static_cast<uint32_t>(__builtin_popcountll(peers)))
+            s_count[wave][d] = static_cast<uint16_t>(rank[j] + 1);
+        wave_fence();
+    }
+    __syncthreads();
+    uint32_t before = 0, total = 0;
+    if (tid < bins) {
+#pragma unroll
+        for (uint32_t w = 0; w < kSortWaves; ++w) {
+            const uint32_t n = s_count[w][tid];
+            s_count[w][tid] = static_cast<uint16_t>(total);
+            total += n;
+        }
+        if (p.tiles > 1) {
+            total = 0;
+            for (uint32_t x = tid; x < kSortBlock; x += bins) {
+                before += s_part[0][x];
+                total += s_part[1][x];
+            }
+        }
+    }
+    const uint32_t incl = wave_inclusive_sum(total);
+    if (lane == kWave - 1) s_wave[wave] = incl;
+    __syncthreads();
+    uint32_t start = incl - total;
+    for (uint32_t w = 0; w < wave; ++w) start += s_wave[w];
+    if (tid < bins) s_base[tid] = start + before;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        if (key[j] == ~0u) continue;
+        const uint32_t d = (key[j] >> p.shift) & (bins - 1);
+        const uint32_t to = s_base[d] + s_count[wave][d] + rank[j];
+        p.keys_out[to] = key[j];
+        p.at_out[to] = at[j];
+        if (p.occurs && p.at == nullptr && key[j] < p.vocab) p.occurs[key[j]] = 1;   // from all that do, the same byte
+    }
+}
+
+// Sort keys and positions for the library's sort, which takes over above
+// kMaxTiles tiles of 16384 tokens.
+__global__ __launch_bounds__(kSortBlock) void embed_keys_kernel(Pass p) {
+    const uint64_t i = static_cast<uint64_t>(block_id()) * kSortBlock + threadIdx.x;
+    if (p.occurs) {
+        const uint64_t step = static_cast<uint64_t>(gridDim.x) * gridDim.y * kSortBlock;
+        const uint64_t words = (static_cast<uint64_t>(p.vocab) + 3) / 4;
+        for (uint64_t w = i; w < words; w += step) reinterpret_cast<uint32_t*>(p.occurs)[w] = 0;
+    }
+    if (i >= p.n) return;
+    p.keys_out[i] = key_of(p, i);
+    p.at_out[i] = static_cast<uint32_t>(i);
+}
+
+__global__ __launch_bounds__(kSortBlock) void embed_mark_kernel(Pass p) {
+    const uint64_t i = static_cast<uint64_t>(block_id()) * kSortBlock + threadIdx.x;
+    if (i < p.n && p.keys[i] < p.vocab) p.occurs[p.keys[i]] = 1;
+}
+
+// ---- the sums -------------------------------------------------------------------------------
+
+// kPart columns of a lane, beginning at `col`, of which `left` exist.
+template <class O, int V>
+__device__ __forceinline__ void store_row(const EmbedGradArgs& a, uint32_t id, uint32_t col, uint32_t left, float (&sum)[V]) {
     O* to = static_cast<O*>(a.dtable) + id * a.dtable_stride + col;
 #pragma unroll
     for (int j = 0; j < V; ++j) sum[j] *= a.scale;
@@ -77,177 +309,281 @@ __device__ __forceinline__ void store_row(const EmbedGradArgs& a, uint32_t id, u
     store_some<V>(to, left, sum);
 }
 
-// Parts of tokens that cross pieces: two rows of `width` f32 for each piece,
-// of its first token, if that began before, and of its last.
-template <class T, class O>
-__global__ __launch_bounds__(kEmbedBlock) void embed_sum_kernel(EmbedGradArgs a, uint32_t chunks,
-                                                                const uint32_t* __restrict__ keys,
-                                                                const uint32_t* __restrict__ at,
-                                                                float* __restrict__ parts) {
+struct Sorted {
+    const uint32_t* keys;
+    const uint32_t* at;
+    float* parts;      // [pieces][2][width]: of a piece's first token, if it began before, and of its last
+    uint32_t piece;    // positions of a piece, at most 64
+    uint32_t chunks;   // of a row, or 1 where L lanes have it all
+};
+
+constexpr int kInFlight = 8;
+
+// L lanes take a piece and 64 vectors of the rows, or, L < 64, all of them.
+// Blocks behind the last piece fill the rows without tokens.
+template <class T, class O, int L>
+__global__ __launch_bounds__(kMoveBlock) void embed_sum_kernel(EmbedGradArgs a, Sorted s, Zeros z, uint32_t sums) {
     constexpr int V = kVec<T>;
-    const uint64_t unit = static_cast<uint64_t>(block_id()) * kEmbedWaves + threadIdx.x / kWave;
-    const uint64_t piece = unit / chunks;
-    const uint64_t begin = piece * kPiece;
+    if (block_id() >= sums) return zero_rows<O>(z, static_cast<uint64_t>(block_id() - sums) * kMoveWaves + threadIdx.x / kWave);
+    const uint32_t unit = block_id() * (kMoveBlock / L) + threadIdx.x / L;
+    const uint32_t piece = unit / s.chunks;
+    const uint64_t begin = static_cast<uint64_t>(piece) * s.piece;
     if (begin >= a.n) return;
-    const uint32_t end = a.n - begin < kPiece ? a.n : static_cast<uint32_t>(begin) + kPiece;
-    const uint32_t col = static_cast<uint32_t>(unit % chunks) * (kWave * V) + lane_id() * V;
+    const uint32_t count = a.n - begin < s.piece ? a.n - static_cast<uint32_t>(begin) : s.piece;
+    const uint32_t lane = threadIdx.x % L;
+    const uint32_t col = (unit % s.chunks * L + lane) * V;
     const uint32_t left = col < a.width ? a.width - col : 0u;
-    uint32_t id = keys[begin];
-    bool before = begin > 0 && keys[begin - 1] == id;
-    float sum[V];
+    const T* rows = static_cast<const T*>(a.dout) + col;
+    const uint32_t* keys = s.keys + begin;
+    const uint32_t* ats = s.at + begin;
+    // with a wave a piece, its keys and positions are in the lanes
+    const uint32_t lane_key = L == kWave && lane < count ? keys[lane] : 0u;
+    const uint32_t lane_at = L == kWave && lane < count ? ats[lane] : 0u;
+    auto key = [&](uint32_t i) { return L == kWave ? lane_value(lane_key, i) : keys[i]; };
+    auto at = [&](uint32_t i) { return L == kWave ? lane_value(lane_at, i) : ats[i]; };
+    const uint32_t next = begin + count < a.n ? keys[count] : ~0u;   // no key is ~0
+    bool before = begin > 0 && s.keys[begin - 1] == key(0);
+    float sum[V] = {};
+    for (uint32_t i0 = 0; i0 < count; i0 += kInFlight) {
+        float r[kInFlight][V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) sum[j] = 0.0f;
-    for (uint32_t i = static_cast<uint32_t>(begin); i < end; ++i) {
-        float v[V];
-        load_some<V>(static_cast<const T*>(a.dout) + at[i] * a.dout_stride + col, left, 0.0f, v);
+        for (uint32_t b = 0; b < kInFlight; ++b)
+            if (i0 + b < count && key(i0 + b) < a.vocab)
+                load_some<V>(rows + at(i0 + b) * a.dout_stride, left, 0.0f, r[b]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) sum[j] += v[j];
-        const uint32_t next = i + 1 < a.n ? keys[i + 1] : ~0u;   // no key is ~0
-        if (next == id && i + 1 < end) continue;
-        const bool after = next == id;
-        if (id < a.vocab) {
-            if (!before && !after) store_row<T, O>(a, id, col, left, sum);
-            else store_some<V>(parts + (2 * piece + (before ? 0 : 1)) * a.width + col, left, sum);
+        for (uint32_t b = 0; b < kInFlight; ++b) {
+            const uint32_t i = i0 + b;
+            if (i >= count) break;
+            const uint32_t id = key(i);
+            if (id >= a.vocab) break;
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum[j] += r[b][j];
+            const bool last = i + 1 == count;
+            const uint32_t then = last ? next : key(i + 1);
+            if (then == id && !last) continue;
+            if (!before && then != id) store_row<O, V>(a, id, col, left, sum);
+            else store_some<V>(s.parts + (static_cast<uint64_t>(piece) * 2 + (before ? 0 : 1)) * a.width + col, left, sum);
+            before = false;
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum[j] = 0.0f;
         }
-        id = next;
-        before = false;
-#pragma unroll
-        for (int j = 0; j < V; ++j) sum[j] = 0.0f;
     }
 }
 
-template <class T, class O>
-__global__ __launch_bounds__(kEmbedBlock) void embed_join_kernel(EmbedGradArgs a, uint32_t chunks,
-                                                                 const uint32_t* __restrict__ keys,
-                                                                 const float* __restrict__ parts) {
+constexpr int kJoinBlock = 512;
+
+// A block for each piece (and 64 vectors): if a token begins in it and goes
+// on, its parts, a run of them for each L lanes, then the runs.
+template <class T, class O, int L>
+__global__ __launch_bounds__(kJoinBlock) void embed_join_kernel(EmbedGradArgs a, Sorted s) {
     constexpr int V = kVec<T>;
-    const uint64_t unit = static_cast<uint64_t>(block_id()) * kEmbedWaves + threadIdx.x / kWave;
-    uint64_t piece = unit / chunks;
-    const uint64_t begin = piece * kPiece;
-    if (a.n <= kPiece || begin >= a.n - kPiece) return;   // the last piece's tokens end there
-    const uint32_t id = keys[begin + kPiece - 1];
-    if (id >= a.vocab || keys[begin + kPiece] != id) return;
-    if (keys[begin] == id && begin > 0 && keys[begin - 1] == id) return;   // begins in an earlier piece
-    const uint32_t col = static_cast<uint32_t>(unit % chunks) * (kWave * V) + lane_id() * V;
-    const uint32_t left = col < a.width ? a.width - col : 0u;
-    float sum[V];
-    load_some<V>(parts + (2 * piece + 1) * a.width + col, left, 0.0f, sum);
-    for (++piece; piece * kPiece < a.n && keys[piece * kPiece] == id; ++piece) {
-        float v[V];
-        load_some<V>(parts + 2 * piece * a.width + col, left, 0.0f, v);
-#pragma unroll
-        for (int j = 0; j < V; ++j) sum[j] += v[j];
-    }
-    store_row<T, O>(a, id, col, left, sum);
-}
-
-// Zeros in the rows of tokens that do not occur, a wave for each chunk of a row.
-template <class O>
-__global__ __launch_bounds__(kEmbedBlock) void embed_zero_kernel(EmbedGradArgs a, uint32_t chunks,
-                                                                 const uint32_t* __restrict__ keys) {
-    constexpr int V = kVec<O>;
-    const uint64_t unit = static_cast<uint64_t>(block_id()) * kEmbedWaves + threadIdx.x / kWave;
-    const uint64_t id = unit / chunks;
-    if (id >= a.vocab) return;
-    uint32_t lo = 0, hi = a.n;   // the first key that is not below id
+    constexpr uint32_t kWorkers = kJoinBlock / L;
+    __shared__ float s_sum[kWorkers][L * V];
+    const uint32_t piece = block_id() / s.chunks;
+    const uint64_t end = (static_cast<uint64_t>(piece) + 1) * s.piece;
+    if (end >= a.n) return;   // the last piece's tokens end there
+    const uint32_t id = s.keys[end - 1];
+    if (id >= a.vocab || s.keys[end] != id) return;
+    const uint64_t begin = end - s.piece;
+    if (s.keys[begin] == id && begin > 0 && s.keys[begin - 1] == id) return;   // begins in an earlier piece
+    // pieces that begin with the token: behind `piece` up to the last one, found by halving
+    uint32_t lo = piece + 1, hi = static_cast<uint32_t>((a.n - 1) / s.piece);
     while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (keys[mid] < id) lo = mid + 1;
-        else hi = mid;
+        const uint32_t mid = hi - (hi - lo) / 2;
+        if (s.keys[static_cast<uint64_t>(mid) * s.piece] == id) lo = mid;
+        else hi = mid - 1;
     }
-    if (lo < a.n && keys[lo] == id) return;
-    const uint32_t col = static_cast<uint32_t>(unit % chunks) * (kWave * V) + lane_id() * V;
-    if (col >= a.width) return;
-    const float zero[V] = {};
-    store_some<V>(static_cast<O*>(a.dtable) + id * a.dtable_stride + col, a.width - col, zero);
+    const uint32_t count = lo - piece + 1;
+    const uint32_t run = (count + kWorkers - 1) / kWorkers;
+    const uint32_t worker = threadIdx.x / L, lane = threadIdx.x % L;
+    const uint32_t col = (block_id() % s.chunks * L + lane) * V;
+    const uint32_t left = col < a.width ? a.width - col : 0u;
+    const uint32_t stop = (worker + 1) * run < count ? (worker + 1) * run : count;
+    float sum[V] = {};
+    for (uint32_t i0 = worker * run; i0 < stop; i0 += 4) {
+        float r[4][V];
+#pragma unroll
+        for (uint32_t b = 0; b < 4; ++b)
+            if (i0 + b < stop)
+                load_some<V>(s.parts + (static_cast<uint64_t>(piece + i0 + b) * 2 + (i0 + b == 0 ? 1 : 0)) * a.width + col, left, 0.0f, r[b]);
+#pragma unroll
+        for (uint32_t b = 0; b < 4; ++b) {
+            if (i0 + b >= stop) break;
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum[j] += r[b][j];
+        }
+    }
+    const uint32_t workers = (count + run - 1) / run;
+    if (worker < workers) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) s_sum[worker][j * L + lane] = sum[j];
+    }
+    __syncthreads();
+    if (worker != 0) return;
+    for (uint32_t w = 1; w < workers; ++w) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j] += s_sum[w][j * L + lane];
+    }
+    store_row<O, V>(a, id, col, left, sum);
 }
 
-uint64_t pieces_of(uint64_t n) { return (n + kPiece - 1) / kPiece; }
+// ---- launches ---------------------------------------------------------------------------------
+
+uint32_t sort_items(uint64_t n) { return n <= kMaxTiles * kSortBlock ? 1 : n <= kMaxTiles * kSortBlock * 4 ? 4 : 16; }
+bool own_sort(uint64_t n) { return n <= uint64_t{kMaxTiles} * kSortBlock * 16; }
+uint32_t piece_of(uint64_t n) { return n <= 1u << 15 ? 16 : n <= 1u << 17 ? 32 : 64; }
 
 size_t up256(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
-// Temp: keys, positions, both sorted, the sort's own temp, the parts.
+// Temp: keys and positions twice, the tiles' counts or the library sort's own
+// temp, which tokens occur, the parts.
 struct Temp {
-    size_t array, sort, parts;
-    Temp(uint64_t n, uint32_t width) {
+    size_t array, sort, occurs, parts;
+    Temp(uint64_t n, uint32_t vocab, uint32_t width) {
         array = up256(n * sizeof(uint32_t));
-        sort = up256(sort_temp_bytes(n, true, SortKind{}));
-        parts = n > kPiece ? up256(pieces_of(n) * 2 * width * sizeof(float)) : 0;
+        sort = own_sort(n) ? kMaxTiles * sizeof(uint32_t) << kMaxBits : up256(sort_temp_bytes(n, true, SortKind{}));
+        occurs = up256(vocab);
+        parts = n > piece_of(n) ? up256(up(n, piece_of(n)) * 2 * width * sizeof(float)) : 0;
     }
-    size_t bytes() const { return 4 * array + sort + parts; }
+    size_t bytes() const { return 4 * array + sort + occurs + parts; }
 };
 
-template <class T>
-hipError_t embed_of(const EmbedArgs& a, hipStream_t stream) {
-    const uint32_t chunks = chunks_of<T>(a.width);
-    timing_before(stream, RS_KERNEL_EMBED);
-    const auto kernel = a.scale == 1.0f ? embed_kernel<T, false> : embed_kernel<T, true>;
-    kernel<<<many_blocks((static_cast<uint64_t>(a.n) * chunks + kEmbedWaves - 1) / kEmbedWaves), kEmbedBlock, 0,
-             stream>>>(a, chunks);
-    const hipError_t e = hipGetLastError();
-    timing_after(stream);
-    return e;
+template <class O>
+hipError_t sort_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&keys)[2], uint32_t* const (&at)[2], Zeros& z,
+                       uint64_t ride, int* last, hipStream_t stream) {
+    uint32_t bits = 1;
+    while ((uint64_t{a.vocab} >> bits) != 0) ++bits;
+    const uint32_t passes = (bits + kMaxBits - 1) / kMaxBits;
+    const uint32_t each_bits = (bits + passes - 1) / passes;
+    const uint32_t items = sort_items(a.n);
+    p.tiles = static_cast<uint32_t>(up(a.n, uint64_t{kSortBlock} * items));
+    // the next rows to be filled beside a launch: blocks, and their end in z
+    auto riders = [&](bool known) {
+        z.occurs = known ? p.occurs : nullptr;
+        z.first = z.last;
+        const uint64_t rows = ride < a.vocab - z.first ? ride : a.vocab - z.first;
+        z.last += static_cast<uint32_t>(rows);
+        return static_cast<uint32_t>(up(up(rows, z.each), kSortWaves));
+    };
+    for (uint32_t k = 0; k < passes; ++k) {
+        p.shift = k * each_bits;
+        p.bits = bits - p.shift < each_bits ? bits - p.shift : each_bits;
+        p.keys = k == 0 ? a.ids : keys[(k - 1) & 1];
+        p.at = k == 0 ? nullptr : at[(k - 1) & 1];
+        p.keys_out = keys[k & 1];
+        p.at_out = at[k & 1];
+        if (p.tiles > 1 || (k == 0 && p.occurs)) {
+            const uint32_t beside = riders(k > 0);
+            timing_before(stream, RS_KERNEL_EMBED_SORT);
+            const auto kernel = items == 1 ? embed_count_kernel<O, 1> : items == 4 ? embed_count_kernel<O, 4> : embed_count_kernel<O, 16>;
+            kernel<<<dim3(p.tiles + beside), kSortBlock, 0, stream>>>(p, z, k == 0);
+            const hipError_t e = done(stream);
+            if (e != hipSuccess) return e;
+        }
+        const uint32_t beside = riders(k > 0);
+        timing_before(stream, RS_KERNEL_EMBED_SORT);
+        const auto kernel = items == 1 ? embed_place_kernel<O, 1> : items == 4 ? embed_place_kernel<O, 4> : embed_place_kernel<O, 16>;
+        kernel<<<dim3(p.tiles + beside), kSortBlock, 0, stream>>>(p, z);
+        const hipError_t e = done(stream);
+        if (e != hipSuccess) return e;
+        *last = k & 1;
+    }
+    return hipSuccess;
+}
+
+hipError_t sort_many_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&keys)[2], uint32_t* const (&at)[2], void* temp,
+                            hipStream_t stream) {
+    p.keys = a.ids;
+    p.keys_out = keys[0];
+    p.at_out = at[0];
+    const dim3 grid = many_blocks(up(a.n, kSortBlock));
+    timing_before(stream, RS_KERNEL_EMBED_SORT);
+    embed_keys_kernel<<<grid, kSortBlock, 0, stream>>>(p);
+    hipError_t e = done(stream);
+    if (e != hipSuccess) return e;
+    if (p.occurs) {
+        p.keys = keys[0];
+        timing_before(stream, RS_KERNEL_EMBED_SORT);
+        embed_mark_kernel<<<grid, kSortBlock, 0, stream>>>(p);
+        e = done(stream);
+        if (e != hipSuccess) return e;
+    }
+    int bits = 1;
+    while ((uint64_t{a.vocab} >> bits) != 0) ++bits;
+    return launch_sort(SortIo{keys[0], keys[1], nullptr, nullptr, at[0], at[1], a.n}, SortKind{}, 0, bits, temp, stream);
+}
+
+template <class T, class O, int L>
+hipError_t sum_tokens(const EmbedGradArgs& a, Sorted s, const Zeros& z, hipStream_t stream) {
+    const uint64_t pieces = up(a.n, s.piece);
+    const uint64_t sums = up(pieces * s.chunks, kMoveBlock / L);
+    const uint64_t fill = up(up(z.last - z.first, z.each), kMoveWaves);
+    hipError_t e = hipSuccess;
+    if (sums + fill > 0) {
+        timing_before(stream, RS_KERNEL_EMBED_SUM);
+        embed_sum_kernel<T, O, L><<<many_blocks(sums + fill), kMoveBlock, 0, stream>>>(a, s, z, static_cast<uint32_t>(sums));
+        e = done(stream);
+    }
+    if (e != hipSuccess || pieces <= 1) return e;
+    timing_before(stream, RS_KERNEL_EMBED_JOIN);
+    embed_join_kernel<T, O, L><<<many_blocks(pieces * s.chunks), kJoinBlock, 0, stream>>>(a, s);
+    return done(stream);
 }
 
 template <class T, class O>
 hipError_t embed_grad_of(const EmbedGradArgs& a, void* temp, hipStream_t stream) {
-    const Temp size(a.n, a.width);
+    const Temp size(a.n, a.vocab, a.width);
     char* base = static_cast<char*>(temp);
-    uint32_t* keys_in = reinterpret_cast<uint32_t*>(base);
-    uint32_t* at_in = reinterpret_cast<uint32_t*>(base + size.array);
-    uint32_t* keys = reinterpret_cast<uint32_t*>(base + 2 * size.array);
-    uint32_t* at = reinterpret_cast<uint32_t*>(base + 3 * size.array);
-    void* sort_temp = base + 4 * size.array;
-    float* parts = reinterpret_cast<float*>(base + 4 * size.array + size.sort);
-    hipError_t e = hipSuccess;
+    auto words = [&](size_t offset) { return reinterpret_cast<uint32_t*>(base + offset); };
+    uint32_t* const keys[2] = {words(0), words(2 * size.array)};
+    uint32_t* const at[2] = {words(size.array), words(3 * size.array)};
+    void* sort = base + 4 * size.array;
+    uint8_t* occurs = reinterpret_cast<uint8_t*>(base + 4 * size.array + size.sort);
+    Sorted s{keys[0], at[0], reinterpret_cast<float*>(occurs + size.occurs), piece_of(a.n), 1};
+
+    Zeros z{a.dtable, a.dtable_stride, nullptr, 0, 0, a.width, 1, 6};
+    const uint64_t row_bytes = uint64_t{a.width} * sizeof(O);
+    while (z.each < 64 && z.each * row_bytes < 16384) z.each *= 2;
+    while (z.lanes_log2 > 0 && (kVec<O> << (z.lanes_log2 - 1)) >= a.width) --z.lanes_log2;
+    const uint64_t ride = a.accumulate ? 0 : RIDE / row_bytes;
+
+    Pass p{};
+    p.n = a.n;
+    p.vocab = a.vocab;
+    p.counts = static_cast<uint32_t*>(sort);
+    p.occurs = a.accumulate ? nullptr : occurs;
     if (a.n > 0) {
-        timing_before(stream, RS_KERNEL_EMBED_KEYS);
-        embed_keys_kernel<<<many_blocks((a.n + uint64_t{kEmbedBlock} - 1) / kEmbedBlock), kEmbedBlock, 0, stream>>>(
-            a.ids, a.n, a.vocab, keys_in, at_in);
-        e = hipGetLastError();
-        timing_after(stream);
+        int last = 1;
+        const hipError_t e = own_sort(a.n) ? sort_tokens<O>(a, p, keys, at, z, ride, &last, stream)
+                                           : sort_many_tokens(a, p, keys, at, sort, stream);
         if (e != hipSuccess) return e;
-        int bits = 1;
-        while ((uint64_t{a.vocab} >> bits) != 0) ++bits;
-        e = launch_sort(SortIo{keys_in, keys, nullptr, nullptr, at_in, at, a.n}, SortKind{}, 0, bits, sort_temp, stream);
-        if (e != hipSuccess) return e;
+        s.keys = keys[last];
+        s.at = at[last];
+        z.occurs = p.occurs;
     }
-    const uint32_t chunks = chunks_of<T>(a.width);
-    if (!a.accumulate) {
-        const uint32_t out_chunks = chunks_of<O>(a.width);
-        timing_before(stream, RS_KERNEL_EMBED_SUM);
-        embed_zero_kernel<O><<<many_blocks((static_cast<uint64_t>(a.vocab) * out_chunks + kEmbedWaves - 1) / kEmbedWaves),
-                               kEmbedBlock, 0, stream>>>(a, out_chunks, keys);
-        e = hipGetLastError();
-        timing_after(stream);
-        if (e != hipSuccess) return e;
-    }
-    if (a.n == 0) return hipSuccess;
-    const dim3 grid = many_blocks((pieces_of(a.n) * chunks + kEmbedWaves - 1) / kEmbedWaves);
-    timing_before(stream, RS_KERNEL_EMBED_SUM);
-    embed_sum_kernel<T, O><<<grid, kEmbedBlock, 0, stream>>>(a, chunks, keys, at, parts);
-    e = hipGetLastError();
-    timing_after(stream);
-    if (e != hipSuccess || a.n <= kPiece) return e;
-    timing_before(stream, RS_KERNEL_EMBED_JOIN);
-    embed_join_kernel<T, O><<<grid, kEmbedBlock, 0, stream>>>(a, chunks, keys, parts);
-    e = hipGetLastError();
-    timing_after(stream);
-    return e;
+    z.first = z.last;   // what the sort's launches did not fill
+    z.last = a.accumulate ? z.first : a.vocab;
+    const uint32_t vectors = static_cast<uint32_t>(up(a.width, kVec<T>));
+    if (vectors <= 4) return sum_tokens<T, O, 4>(a, s, z, stream);
+    if (vectors <= 16) return sum_tokens<T, O, 16>(a, s, z, stream);
+    s.chunks = static_cast<uint32_t>(up(vectors, kWave));
+    return sum_tokens<T, O, kWave>(a, s, z, stream);
 }
 
 }  // namespace
 
 hipError_t launch_embed(int elem_type, const EmbedArgs& a, hipStream_t stream) {
     if (a.n == 0) return hipSuccess;
+    // with scale 1 the rows are copied bit by bit, whatever they hold
+    if (a.scale == 1.0f) return elem_type == RS_ELEM_F32 ? embed_of<float, false>(a, stream) : embed_of<_Float16, false>(a, stream);
     switch (elem_type) {
-        case RS_ELEM_F32: return embed_of<float>(a, stream);
-        case RS_ELEM_F16: return embed_of<_Float16>(a, stream);
-        default: return embed_of<__bf16>(a, stream);
+        case RS_ELEM_F32: return embed_of<float, true>(a, stream);
+        case RS_ELEM_F16: return embed_of<_Float16, true>(a, stream);
+        default: return embed_of<__bf16, true>(a, stream);
     }
 }
 
-size_t embed_grad_temp_bytes(uint64_t n, uint32_t vocab, uint32_t width) { return Temp(n, width).bytes(); }
+size_t embed_grad_temp_bytes(uint64_t n, uint32_t vocab, uint32_t width) { return Temp(n, vocab, width).bytes(); }
 
 hipError_t launch_embed_grad(int elem_type, int table_type, const EmbedGradArgs& a, void* temp, hipStream_t stream) {
     const bool f32 = table_type == RS_ELEM_F32;

@@ -199,3 +199,32 @@ def test_replays_of_a_graph(n):
         assert torch.equal(got, want), i
         assert torch.equal(rows, rs.embed_tokens(want, ids))
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("n,vocab", [(131072, 1000), (131073, 5000), (300000, 1 << 20), (524289, 70000), (2097152, 300), (2097153, 1500)])
+def test_many_tokens(n, vocab):
+    """Every size of the sort: whole numbers, whose sums are exact in f32."""
+    print("many tokens", n, vocab, flush=True)
+    rng = np.random.default_rng(n)
+    ids = np.minimum(rng.zipf(1.2, n) - 2, vocab).astype(np.int32)   # -1 and `vocab` among them
+    x = rng.integers(-8, 9, (n, 3)).astype(np.float32)
+    want = np.zeros((vocab + 1, 3))
+    np.add.at(want, np.where((ids >= 0) & (ids < vocab), ids, vocab), x)
+    got = rs.embed_tokens_grad(on(x).half(), on(ids), vocab, dtype=torch.float32)
+    assert np.abs(want).max() < 2 ** 24
+    assert np.array_equal(got.cpu().numpy(), want[:vocab])
+
+
+@pytest.mark.parametrize("vocab,width", [(200000, 300), (1 << 20, 33), (3, 1 << 21)])
+def test_large_tables(vocab, width):
+    """Rows filled beside the sort, with and without tokens, and behind it."""
+    print("large tables", vocab, width, flush=True)
+    rng = np.random.default_rng(vocab)
+    n = 2000 if width < 1000 else 5
+    ids = np.concatenate([rng.integers(0, vocab, n - 3), [0, vocab - 1, -1]]).astype(np.int32)
+    x = torch.randint(-8, 9, (n, width), device=DEV).bfloat16()
+    got = torch.full((vocab, width), float("nan"), dtype=torch.bfloat16, device=DEV)
+    rs.embed_tokens_grad(x, on(ids), vocab, out=got)
+    want = torch.zeros(vocab, width, device=DEV)
+    want.index_add_(0, on(ids[:-1]).long(), x[:-1].float())
+    assert torch.equal(got, want.bfloat16())
