@@ -274,7 +274,7 @@ __global__ __launch_bounds__(kSortBlock) void embed_place_kernel(Pass p, Zeros z
 }
 
 // Sort keys and positions for the library's sort, which takes over above
-// kMaxTiles tiles of 16384 tokens.
+// kMaxTiles tiles of 4096 tokens.
 __global__ __launch_bounds__(kSortBlock) void embed_keys_kernel(Pass p) {
     const uint64_t i = static_cast<uint64_t>(block_id()) * kSortBlock + threadIdx.x;
     if (p.occurs) {
@@ -294,19 +294,44 @@ __global__ __launch_bounds__(kSortBlock) void embed_mark_kernel(Pass p) {
 
 // ---- the sums -------------------------------------------------------------------------------
 
-// kPart columns of a lane, beginning at `col`, of which `left` exist.
-template <class O, int V>
-__device__ __forceinline__ void store_row(const EmbedGradArgs& a, uint32_t id, uint32_t col, uint32_t left, float (&sum)[V]) {
-    O* to = static_cast<O*>(a.dtable) + id * a.dtable_stride + col;
+// A lane's vector of the rows.  With WIDE the rows have a whole one, and the last
+// begins where a whole one is left (as in RowPart): what it holds of the vector
+// before is summed twice, to the same value.
+template <class T, bool WIDE>
+struct Columns {
+    static constexpr int V = kVec<T>;
+    using Vec = AnyVec<16>::V;
+    uint32_t at, left, twice;   // first element, elements that the row has from there, those of the vector before
+
+    __device__ __forceinline__ Columns(uint32_t vector, uint32_t width) {
+        const uint32_t c = vector * V;
+        at = WIDE && c > width - V ? width - V : c;
+        left = c < width ? width - at : 0u;
+        twice = c - at;
+    }
+    __device__ __forceinline__ Vec load(const T* row) const {
+        if (WIDE) return __builtin_nontemporal_load(reinterpret_cast<const Vec*>(row + at));
+        float x[V];
+        load_some<V>(row + at, left, 0.0f, x);
+        return narrow<T>(x);   // exact: they are T's
+    }
+    template <class P>
+    __device__ __forceinline__ void store(P* row, const float (&x)[V]) const {
+        if (left) store_some<V>(row + at, WIDE ? V : left, x);
+    }
+};
+
+template <class T, class O, bool WIDE>
+__device__ __forceinline__ void store_row(const EmbedGradArgs& a, uint32_t id, const Columns<T, WIDE>& c, float (&sum)[kVec<T>]) {
+    constexpr int V = kVec<T>;
+    O* row = static_cast<O*>(a.dtable) + id * a.dtable_stride;
 #pragma unroll
     for (int j = 0; j < V; ++j) sum[j] *= a.scale;
-    if (a.accumulate) {
-        float old[V];
-        load_some<V>(to, left, 0.0f, old);
+    if (!a.accumulate) return c.store(row, sum);
+    // each element by one lane alone
 #pragma unroll
-        for (int j = 0; j < V; ++j) sum[j] += old[j];
-    }
-    store_some<V>(to, left, sum);
+    for (uint32_t j = 0; j < V; ++j)
+        if (j >= c.twice && j < c.left) row[c.at + j] = static_cast<O>(static_cast<float>(row[c.at + j]) + sum[j]);
 }
 
 struct Sorted {
@@ -317,52 +342,64 @@ struct Sorted {
     uint32_t chunks;   // of a row, or 1 where L lanes have it all
 };
 
-constexpr int kInFlight = 8;
+#ifndef IF
+#define IF 8
+#endif
+constexpr int kInFlight = IF;
 
 // L lanes take a piece and 64 vectors of the rows, or, L < 64, all of them.
 // Blocks behind the last piece fill the rows without tokens.
 template <class T, class O, int L>
 __global__ __launch_bounds__(kMoveBlock) void embed_sum_kernel(EmbedGradArgs a, Sorted s, Zeros z, uint32_t sums) {
     constexpr int V = kVec<T>;
+    using Cols = Columns<T, L == kWave>;
     if (block_id() >= sums) return zero_rows<O>(z, static_cast<uint64_t>(block_id() - sums) * kMoveWaves + threadIdx.x / kWave);
-    const uint32_t unit = block_id() * (kMoveBlock / L) + threadIdx.x / L;
+    const uint32_t unit = block_id() * (kMoveBlock / L) + (L == kWave ? wave_id() : threadIdx.x / L);
     const uint32_t piece = unit / s.chunks;
     const uint64_t begin = static_cast<uint64_t>(piece) * s.piece;
     if (begin >= a.n) return;
-    const uint32_t count = a.n - begin < s.piece ? a.n - static_cast<uint32_t>(begin) : s.piece;
+    uint32_t count = a.n - begin < s.piece ? a.n - static_cast<uint32_t>(begin) : s.piece;
     const uint32_t lane = threadIdx.x % L;
-    const uint32_t col = (unit % s.chunks * L + lane) * V;
-    const uint32_t left = col < a.width ? a.width - col : 0u;
-    const T* rows = static_cast<const T*>(a.dout) + col;
+    const Cols cols(unit % s.chunks * L + lane, a.width);
+    const T* rows = static_cast<const T*>(a.dout);
     const uint32_t* keys = s.keys + begin;
     const uint32_t* ats = s.at + begin;
+    const uint32_t next = begin + count < a.n ? keys[count] : ~0u;   // no key is ~0
+    bool before = begin > 0 && s.keys[begin - 1] == keys[0];
     // with a wave a piece, its keys and positions are in the lanes
-    const uint32_t lane_key = L == kWave && lane < count ? keys[lane] : 0u;
-    const uint32_t lane_at = L == kWave && lane < count ? ats[lane] : 0u;
+    uint32_t lane_key = ~0u, lane_at = 0;
+    if (L == kWave) {
+        if (lane < count) {
+            lane_key = keys[lane];
+            lane_at = ats[lane];
+        }
+        count = __builtin_popcountll(ballot(lane_key < a.vocab));   // the others are last
+        // what follows reads them across lanes, and must not wait for them between the rows' loads
+        asm volatile("" : "+v"(lane_key), "+v"(lane_at));
+    }
     auto key = [&](uint32_t i) { return L == kWave ? lane_value(lane_key, i) : keys[i]; };
     auto at = [&](uint32_t i) { return L == kWave ? lane_value(lane_at, i) : ats[i]; };
-    const uint32_t next = begin + count < a.n ? keys[count] : ~0u;   // no key is ~0
-    bool before = begin > 0 && s.keys[begin - 1] == key(0);
     float sum[V] = {};
     for (uint32_t i0 = 0; i0 < count; i0 += kInFlight) {
-        float r[kInFlight][V];
+        typename Cols::Vec r[kInFlight];
 #pragma unroll
-        for (uint32_t b = 0; b < kInFlight; ++b)
-            if (i0 + b < count && key(i0 + b) < a.vocab)
-                load_some<V>(rows + at(i0 + b) * a.dout_stride, left, 0.0f, r[b]);
+        for (uint32_t b = 0; b < kInFlight; ++b)   // the last row again behind the end: no branch between the loads
+            r[b] = cols.load(rows + at(i0 + b < count ? i0 + b : count - 1) * a.dout_stride);
 #pragma unroll
         for (uint32_t b = 0; b < kInFlight; ++b) {
             const uint32_t i = i0 + b;
             if (i >= count) break;
             const uint32_t id = key(i);
-            if (id >= a.vocab) break;
+            if (L < kWave && id >= a.vocab) break;
+            float x[V];
+            widen<T>(r[b], x);
 #pragma unroll
-            for (int j = 0; j < V; ++j) sum[j] += r[b][j];
-            const bool last = i + 1 == count;
-            const uint32_t then = last ? next : key(i + 1);
+            for (int j = 0; j < V; ++j) sum[j] += x[j];
+            const bool last = i + 1 == s.piece || begin + i + 1 == a.n;
+            const uint32_t then = last ? next : i + 1 < count ? key(i + 1) : ~0u;
             if (then == id && !last) continue;
-            if (!before && then != id) store_row<O, V>(a, id, col, left, sum);
-            else store_some<V>(s.parts + (static_cast<uint64_t>(piece) * 2 + (before ? 0 : 1)) * a.width + col, left, sum);
+            if (!before && then != id) store_row<T, O>(a, id, cols, sum);
+            else cols.store(s.parts + (static_cast<uint64_t>(piece) * 2 + (before ? 0 : 1)) * a.width, sum);
             before = false;
 #pragma unroll
             for (int j = 0; j < V; ++j) sum[j] = 0.0f;
@@ -370,68 +407,129 @@ __global__ __launch_bounds__(kMoveBlock) void embed_sum_kernel(EmbedGradArgs a, 
     }
 }
 
-constexpr int kJoinBlock = 512;
+constexpr int kJoinBlock = 1024;
+constexpr uint32_t kFewParts = 8;   // that L lanes join by themselves
 
-// A block for each piece (and 64 vectors): if a token begins in it and goes
-// on, its parts, a run of them for each L lanes, then the runs.
-template <class T, class O, int L>
-__global__ __launch_bounds__(kJoinBlock) void embed_join_kernel(EmbedGradArgs a, Sorted s) {
-    constexpr int V = kVec<T>;
-    constexpr uint32_t kWorkers = kJoinBlock / L;
-    __shared__ float s_sum[kWorkers][L * V];
-    const uint32_t piece = block_id() / s.chunks;
-    const uint64_t end = (static_cast<uint64_t>(piece) + 1) * s.piece;
-    if (end >= a.n) return;   // the last piece's tokens end there
-    const uint32_t id = s.keys[end - 1];
-    if (id >= a.vocab || s.keys[end] != id) return;
-    const uint64_t begin = end - s.piece;
-    if (s.keys[begin] == id && begin > 0 && s.keys[begin - 1] == id) return;   // begins in an earlier piece
-    // pieces that begin with the token: behind `piece` up to the last one, found by halving
-    uint32_t lo = piece + 1, hi = static_cast<uint32_t>((a.n - 1) / s.piece);
-    while (lo < hi) {
-        const uint32_t mid = hi - (hi - lo) / 2;
-        if (s.keys[static_cast<uint64_t>(mid) * s.piece] == id) lo = mid;
-        else hi = mid - 1;
-    }
-    const uint32_t count = lo - piece + 1;
-    const uint32_t run = (count + kWorkers - 1) / kWorkers;
-    const uint32_t worker = threadIdx.x / L, lane = threadIdx.x % L;
-    const uint32_t col = (block_id() % s.chunks * L + lane) * V;
-    const uint32_t left = col < a.width ? a.width - col : 0u;
-    const uint32_t stop = (worker + 1) * run < count ? (worker + 1) * run : count;
-    float sum[V] = {};
-    for (uint32_t i0 = worker * run; i0 < stop; i0 += 4) {
-        float r[4][V];
+// The sum of parts first .. stop of a token that begins in `piece`: its last
+// token's, then the first ones' of the pieces behind.
+template <class Cols>
+__device__ __forceinline__ void sum_parts(const Sorted& s, uint32_t width, uint32_t piece, uint32_t first, uint32_t stop,
+                                          const Cols& cols, float (&sum)[Cols::V]) {
+    constexpr int V = Cols::V;
+    constexpr uint32_t kAhead = 4;
 #pragma unroll
-        for (uint32_t b = 0; b < 4; ++b)
+    for (int j = 0; j < V; ++j) sum[j] = 0.0f;
+    for (uint32_t i0 = first; i0 < stop; i0 += kAhead) {
+        float r[kAhead][V];
+#pragma unroll
+        for (uint32_t b = 0; b < kAhead; ++b)
             if (i0 + b < stop)
-                load_some<V>(s.parts + (static_cast<uint64_t>(piece + i0 + b) * 2 + (i0 + b == 0 ? 1 : 0)) * a.width + col, left, 0.0f, r[b]);
+                load_some<V>(s.parts + (static_cast<uint64_t>(piece + i0 + b) * 2 + (i0 + b == 0 ? 1 : 0)) * width + cols.at,
+                             cols.left, 0.0f, r[b]);
 #pragma unroll
-        for (uint32_t b = 0; b < 4; ++b) {
+        for (uint32_t b = 0; b < kAhead; ++b) {
             if (i0 + b >= stop) break;
 #pragma unroll
             for (int j = 0; j < V; ++j) sum[j] += r[b][j];
         }
     }
-    const uint32_t workers = (count + run - 1) / run;
-    if (worker < workers) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) s_sum[worker][j * L + lane] = sum[j];
-    }
-    __syncthreads();
-    if (worker != 0) return;
-    for (uint32_t w = 1; w < workers; ++w) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) sum[j] += s_sum[w][j * L + lane];
-    }
-    store_row<O, V>(a, id, col, left, sum);
 }
 
+// L lanes for each piece (and 64 vectors): if a token begins in it and goes on,
+// they join its parts, or, if there are many, all of the block do, a run of
+// them each, then the runs.
+template <class T, class O, int L>
+__global__ __launch_bounds__(kJoinBlock) void embed_join_kernel(EmbedGradArgs a, Sorted s) {
+    constexpr int V = kVec<T>;
+    constexpr uint32_t kWorkers = kJoinBlock / L;
+    __shared__ float s_sum[kWorkers][L * V];
+    __shared__ uint32_t s_many, s_piece[kWorkers], s_count[kWorkers], s_id[kWorkers];   // tokens of many parts
+    const uint32_t worker = threadIdx.x / L, lane = threadIdx.x % L;
+    const uint32_t piece0 = block_id() / s.chunks * kWorkers;
+    const Columns<T, L == kWave> cols(block_id() % s.chunks * L + lane, a.width);
+    const uint32_t piece = piece0 + worker;
+    const uint64_t end = (static_cast<uint64_t>(piece) + 1) * s.piece;
+    uint32_t count = 0, id = a.vocab;
+    if (threadIdx.x == 0) s_many = 0;
+    __syncthreads();
+    if (end < a.n) {   // the last piece's tokens end there
+        const uint64_t begin = end - s.piece;
+        id = s.keys[end - 1];
+        const bool goes_on = s.keys[end] == id;
+        const bool whole = s.keys[begin] == id;
+        if (id < a.vocab && goes_on && !(whole && begin > 0 && s.keys[begin - 1] == id)) {
+            // pieces that begin with the token: behind `piece` up to the last one, found by halving
+            uint32_t lo = piece + 1, hi = static_cast<uint32_t>((a.n - 1) / s.piece);
+            if (hi - lo > kFewParts && s.keys[static_cast<uint64_t>(lo + kFewParts) * s.piece] != id) hi = lo + kFewParts - 1;
+            while (lo < hi) {
+                const uint32_t mid = hi - (hi - lo) / 2;
+                if (s.keys[static_cast<uint64_t>(mid) * s.piece] == id) lo = mid;
+                else hi = mid - 1;
+            }
+            count = lo - piece + 1;
+        }
+    }
+    float sum[V];
+    if (count > 0 && count <= kFewParts) {
+        sum_parts(s, a.width, piece, 0, count, cols, sum);
+        store_row<T, O>(a, id, cols, sum);
+    }
+    if (lane == 0 && count > kFewParts) {   // in any order: each token has its own row
+        const uint32_t i = atomicAdd(&s_many, 1u);
+        s_piece[i] = piece;
+        s_count[i] = count;
+        s_id[i] = id;
+    }
+    __syncthreads();
+    const uint32_t many = s_many;
+    for (uint32_t i = 0; i < many; ++i) {
+        count = s_count[i];
+        const uint32_t run = (count + kWorkers - 1) / kWorkers;
+        const uint32_t workers = (count + run - 1) / run;
+        if (worker < workers) {
+            sum_parts(s, a.width, s_piece[i], worker * run, worker + 1 < workers ? (worker + 1) * run : count, cols, sum);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s_sum[worker][j * L + lane] = sum[j];
+        }
+        __syncthreads();
+        if (worker == 0) {
+            for (uint32_t x = 1; x < workers; ++x) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) sum[j] += s_sum[x][j * L + lane];
+            }
+            store_row<T, O>(a, s_id[i], cols, sum);
+        }
+        __syncthreads();
+    }
+}
+
+#ifndef OWNMAX
+#define OWNMAX uint64_t{kMaxTiles} * kSortBlock * 4
+#endif
 // ---- launches ---------------------------------------------------------------------------------
 
-uint32_t sort_items(uint64_t n) { return n <= kMaxTiles * kSortBlock ? 1 : n <= kMaxTiles * kSortBlock * 4 ? 4 : 16; }
-bool own_sort(uint64_t n) { return n <= uint64_t{kMaxTiles} * kSortBlock * 16; }
-uint32_t piece_of(uint64_t n) { return n <= 1u << 15 ? 16 : n <= 1u << 17 ? 32 : 64; }
+uint32_t sort_items(uint64_t n) { return n <= kMaxTiles * kSortBlock ? 1 : 4; }
+bool own_sort(uint64_t n) { return n <= OWNMAX; }
+#ifndef PW
+#define PW 4096
+#endif
+// Lanes that take a row's vectors of T, 64 for one of several chunks, and the chunks.
+struct Lanes {
+    uint32_t lanes, chunks;
+};
+Lanes lanes_of(uint64_t vectors) {
+    if (vectors <= 4) return {4, 1};
+    if (vectors <= 16) return {16, 1};
+    return {kWave, static_cast<uint32_t>(up(vectors, kWave))};
+}
+
+// Positions of a piece: 8 to 64, so that the waves fill the chip.
+uint32_t piece_of(uint64_t n, uint64_t vectors) {
+    const Lanes l = lanes_of(vectors);
+    uint32_t piece = 8;
+    while (piece < 64 && n * l.chunks * l.lanes / kWave >= uint64_t{piece} * 2 * PW) piece *= 2;
+    return piece;
+}
 
 size_t up256(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
@@ -439,11 +537,13 @@ size_t up256(size_t bytes) { return (bytes + 255) / 256 * 256; }
 // temp, which tokens occur, the parts.
 struct Temp {
     size_t array, sort, occurs, parts;
-    Temp(uint64_t n, uint32_t vocab, uint32_t width) {
+    uint32_t piece;
+    Temp(uint64_t n, uint32_t vocab, uint32_t width, uint32_t vector) {
         array = up256(n * sizeof(uint32_t));
         sort = own_sort(n) ? kMaxTiles * sizeof(uint32_t) << kMaxBits : up256(sort_temp_bytes(n, true, SortKind{}));
         occurs = up256(vocab);
-        parts = n > piece_of(n) ? up256(up(n, piece_of(n)) * 2 * width * sizeof(float)) : 0;
+        piece = piece_of(n, up(width, vector));
+        parts = n > piece ? up256(up(n, piece) * 2 * width * sizeof(float)) : 0;
     }
     size_t bytes() const { return 4 * array + sort + occurs + parts; }
 };
@@ -461,7 +561,8 @@ hipError_t sort_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&keys)[2
     auto riders = [&](bool known) {
         z.occurs = known ? p.occurs : nullptr;
         z.first = z.last;
-        const uint64_t rows = ride < a.vocab - z.first ? ride : a.vocab - z.first;
+        uint64_t rows = ride < a.vocab - z.first ? ride : a.vocab - z.first;
+        if (!known && a.n > a.vocab / 4) rows = 0;   // too many would be written twice
         z.last += static_cast<uint32_t>(rows);
         return static_cast<uint32_t>(up(up(rows, z.each), kSortWaves));
     };
@@ -475,14 +576,14 @@ hipError_t sort_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&keys)[2
         if (p.tiles > 1 || (k == 0 && p.occurs)) {
             const uint32_t beside = riders(k > 0);
             timing_before(stream, RS_KERNEL_EMBED_SORT);
-            const auto kernel = items == 1 ? embed_count_kernel<O, 1> : items == 4 ? embed_count_kernel<O, 4> : embed_count_kernel<O, 16>;
+            const auto kernel = items == 1 ? embed_count_kernel<O, 1> : embed_count_kernel<O, 4>;
             kernel<<<dim3(p.tiles + beside), kSortBlock, 0, stream>>>(p, z, k == 0);
             const hipError_t e = done(stream);
             if (e != hipSuccess) return e;
         }
         const uint32_t beside = riders(k > 0);
         timing_before(stream, RS_KERNEL_EMBED_SORT);
-        const auto kernel = items == 1 ? embed_place_kernel<O, 1> : items == 4 ? embed_place_kernel<O, 4> : embed_place_kernel<O, 16>;
+        const auto kernel = items == 1 ? embed_place_kernel<O, 1> : embed_place_kernel<O, 4>;
         kernel<<<dim3(p.tiles + beside), kSortBlock, 0, stream>>>(p, z);
         const hipError_t e = done(stream);
         if (e != hipSuccess) return e;
@@ -526,20 +627,20 @@ hipError_t sum_tokens(const EmbedGradArgs& a, Sorted s, const Zeros& z, hipStrea
     }
     if (e != hipSuccess || pieces <= 1) return e;
     timing_before(stream, RS_KERNEL_EMBED_JOIN);
-    embed_join_kernel<T, O, L><<<many_blocks(pieces * s.chunks), kJoinBlock, 0, stream>>>(a, s);
+    embed_join_kernel<T, O, L><<<many_blocks(up(pieces, kJoinBlock / L) * s.chunks), kJoinBlock, 0, stream>>>(a, s);
     return done(stream);
 }
 
 template <class T, class O>
 hipError_t embed_grad_of(const EmbedGradArgs& a, void* temp, hipStream_t stream) {
-    const Temp size(a.n, a.vocab, a.width);
+    const Temp size(a.n, a.vocab, a.width, kVec<T>);
     char* base = static_cast<char*>(temp);
     auto words = [&](size_t offset) { return reinterpret_cast<uint32_t*>(base + offset); };
     uint32_t* const keys[2] = {words(0), words(2 * size.array)};
     uint32_t* const at[2] = {words(size.array), words(3 * size.array)};
     void* sort = base + 4 * size.array;
     uint8_t* occurs = reinterpret_cast<uint8_t*>(base + 4 * size.array + size.sort);
-    Sorted s{keys[0], at[0], reinterpret_cast<float*>(occurs + size.occurs), piece_of(a.n), 1};
+    Sorted s{keys[0], at[0], reinterpret_cast<float*>(occurs + size.occurs), size.piece, 1};
 
     Zeros z{a.dtable, a.dtable_stride, nullptr, 0, 0, a.width, 1, 6};
     const uint64_t row_bytes = uint64_t{a.width} * sizeof(O);
@@ -563,11 +664,10 @@ hipError_t embed_grad_of(const EmbedGradArgs& a, void* temp, hipStream_t stream)
     }
     z.first = z.last;   // what the sort's launches did not fill
     z.last = a.accumulate ? z.first : a.vocab;
-    const uint32_t vectors = static_cast<uint32_t>(up(a.width, kVec<T>));
-    if (vectors <= 4) return sum_tokens<T, O, 4>(a, s, z, stream);
-    if (vectors <= 16) return sum_tokens<T, O, 16>(a, s, z, stream);
-    s.chunks = static_cast<uint32_t>(up(vectors, kWave));
-    return sum_tokens<T, O, kWave>(a, s, z, stream);
+    const Lanes l = lanes_of(up(a.width, kVec<T>));
+    s.chunks = l.chunks;
+    return l.lanes == 4 ? sum_tokens<T, O, 4>(a, s, z, stream) : l.lanes == 16 ? sum_tokens<T, O, 16>(a, s, z, stream)
+                                                                             : sum_tokens<T, O, kWave>(a, s, z, stream);
 }
 
 }  // namespace
@@ -583,7 +683,9 @@ hipError_t launch_embed(int elem_type, const EmbedArgs& a, hipStream_t stream) {
     }
 }
 
-size_t embed_grad_temp_bytes(uint64_t n, uint32_t vocab, uint32_t width) { return Temp(n, vocab, width).bytes(); }
+size_t embed_grad_temp_bytes(int elem_type, uint64_t n, uint32_t vocab, uint32_t width) {
+    return Temp(n, vocab, width, elem_type == RS_ELEM_F32 ? kVec<float> : kVec<__bf16>).bytes();
+}
 
 hipError_t launch_embed_grad(int elem_type, int table_type, const EmbedGradArgs& a, void* temp, hipStream_t stream) {
     const bool f32 = table_type == RS_ELEM_F32;

@@ -236,7 +236,7 @@ struct EmbedGradArgs {
     void* dtable;
     uint64_t dtable_stride;
 };
-size_t embed_grad_temp_bytes(uint64_t n, uint32_t vocab, uint32_t width);
+size_t embed_grad_temp_bytes(int elem_type, uint64_t n, uint32_t vocab, uint32_t width);
 hipError_t launch_embed_grad(int elem_type, int table_type, const EmbedGradArgs& a, void* temp,
                              hipStream_t stream);
 

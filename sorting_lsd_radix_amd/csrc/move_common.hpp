@@ -13,6 +13,9 @@ constexpr int kMoveWaves = kMoveBlock / kWave;
 template <class T>
 constexpr int kVec = 16 / sizeof(T);
 
+// The wave's number in its block, known to be the same for the whole wave.
+__device__ __forceinline__ uint32_t wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); }
+
 // The value of lane `from`, the same lane for the whole wave.
 __device__ __forceinline__ uint32_t lane_value(uint32_t x, uint32_t from) {
     return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), static_cast<int>(from)));

@@ -826,7 +826,7 @@ rs_status rs_embed_tokens_grad(rs_elem_type elem_type, const void* dout, uint64_
     if (n >= RS_MAX_N || vocab >= RS_MAX_N || width >= RS_MAX_N || n * width > (uint64_t{1} << 38))
         return RS_ERR_UNSUPPORTED_SIZE;
     if (vocab == 0 || width == 0 || !(scale - scale == 0.0f)) return RS_ERR_INVALID_VALUE;
-    const size_t need = embed_grad_temp_bytes(n, vocab, width);
+    const size_t need = embed_grad_temp_bytes(elem_type, n, vocab, width);
     if (d_temp == nullptr) {
         *temp_bytes = need;
         return RS_OK;
