@@ -50,7 +50,7 @@ __device__ __forceinline__ bool owns(const uint32_t* order, uint32_t room, uint3
 template <class T, int U, bool WEIGHTS>
 __global__ __launch_bounds__(kMoveBlock) void gather_kernel(GatherArgs a, uint32_t parts, uint32_t fill,
                                                             uint32_t each) {
-    const uint32_t unit = block_id() * kMoveWaves + threadIdx.x / kWave;
+    const uint32_t unit = block_id() * kMoveWaves + wave_id();
     if (unit < fill) return fill_rows<T, U, WEIGHTS>(a, unit, parts, each);
     const uint32_t t = (unit - fill) / parts, part = (unit - fill) % parts;
     if (t >= a.rows) return;
@@ -59,8 +59,9 @@ __global__ __launch_bounds__(kMoveBlock) void gather_kernel(GatherArgs a, uint32
     const RowPart<T, U> row(part, a.width);
     typename RowPart<T, U>::Vec x[U];
     row.load(static_cast<const T*>(a.x) + t * a.x_stride, x);
-    const uint32_t p = lane < a.top_k ? a.place[c] : ~0u;
-    const float w = WEIGHTS && lane < a.top_k ? a.weights[c] : 0.0f;
+    uint32_t p = lane < a.top_k ? a.place[c] : ~0u;
+    float w = WEIGHTS && lane < a.top_k ? a.weights[c] : 0.0f;
+    arrived(p, w);
     uint64_t todo = ballot(owns(a.order, a.room, p, c));
     while (todo) {
         const uint32_t l = __builtin_ctzll(todo);
@@ -85,13 +86,14 @@ template <class T, bool WEIGHTS, bool ONCE>
 __global__ __launch_bounds__(kMoveBlock) void combine_kernel(CombineArgs a, uint32_t parts) {
     using Row = RowPart<T, 1>;
     constexpr int V = kVec<T>;
-    const uint32_t unit = block_id() * kMoveWaves + threadIdx.x / kWave;
+    const uint32_t unit = block_id() * kMoveWaves + wave_id();
     const uint32_t t = unit / parts;
     if (t >= a.rows) return;
     const uint32_t lane = lane_id();
     const Row row(unit % parts, a.width);
-    const uint32_t p = lane < a.top_k ? a.place[t * a.top_k + lane] : ~0u;
-    const float w = WEIGHTS && lane < a.top_k ? a.weights[t * a.top_k + lane] : 1.0f;
+    uint32_t p = lane < a.top_k ? a.place[t * a.top_k + lane] : ~0u;
+    float w = WEIGHTS && lane < a.top_k ? a.weights[t * a.top_k + lane] : 1.0f;
+    arrived(p, w);
     float sum[V] = {};
     for (uint64_t todo = ballot(p < a.room); todo != 0;) {
         typename Row::Vec r[kBatch][1];
@@ -121,14 +123,14 @@ __global__ __launch_bounds__(kMoveBlock) void combine_kernel(CombineArgs a, uint
 
 // Gradients, WAVES waves a row: the products of x_t with the rows of y at its
 // choices, and beside them the sum of those rows by their weights (SUM), or x_t
-// times each weight at its choices' positions in g.y.
-template <class T, int WAVES, bool SUM>
+// times each weight at its choices' positions in g.y.  MANY: more than kBatch choices a row.
+template <class T, int WAVES, bool SUM, bool MANY>
 __global__ __launch_bounds__(kMoveBlock, 4) void products_kernel(CombineArgs a, GatherArgs g, uint32_t fill,
                                                                  uint32_t fill_parts, uint32_t each) {
     using Row = RowPart<T, 1>;
     constexpr int V = kVec<T>;
     __shared__ float s_dots[kMoveWaves][RS_MAX_TOP_K];
-    const uint32_t wave = threadIdx.x / kWave, lane = lane_id();
+    const uint32_t wave = wave_id(), lane = lane_id();
     if (!SUM && block_id() < fill) return fill_rows<T, 4, true>(g, block_id() * kMoveWaves + wave, fill_parts, each);
     const uint32_t t = ((block_id() - fill) * kMoveWaves + wave) / WAVES;
     const bool real = t < a.rows;
@@ -136,8 +138,9 @@ __global__ __launch_bounds__(kMoveBlock, 4) void products_kernel(CombineArgs a, 
     wave_fence();
     if (real) {
         const uint32_t c = t * a.top_k + lane;
-        const uint32_t p = lane < a.top_k ? a.place[c] : ~0u;
-        const float w = lane < a.top_k ? a.weights[c] : 0.0f;
+        uint32_t p = lane < a.top_k ? a.place[c] : ~0u;
+        float w = lane < a.top_k ? a.weights[c] : 0.0f;
+        arrived(p, w);
         const uint64_t valid = ballot(p < a.room);
         const uint64_t owned = SUM ? 0 : ballot(owns(g.order, g.room, p, c));
         const uint32_t steps = (a.width + kWave * V - 1) / (kWave * V);
@@ -149,7 +152,8 @@ __global__ __launch_bounds__(kMoveBlock, 4) void products_kernel(CombineArgs a, 
             typename Row::Vec xr[1];
             row.load(x_row, xr);
             float x[V], sum[V] = {};
-            for (uint64_t todo = valid; todo != 0;) {
+            uint64_t todo = valid;
+            do {   // once without MANY, so that the load of x goes out with the others
                 typename Row::Vec r[kBatch][1];
                 uint32_t l[kBatch], n = 0;
 #pragma unroll
@@ -175,7 +179,7 @@ __global__ __launch_bounds__(kMoveBlock, 4) void products_kernel(CombineArgs a, 
 #pragma unroll
                     for (uint32_t e = 0; e < V; ++e) dot[b] = fmaf(x[e], y[e], dot[b]);
                 }
-                if (a.top_k > kBatch) {
+                if (MANY) {
 #pragma unroll
                     for (uint32_t b = 0; b < kBatch; ++b) {
                         if (b >= n) break;
@@ -184,19 +188,19 @@ __global__ __launch_bounds__(kMoveBlock, 4) void products_kernel(CombineArgs a, 
                         dot[b] = 0.0f;
                     }
                 }
-            }
+            } while (MANY && todo != 0);
             if (SUM) {
                 const typename Row::Vec v[1] = {narrow<T>(sum)};
                 row.store(static_cast<T*>(a.out) + t * a.out_stride, v);
             } else {
-                for (uint64_t todo = owned; todo != 0; todo &= todo - 1) {
-                    const uint32_t b = __builtin_ctzll(todo);
+                for (uint64_t own_places = owned; own_places != 0; own_places &= own_places - 1) {
+                    const uint32_t b = __builtin_ctzll(own_places);
                     const typename Row::Vec v[1] = {scaled<T>(xr[0], lane_value(w, b))};
                     row.store(static_cast<T*>(g.y) + lane_value(p, b) * g.y_stride, v);
                 }
             }
         }
-        if (a.top_k <= kBatch) {
+        if (!MANY) {
             uint64_t todo = valid;
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
@@ -401,9 +405,12 @@ hipError_t products_of(const CombineArgs& a, const GatherArgs& g, hipStream_t st
     const uint32_t each = fill_each(g.room, static_cast<uint64_t>(a.rows) * a.top_k);
     const uint32_t fill = SUM ? 0 : static_cast<uint32_t>(up(up(g.room, each) * parts, kMoveWaves));
     return timed(RS_KERNEL_COMBINE, stream, [&] {
-        const auto kernel = vectors <= kWave ? products_kernel<T, 1, SUM> : vectors <= 2 * kWave ? products_kernel<T, 2, SUM>
-                                                                                                 : products_kernel<T, 4, SUM>;
-        kernel<<<many_blocks(fill + up(uint64_t{a.rows} * waves, kMoveWaves)), kMoveBlock, 0, stream>>>(a, g, fill, parts, each);
+        pick(a.top_k > kBatch, [&](auto many) {
+            constexpr bool MANY = decltype(many)::value;
+            const auto kernel = waves == 1 ? products_kernel<T, 1, SUM, MANY> : waves == 2 ? products_kernel<T, 2, SUM, MANY>
+                                                                                           : products_kernel<T, 4, SUM, MANY>;
+            kernel<<<many_blocks(fill + up(uint64_t{a.rows} * waves, kMoveWaves)), kMoveBlock, 0, stream>>>(a, g, fill, parts, each);
+        });
     });
 }
 

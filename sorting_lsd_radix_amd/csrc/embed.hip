@@ -36,7 +36,7 @@ uint64_t up(uint64_t n, uint64_t d) { return (n + d - 1) / d; }
 // A wave for each part of a row of more than 32 vectors.
 template <class T, int U, bool SCALED>
 __global__ __launch_bounds__(kMoveBlock) void embed_kernel(EmbedArgs a, uint32_t parts) {
-    const uint32_t unit = block_id() * kMoveWaves + threadIdx.x / kWave;
+    const uint32_t unit = block_id() * kMoveWaves + wave_id();
     const uint32_t i = unit / parts;
     if (i >= a.n) return;
     const uint32_t id = a.ids[i];
@@ -353,7 +353,7 @@ template <class T, class O, int L>
 __global__ __launch_bounds__(kMoveBlock) void embed_sum_kernel(EmbedGradArgs a, Sorted s, Zeros z, uint32_t sums) {
     constexpr int V = kVec<T>;
     using Cols = Columns<T, L == kWave>;
-    if (block_id() >= sums) return zero_rows<O>(z, static_cast<uint64_t>(block_id() - sums) * kMoveWaves + threadIdx.x / kWave);
+    if (block_id() >= sums) return zero_rows<O>(z, static_cast<uint64_t>(block_id() - sums) * kMoveWaves + wave_id());
     const uint32_t unit = block_id() * (kMoveBlock / L) + (L == kWave ? wave_id() : threadIdx.x / L);
     const uint32_t piece = unit / s.chunks;
     const uint64_t begin = static_cast<uint64_t>(piece) * s.piece;
@@ -374,8 +374,7 @@ __global__ __launch_bounds__(kMoveBlock) void embed_sum_kernel(EmbedGradArgs a, 
             lane_at = ats[lane];
         }
         count = __builtin_popcountll(ballot(lane_key < a.vocab));   // the others are last
-        // what follows reads them across lanes, and must not wait for them between the rows' loads
-        asm volatile("" : "+v"(lane_key), "+v"(lane_at));
+        arrived(lane_key, lane_at);
     }
     auto key = [&](uint32_t i) { return L == kWave ? lane_value(lane_key, i) : keys[i]; };
     auto at = [&](uint32_t i) { return L == kWave ? lane_value(lane_at, i) : ats[i]; };
