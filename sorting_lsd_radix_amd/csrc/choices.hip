@@ -46,14 +46,14 @@ __device__ __forceinline__ bool owns(const uint32_t* order, uint32_t room, uint3
 }
 
 // A wave for each part of a row, which it reads once and writes to all its
-// choices' positions; the first `fill` waves write the other positions, `each` a wave.
+// choices' positions; the waves behind write the other positions, `each` a wave (in
+// front of the rows' waves they took 131072 choices in 163584 positions of 4096 bf16 from 282 us to 297).
 template <class T, int U, bool WEIGHTS>
-__global__ __launch_bounds__(kMoveBlock) void gather_kernel(GatherArgs a, uint32_t parts, uint32_t fill,
-                                                            uint32_t each) {
+__global__ __launch_bounds__(kMoveBlock) void gather_kernel(GatherArgs a, uint32_t parts, uint32_t each) {
     const uint32_t unit = block_id() * kMoveWaves + wave_id();
-    if (unit < fill) return fill_rows<T, U, WEIGHTS>(a, unit, parts, each);
-    const uint32_t t = (unit - fill) / parts, part = (unit - fill) % parts;
-    if (t >= a.rows) return;
+    const uint32_t rows = a.rows * parts;   // waves
+    if (unit >= rows) return fill_rows<T, U, WEIGHTS>(a, unit - rows, parts, each);
+    const uint32_t t = unit / parts, part = unit % parts;
     const uint32_t lane = lane_id();
     const uint32_t c = t * a.top_k + lane;
     const RowPart<T, U> row(part, a.width);
@@ -358,14 +358,13 @@ hipError_t gather_of(const GatherArgs& a, hipStream_t stream) {
                 gather_narrow_kernel<T, L, WEIGHTS><<<many_blocks(up(a.room, kMoveBlock / L * kRowsEach)), kMoveBlock, 0, stream>>>(a);
             });
         });
-    const Split s = split_rows(vectors, a.rows);
+    const Split s = split_rows(vectors, a.rows, 4);
     const uint32_t each = fill_each(a.room, static_cast<uint64_t>(a.rows) * a.top_k);
-    const uint32_t fill = static_cast<uint32_t>(up(a.room, each) * s.parts);
-    const dim3 grid = many_blocks(up(fill + static_cast<uint64_t>(a.rows) * s.parts, kMoveWaves));
+    const dim3 grid = many_blocks(up((a.rows + up(a.room, each)) * s.parts, kMoveWaves));
     return timed(RS_KERNEL_GATHER, stream, [&] {
         const auto kernel = s.unroll == 1 ? gather_kernel<T, 1, WEIGHTS> : s.unroll == 2 ? gather_kernel<T, 2, WEIGHTS>
                                                                                          : gather_kernel<T, 4, WEIGHTS>;
-        kernel<<<grid, kMoveBlock, 0, stream>>>(a, s.parts, fill, each);
+        kernel<<<grid, kMoveBlock, 0, stream>>>(a, s.parts, each);
     });
 }
 
@@ -383,8 +382,7 @@ hipError_t combine_of(const CombineArgs& a, hipStream_t stream) {
     return timed(RS_KERNEL_COMBINE, stream, [&] {
         pick(large(static_cast<uint64_t>(a.rows) * a.top_k * a.width * sizeof(T)), [&](auto once) {
             constexpr bool ONCE = decltype(once)::value;
-            combine_kernel<T, WEIGHTS, ONCE><<<many_blocks(up(static_cast<uint64_t>(a.rows) * parts, kMoveWaves)), kMoveBlock, 0,
-                                               stream>>>(a, parts);
+            combine_kernel<T, WEIGHTS, ONCE><<<many_blocks(up(static_cast<uint64_t>(a.rows) * parts, kMoveWaves)), kMoveBlock, 0, stream>>>(a, parts);
         });
     });
 }

@@ -87,9 +87,8 @@ hipError_t embed_of(const EmbedArgs& a, hipStream_t stream) {
                                                                                          : embed_narrow_kernel<T, 32, SCALED>;
         kernel<<<many_blocks(up(a.n, kMoveBlock / lanes)), kMoveBlock, 0, stream>>>(a);
     } else {
-        const Split s = split_rows(vectors, a.n);
-        const auto kernel = s.unroll == 1 ? embed_kernel<T, 1, SCALED> : s.unroll == 2 ? embed_kernel<T, 2, SCALED>
-                                                                                       : embed_kernel<T, 4, SCALED>;
+        const Split s = split_rows(vectors, a.n, 2);
+        const auto kernel = s.unroll == 1 ? embed_kernel<T, 1, SCALED> : embed_kernel<T, 2, SCALED>;
         kernel<<<many_blocks(up(static_cast<uint64_t>(a.n) * s.parts, kMoveWaves)), kMoveBlock, 0, stream>>>(a, s.parts);
     }
     return done(stream);
@@ -350,10 +349,13 @@ constexpr int kInFlight = IF;
 // L lanes take a piece and 64 vectors of the rows, or, L < 64, all of them.
 // Blocks behind the last piece fill the rows without tokens.
 template <class T, class O, int L>
-__global__ __launch_bounds__(kMoveBlock) void embed_sum_kernel(EmbedGradArgs a, Sorted s, Zeros z, uint32_t sums) {
+__global__ __launch_bounds__(kMoveBlock) void embed_sum_kernel(EmbedGradArgs a, Sorted s, Zeros z, uint32_t sums, uint32_t fill) {
     constexpr int V = kVec<T>;
     using Cols = Columns<T, L == kWave>;
-    if (block_id() >= sums) return zero_rows<O>(z, static_cast<uint64_t>(block_id() - sums) * kMoveWaves + wave_id());
+    if (block_id() >= sums) {
+        if (block_id() - sums < fill) zero_rows<O>(z, static_cast<uint64_t>(xcd_run(block_id() - sums, fill)) * kMoveWaves + wave_id());
+        return;
+    }
     const uint32_t unit = block_id() * (kMoveBlock / L) + (L == kWave ? wave_id() : threadIdx.x / L);
     const uint32_t piece = unit / s.chunks;
     const uint64_t begin = static_cast<uint64_t>(piece) * s.piece;
@@ -616,12 +618,12 @@ hipError_t sort_many_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&ke
 template <class T, class O, int L>
 hipError_t sum_tokens(const EmbedGradArgs& a, Sorted s, const Zeros& z, hipStream_t stream) {
     const uint64_t pieces = up(a.n, s.piece);
-    const uint64_t sums = up(pieces * s.chunks, kMoveBlock / L);
-    const uint64_t fill = up(up(z.last - z.first, z.each), kMoveWaves);
+    const uint32_t sums = static_cast<uint32_t>(up(pieces * s.chunks, kMoveBlock / L * 8) * 8);   // a multiple of the XCDs
+    const uint32_t fill = static_cast<uint32_t>(up(up(z.last - z.first, z.each), kMoveWaves));
     hipError_t e = hipSuccess;
     if (sums + fill > 0) {
         timing_before(stream, RS_KERNEL_EMBED_SUM);
-        embed_sum_kernel<T, O, L><<<many_blocks(sums + fill), kMoveBlock, 0, stream>>>(a, s, z, static_cast<uint32_t>(sums));
+        embed_sum_kernel<T, O, L><<<many_blocks(uint64_t{sums} + fill), kMoveBlock, 0, stream>>>(a, s, z, sums, fill);
         e = done(stream);
     }
     if (e != hipSuccess || pieces <= 1) return e;
@@ -643,7 +645,7 @@ hipError_t embed_grad_of(const EmbedGradArgs& a, void* temp, hipStream_t stream)
 
     Zeros z{a.dtable, a.dtable_stride, nullptr, 0, 0, a.width, 1, 6};
     const uint64_t row_bytes = uint64_t{a.width} * sizeof(O);
-    while (z.each < 64 && z.each * row_bytes < 16384) z.each *= 2;
+    while (z.each < 64 && z.each * row_bytes < 4096) z.each *= 2;
     while (z.lanes_log2 > 0 && (kVec<O> << (z.lanes_log2 - 1)) >= a.width) --z.lanes_log2;
     const uint64_t ride = a.accumulate ? 0 : RIDE / row_bytes;
 

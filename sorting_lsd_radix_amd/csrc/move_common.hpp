@@ -16,6 +16,13 @@ constexpr int kVec = 16 / sizeof(T);
 // The wave's number in its block, known to be the same for the whole wave.
 __device__ __forceinline__ uint32_t wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); }
 
+// Block b of n in the order that gives each XCD (blocks go round all 8) one run of
+// the work.
+__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n) {
+    const uint32_t x = b & 7u, each = n >> 3, more = n & 7u;
+    return x * each + (x < more ? x : more) + (b >> 3);
+}
+
 // The value of lane `from`, the same lane for the whole wave.
 __device__ __forceinline__ uint32_t lane_value(uint32_t x, uint32_t from) {
     return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), static_cast<int>(from)));
@@ -115,15 +122,15 @@ __device__ __forceinline__ AnyVec<16>::V scaled(AnyVec<16>::V r, float w) {
 // with that kernel.
 inline bool large(uint64_t bytes) { return bytes > (uint64_t{96} << 20); }
 
-// How rows are split among waves: vectors of a lane (1, 2 or 4, so many that the
-// parts still fill the chip: 8192 waves), and parts of a row.
+// How rows are split among waves: vectors of a lane (1, 2 or 4, up to `most`, so
+// many that the parts still fill the chip), and parts of a row.
 struct Split {
     uint32_t unroll, parts;
 };
-inline Split split_rows(uint32_t vectors, uint64_t rows) {
+inline Split split_rows(uint32_t vectors, uint64_t rows, uint32_t most) {
     const uint32_t each = (vectors + kWave - 1) / kWave;   // vectors of a lane, were a row one wave's
     uint32_t u = 1;
-    while (u < 4 && u < each && rows * ((each + 2 * u - 1) / (2 * u)) >= 8192) u *= 2;
+    while (u < most && u < each && rows * ((each + 2 * u - 1) / (2 * u)) >= 4096) u *= 2;
     return Split{u, (each + u - 1) / u};
 }
 
