@@ -7,11 +7,15 @@
 // token begins joins them in order.  Nothing depends on the order in which
 // blocks run.
 //
-// Rows without a token are zeros.  The sort's launches are short chains of
-// dependent steps, so blocks beside them write zeros meanwhile: to the first rows
-// whatever their tokens, which is made good later, and once it is known which tokens
-// occur, to the others' rows only.  The rows that are left are filled beside
-// the sums.
+// Rows without a token are zeros.  Where tokens are few for the table's rows, blocks
+// beside the sort, whose launches are short chains of dependent steps, write all
+// rows, which the sums then make good.  Otherwise the sort's first pass marks the
+// tokens that occur, and the other rows are filled beside the sums (looking a row's
+// mark up costs a tenth of the filling's rate).
+//
+// What bounds it: 131072 rows of 2048 bf16 and 16384 tokens take 128 us, of which
+// the filling is some 95 (512 MB, 5.4 TB/s), the sums 20, the join 6; 32003 rows of
+// 1001 f32 and 50021 tokens 87: the sort 22, the sums and zeros 55 (5.0 TB/s), the join 8.
 #include "internal.hpp"
 #include "move_common.hpp"
 
@@ -19,9 +23,6 @@ namespace rs {
 
 namespace {
 
-#ifndef RIDE
-#define RIDE (24u << 20)
-#endif
 
 hipError_t done(hipStream_t stream) {
     const hipError_t e = hipGetLastError();
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(kSortBlock) void embed_count_kernel(Pass p, Zeros z
         for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kSortBlock + tid; i < words; i += static_cast<uint64_t>(gridDim.x) * kSortBlock)
             reinterpret_cast<uint32_t*>(p.occurs)[i] = 0;
     }
-    if (blockIdx.x >= p.tiles) return zero_rows<O>(z, static_cast<uint64_t>(blockIdx.x - p.tiles) * kSortWaves + tid / kWave);
+    if (blockIdx.x >= p.tiles) return zero_rows<O>(z, static_cast<uint64_t>(blockIdx.x - p.tiles) * kSortWaves + wave_id());
     const uint32_t base = blockIdx.x * (kSortBlock * ITEMS);
     s_count[tid] = 0;
     uint32_t d[ITEMS];
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(kSortBlock) void embed_place_kernel(Pass p, Zeros z
     __shared__ uint32_t s_wave[kSortWaves];
     const uint32_t tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
     const uint32_t tile = blockIdx.x;
-    if (tile >= p.tiles) return zero_rows<O>(z, static_cast<uint64_t>(tile - p.tiles) * kSortWaves + wave);
+    if (tile >= p.tiles) return zero_rows<O>(z, static_cast<uint64_t>(tile - p.tiles) * kSortWaves + wave_id());
     const uint32_t bins = 1u << p.bits;
     const uint32_t base = tile * (kSortBlock * ITEMS) + wave * (kWave * ITEMS) + lane;
     uint32_t key[ITEMS], at[ITEMS], rank[ITEMS];
@@ -341,10 +342,7 @@ struct Sorted {
     uint32_t chunks;   // of a row, or 1 where L lanes have it all
 };
 
-#ifndef IF
-#define IF 8
-#endif
-constexpr int kInFlight = IF;
+constexpr int kInFlight = 8;   // rows; 4 and 16 are within 2 %
 
 // L lanes take a piece and 64 vectors of the rows, or, L < 64, all of them.
 // Blocks behind the last piece fill the rows without tokens.
@@ -353,7 +351,7 @@ __global__ __launch_bounds__(kMoveBlock) void embed_sum_kernel(EmbedGradArgs a, 
     constexpr int V = kVec<T>;
     using Cols = Columns<T, L == kWave>;
     if (block_id() >= sums) {
-        if (block_id() - sums < fill) zero_rows<O>(z, static_cast<uint64_t>(xcd_run(block_id() - sums, fill)) * kMoveWaves + wave_id());
+        if (block_id() - sums < fill) zero_rows<O>(z, static_cast<uint64_t>((block_id() - sums, fill)) * kMoveWaves + wave_id());
         return;
     }
     const uint32_t unit = block_id() * (kMoveBlock / L) + (L == kWave ? wave_id() : threadIdx.x / L);
@@ -504,16 +502,13 @@ __global__ __launch_bounds__(kJoinBlock) void embed_join_kernel(EmbedGradArgs a,
     }
 }
 
-#ifndef OWNMAX
-#define OWNMAX uint64_t{kMaxTiles} * kSortBlock * 4
-#endif
 // ---- launches ---------------------------------------------------------------------------------
 
 uint32_t sort_items(uint64_t n) { return n <= kMaxTiles * kSortBlock ? 1 : 4; }
-bool own_sort(uint64_t n) { return n <= OWNMAX; }
-#ifndef PW
-#define PW 4096
-#endif
+bool own_sort(uint64_t n) { return n <= uint64_t{kMaxTiles} * kSortBlock * 4; }
+// Whether all rows are filled beside the sort.  131072 rows of 2048 bf16: with 32768
+// tokens 146 us, 156 filled by what occurs; with 65536 tokens 194 and 193.
+bool few_tokens(uint64_t n, uint32_t vocab) { return own_sort(n) && n > 0 && n <= vocab / 4; }
 // Lanes that take a row's vectors of T, 64 for one of several chunks, and the chunks.
 struct Lanes {
     uint32_t lanes, chunks;
@@ -524,11 +519,12 @@ Lanes lanes_of(uint64_t vectors) {
     return {kWave, static_cast<uint32_t>(up(vectors, kWave))};
 }
 
-// Positions of a piece: 8 to 64, so that the waves fill the chip.
+// Positions of a piece: 8 to 64, so that 4096 waves or more fill the chip (with 2048
+// 16384 tokens of 2048 bf16 take 148 us for 142, with 8192 150; 100000 of 16 f32 64 for 46).
 uint32_t piece_of(uint64_t n, uint64_t vectors) {
     const Lanes l = lanes_of(vectors);
     uint32_t piece = 8;
-    while (piece < 64 && n * l.chunks * l.lanes / kWave >= uint64_t{piece} * 2 * PW) piece *= 2;
+    while (piece < 64 && n * l.chunks * l.lanes / kWave >= uint64_t{piece} * 2 * 4096) piece *= 2;
     return piece;
 }
 
@@ -551,19 +547,19 @@ struct Temp {
 
 template <class O>
 hipError_t sort_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&keys)[2], uint32_t* const (&at)[2], Zeros& z,
-                       uint64_t ride, int* last, hipStream_t stream) {
+                       bool fill, int* last, hipStream_t stream) {
     uint32_t bits = 1;
     while ((uint64_t{a.vocab} >> bits) != 0) ++bits;
     const uint32_t passes = (bits + kMaxBits - 1) / kMaxBits;
     const uint32_t each_bits = (bits + passes - 1) / passes;
     const uint32_t items = sort_items(a.n);
     p.tiles = static_cast<uint32_t>(up(a.n, uint64_t{kSortBlock} * items));
-    // the next rows to be filled beside a launch: blocks, and their end in z
-    auto riders = [&](bool known) {
-        z.occurs = known ? p.occurs : nullptr;
+    const bool counts = p.tiles > 1;
+    uint32_t launches = passes * (counts ? 2 : 1);
+    // the next rows to be filled beside a launch: their blocks, and their end in z
+    auto beside = [&] {
         z.first = z.last;
-        uint64_t rows = ride < a.vocab - z.first ? ride : a.vocab - z.first;
-        if (!known && a.n > a.vocab / 4) rows = 0;   // too many would be written twice
+        const uint64_t rows = fill ? up(a.vocab - z.first, launches--) : 0;
         z.last += static_cast<uint32_t>(rows);
         return static_cast<uint32_t>(up(up(rows, z.each), kSortWaves));
     };
@@ -574,18 +570,18 @@ hipError_t sort_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&keys)[2
         p.at = k == 0 ? nullptr : at[(k - 1) & 1];
         p.keys_out = keys[k & 1];
         p.at_out = at[k & 1];
-        if (p.tiles > 1 || (k == 0 && p.occurs)) {
-            const uint32_t beside = riders(k > 0);
+        if (counts || (k == 0 && p.occurs)) {   // the latter clears the marks
+            const uint32_t more = beside();
             timing_before(stream, RS_KERNEL_EMBED_SORT);
             const auto kernel = items == 1 ? embed_count_kernel<O, 1> : embed_count_kernel<O, 4>;
-            kernel<<<dim3(p.tiles + beside), kSortBlock, 0, stream>>>(p, z, k == 0);
+            kernel<<<dim3(p.tiles + more), kSortBlock, 0, stream>>>(p, z, k == 0);
             const hipError_t e = done(stream);
             if (e != hipSuccess) return e;
         }
-        const uint32_t beside = riders(k > 0);
+        const uint32_t more = beside();
         timing_before(stream, RS_KERNEL_EMBED_SORT);
         const auto kernel = items == 1 ? embed_place_kernel<O, 1> : embed_place_kernel<O, 4>;
-        kernel<<<dim3(p.tiles + beside), kSortBlock, 0, stream>>>(p, z);
+        kernel<<<dim3(p.tiles + more), kSortBlock, 0, stream>>>(p, z);
         const hipError_t e = done(stream);
         if (e != hipSuccess) return e;
         *last = k & 1;
@@ -618,7 +614,7 @@ hipError_t sort_many_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&ke
 template <class T, class O, int L>
 hipError_t sum_tokens(const EmbedGradArgs& a, Sorted s, const Zeros& z, hipStream_t stream) {
     const uint64_t pieces = up(a.n, s.piece);
-    const uint32_t sums = static_cast<uint32_t>(up(pieces * s.chunks, kMoveBlock / L * 8) * 8);   // a multiple of the XCDs
+    const uint32_t sums = static_cast<uint32_t>(up(pieces * s.chunks, kMoveBlock / L));
     const uint32_t fill = static_cast<uint32_t>(up(up(z.last - z.first, z.each), kMoveWaves));
     hipError_t e = hipSuccess;
     if (sums + fill > 0) {
@@ -647,16 +643,16 @@ hipError_t embed_grad_of(const EmbedGradArgs& a, void* temp, hipStream_t stream)
     const uint64_t row_bytes = uint64_t{a.width} * sizeof(O);
     while (z.each < 64 && z.each * row_bytes < 4096) z.each *= 2;
     while (z.lanes_log2 > 0 && (kVec<O> << (z.lanes_log2 - 1)) >= a.width) --z.lanes_log2;
-    const uint64_t ride = a.accumulate ? 0 : RIDE / row_bytes;
 
     Pass p{};
     p.n = a.n;
     p.vocab = a.vocab;
     p.counts = static_cast<uint32_t*>(sort);
-    p.occurs = a.accumulate ? nullptr : occurs;
+    const bool fill = !a.accumulate && few_tokens(a.n, a.vocab);
+    p.occurs = a.accumulate || fill ? nullptr : occurs;
     if (a.n > 0) {
         int last = 1;
-        const hipError_t e = own_sort(a.n) ? sort_tokens<O>(a, p, keys, at, z, ride, &last, stream)
+        const hipError_t e = own_sort(a.n) ? sort_tokens<O>(a, p, keys, at, z, fill, &last, stream)
                                            : sort_many_tokens(a, p, keys, at, sort, stream);
         if (e != hipSuccess) return e;
         s.keys = keys[last];
@@ -664,7 +660,7 @@ hipError_t embed_grad_of(const EmbedGradArgs& a, void* temp, hipStream_t stream)
         z.occurs = p.occurs;
     }
     z.first = z.last;   // what the sort's launches did not fill
-    z.last = a.accumulate ? z.first : a.vocab;
+    z.last = a.accumulate ? z.first : a.vocab;   // nothing, where all of them were
     const Lanes l = lanes_of(up(a.width, kVec<T>));
     s.chunks = l.chunks;
     return l.lanes == 4 ? sum_tokens<T, O, 4>(a, s, z, stream) : l.lanes == 16 ? sum_tokens<T, O, 16>(a, s, z, stream)

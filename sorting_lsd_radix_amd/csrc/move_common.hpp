@@ -16,13 +16,6 @@ constexpr int kVec = 16 / sizeof(T);
 // The wave's number in its block, known to be the same for the whole wave.
 __device__ __forceinline__ uint32_t wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); }
 
-// Block b of n in the order that gives each XCD (blocks go round all 8) one run of
-// the work.
-__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n) {
-    const uint32_t x = b & 7u, each = n >> 3, more = n & 7u;
-    return x * each + (x < more ? x : more) + (b >> 3);
-}
-
 // The value of lane `from`, the same lane for the whole wave.
 __device__ __forceinline__ uint32_t lane_value(uint32_t x, uint32_t from) {
     return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), static_cast<int>(from)));

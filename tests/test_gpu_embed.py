@@ -228,3 +228,20 @@ def test_large_tables(vocab, width):
     want = torch.zeros(vocab, width, device=DEV)
     want.index_add_(0, on(ids[:-1]).long(), x[:-1].float())
     assert torch.equal(got, want.bfloat16())
+
+
+@pytest.mark.parametrize("n", [1, 100, 1000, 5000])
+@pytest.mark.parametrize("vocab", [7, 1000, 1500, 8000, 8007, 40001, 1 << 21])
+@pytest.mark.parametrize("width", [3, 40])
+def test_rows_without_tokens(n, vocab, width):
+    """Few and many tokens for a table's rows, one to three passes of the sort: every row without one is
+    zeros, every other its sum."""
+    print("rows without tokens", n, vocab, width, flush=True)
+    rng = np.random.default_rng(n + vocab)
+    ids = rng.integers(-1, vocab, n).astype(np.int32)
+    x = rng.integers(-8, 9, (n, width)).astype(np.float32)
+    out = torch.full((vocab, width), float("nan"), dtype=torch.bfloat16, device=DEV)
+    rs.embed_tokens_grad(on(x).bfloat16(), on(ids), vocab, out=out)
+    want = torch.zeros(vocab + 1, width, device=DEV)
+    want.index_add_(0, on(np.where(ids < 0, vocab, ids)).long(), on(x))
+    assert torch.equal(out, want[:vocab].bfloat16())
