@@ -351,7 +351,7 @@ __global__ __launch_bounds__(kMoveBlock) void embed_sum_kernel(EmbedGradArgs a, 
     constexpr int V = kVec<T>;
     using Cols = Columns<T, L == kWave>;
     if (block_id() >= sums) {
-        if (block_id() - sums < fill) zero_rows<O>(z, static_cast<uint64_t>((block_id() - sums, fill)) * kMoveWaves + wave_id());
+        if (block_id() - sums < fill) zero_rows<O>(z, static_cast<uint64_t>(block_id() - sums) * kMoveWaves + wave_id());
         return;
     }
     const uint32_t unit = block_id() * (kMoveBlock / L) + (L == kWave ? wave_id() : threadIdx.x / L);
