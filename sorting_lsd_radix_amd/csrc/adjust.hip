@@ -16,26 +16,18 @@ namespace rs {
 
 namespace {
 
-#ifndef AB
-#define AB 512
-#endif
-constexpr int kAdjustBlock = AB;
+constexpr int kAdjustBlock = 512;
 
-// A token's word: from the low end a bias entry's index + 1, the occurrences
-// behind the prompt, a bit for an occurrence in it.
-template <class W>
-struct Word {
-    static constexpr int kEntryBits = 0, kCountBits = 0;
-};
-template <>
-struct Word<uint32_t> {
-    static constexpr int kEntryBits = 16, kCountBits = 15;
-};
-template <>
-struct Word<unsigned long long> {
-    static constexpr int kEntryBits = 31, kCountBits = 32;
-};
-struct NoWord {};
+// What a block keeps of its tokens: nothing without lists; 16 bits for short
+// histories, 32 for long ones, with a bit for an occurrence in the prompt, one for
+// a bias, whose entry is then looked up, and the occurrences behind the prompt; 64
+// for many biases, with the prompt's bit, the occurrences (32 bits) and a bias
+// entry's index + 1 (31 bits).
+enum Marks { kNoMarks, kMarks16, kMarks32, kMarks64 };
+constexpr uint32_t kMaxHistory16 = 1u << 14;
+constexpr uint32_t kMaxLooked = kAdjustBlock;   // bias entries that are looked up
+constexpr uint32_t kSlots = 2 * kMaxLooked;     // of their table: a token is in the first free one from its low bits on
+constexpr uint32_t kFree = ~0u;
 
 // What a row's lists hold, each count within its list.
 __device__ __forceinline__ uint32_t within(const int32_t* n, uint32_t r, uint32_t otherwise, uint32_t all) {
@@ -45,7 +37,7 @@ __device__ __forceinline__ uint32_t within(const int32_t* n, uint32_t r, uint32_
 }
 
 constexpr int kTokens = 4;   // of a vector load
-constexpr int kAhead = 2;    // vectors of history in flight
+constexpr int kAhead = 1;    // vectors of history in flight while one is marked
 typedef uint32_t Tokens __attribute__((ext_vector_type(kTokens), aligned(4)));
 
 // Tokens i .. i + 4 of `length`; what is behind them is no token.
@@ -58,13 +50,14 @@ __device__ __forceinline__ Tokens load_tokens(const uint32_t* from, uint32_t i, 
     return v;
 }
 
-// HOLD vectors a thread.  W: a token's word, or NoWord without lists.
-template <class T, class O, class W, int HOLD>
+// HOLD vectors a thread.
+template <class T, class O, Marks MARKS, int HOLD>
 __global__ __launch_bounds__(kAdjustBlock) void adjust_kernel(AdjustArgs a, uint32_t slices) {
     constexpr int V = kVec<T>;
-    constexpr bool LISTS = !std::is_same<W, NoWord>::value;
     constexpr uint32_t kSlice = kAdjustBlock * HOLD * V;
+    constexpr bool kLooked = MARKS == kMarks16 || MARKS == kMarks32;
     using Vec = AnyVec<16>::V;
+    typedef unsigned long long Word;
     const uint32_t b = block_id(), tid = threadIdx.x;
     const uint32_t r = b / slices;
     if (r >= a.rows) return;
@@ -89,11 +82,26 @@ __global__ __launch_bounds__(kAdjustBlock) void adjust_kernel(AdjustArgs a, uint
         }
     }
 
-    float by = 1.0f, frequency = 0.0f, presence = 0.0f;
-    __shared__ typename std::conditional<LISTS, W, char>::type s_word[LISTS ? kSlice : 1];
-    if constexpr (LISTS) {
-        constexpr W kOne = W{1} << Word<W>::kEntryBits;
-        constexpr W kPrompt = kOne << Word<W>::kCountBits;
+    constexpr uint32_t kBits = MARKS == kMarks16 ? 16 : MARKS == kMarks32 ? 32 : 64;
+    constexpr uint32_t kVectors = MARKS == kNoMarks ? 1 : kSlice * kBits / 128;
+    __shared__ u32x4 s_marks[kVectors];
+    uint32_t* s_mark = reinterpret_cast<uint32_t*>(s_marks);   // 16 bits: of two tokens
+    Word* s_word = reinterpret_cast<Word*>(s_marks);           // 64 bits
+    constexpr Word kOne = Word{1} << 31, kPrompt64 = Word{1} << 63;
+    constexpr uint32_t kPrompt = 1u << (kBits % 64 - 1) % 32, kBiased = kPrompt >> 1;
+    __shared__ uint32_t s_token[kLooked ? kSlots : 1], s_entry[kLooked ? kSlots : 1];
+    __shared__ float s_bias[kLooked ? kSlots : 1];
+    // a division is a product with the inverse, two roundings for one, unless that may
+    // be inexact, infinite or 0 (`divide`)
+    float by = 1.0f, inverse = 1.0f, frequency = 0.0f, presence = 0.0f;
+    bool divide = false;
+    // a logit of a token that the history holds `count` times behind the prompt
+    auto penalised = [&](float l, bool seen, uint32_t count) {
+        const float scaled = l * (l > 0.0f ? inverse : by);
+        if (seen) l = divide && l > 0.0f ? l / by : scaled;
+        return l - (count > 0 ? fmaf(frequency, static_cast<float>(count), presence) : 0.0f);
+    };
+    if constexpr (MARKS != kNoMarks) {
         const uint32_t length = a.history ? within(a.lengths, r, a.history_len, a.history_len) : 0u;
         const uint32_t prompt = within(a.prompt_lengths, r, 0u, length);
         const uint32_t* history = a.history + r * a.history_stride;
@@ -104,23 +112,50 @@ __global__ __launch_bounds__(kAdjustBlock) void adjust_kernel(AdjustArgs a, uint
             for (int k = 0; k < kAhead; ++k) next[k] = load_tokens(history, i0 + (k * kAdjustBlock + tid) * kTokens, length);
         };
         load(0);
+        uint32_t token = ~0u;   // of this thread's bias entry
+        float bias = 0.0f;
+        if (kLooked && tid < a.bias_len) {
+            token = a.bias_ids[r * a.bias_ids_stride + tid] - lo;
+            bias = a.bias[r * a.bias_stride + tid];
+        }
         if (length > 0) {
             if (a.repetition) by = a.repetition[r];
             if (a.frequency) frequency = a.frequency[r];
             if (a.presence) presence = a.presence[r];
+            inverse = 1.0f / by;
+            divide = !(fabsf(by) >= 0x1p-100f && fabsf(by) <= 0x1p100f);
         }
-#pragma unroll
-        for (uint32_t i = 0; i < kSlice / kAdjustBlock; i += 16 / sizeof(W)) {
-            typedef W Zero __attribute__((ext_vector_type(16 / sizeof(W))));
-            *reinterpret_cast<Zero*>(&s_word[i * kAdjustBlock + tid * (16 / sizeof(W))]) = Zero{};
+        for (uint32_t i = tid; i < kVectors; i += kAdjustBlock) s_marks[i] = u32x4{0, 0, 0, 0};
+        if constexpr (kLooked) {
+            if (a.bias_len > 0) {
+                for (uint32_t i = tid; i < kSlots; i += kAdjustBlock) {
+                    s_token[i] = kFree;
+                    s_entry[i] = 0;
+                }
+            }
         }
         __syncthreads();
-        if (a.bias_ids) {
+        if constexpr (kLooked) {
+            if (a.bias_len > 0) {
+                uint32_t slot = token % kSlots;
+                if (token < size) {
+                    for (;; slot = (slot + 1) % kSlots) {   // there are more slots than entries
+                        const uint32_t held = atomicCAS(&s_token[slot], kFree, token);
+                        if (held == kFree || held == token) break;
+                    }
+                    atomicMax(&s_entry[slot], tid);   // the last entry counts
+                    if constexpr (MARKS == kMarks16) atomicOr(&s_mark[token / 2], kBiased << token % 2 * 16);
+                    else atomicOr(&s_mark[token], kBiased);
+                }
+                __syncthreads();
+                if (token < size && s_entry[slot] == tid) s_bias[slot] = bias;
+            }
+        } else if (a.bias_ids) {
             for (uint32_t i = tid; i < a.bias_len; i += kAdjustBlock) {
                 const uint32_t v = a.bias_ids[r * a.bias_ids_stride + i] - lo;
-                if (v < size) atomicMax(&s_word[v], static_cast<W>(i + 1));
+                if (v < size) atomicMax(&s_word[v], static_cast<Word>(i + 1));
             }
-            __syncthreads();
+            __syncthreads();   // nothing is above the entries yet
         }
         for (uint32_t i0 = 0; i0 < length; i0 += kRound) {
             Tokens now[kAhead];
@@ -134,38 +169,58 @@ __global__ __launch_bounds__(kAdjustBlock) void adjust_kernel(AdjustArgs a, uint
                 for (int j = 0; j < kTokens; ++j) {
                     const uint32_t v = now[k][j] - lo;   // a token that is none lies behind every slice
                     if (v >= size) continue;
-                    if (i + j < prompt) atomicOr(&s_word[v], kPrompt);
-                    else atomicAdd(&s_word[v], kOne);
+                    const bool before = i + j < prompt;
+                    if constexpr (MARKS == kMarks64) {
+                        if (before) atomicOr(&s_word[v], kPrompt64);
+                        else atomicAdd(&s_word[v], kOne);
+                    } else {
+                        uint32_t* mark = &s_mark[MARKS == kMarks16 ? v / 2 : v];
+                        const uint32_t shift = MARKS == kMarks16 ? v % 2 * 16 : 0;
+                        if (before) atomicOr(mark, kPrompt << shift);
+                        else atomicAdd(mark, 1u << shift);
+                    }
                 }
             }
         }
         __syncthreads();
     }
 
+    // the bias of a token that has one
+    auto bias_of = [&](uint32_t v) {
+        uint32_t slot = v % kSlots;
+        while (s_token[slot] != v) slot = (slot + 1) % kSlots;
+        return s_bias[slot];
+    };
 #pragma unroll
     for (int h = 0; h < HOLD; ++h) {
         const uint32_t i = (h * kAdjustBlock + tid) * V;
         if (i >= size) break;
         float l[V];
         widen<T>(x[h], l);
-        if constexpr (LISTS) {
-            constexpr W kOne = W{1} << Word<W>::kEntryBits;
-            constexpr W kPrompt = kOne << Word<W>::kCountBits;
-            W w[V], any = 0;
+        if constexpr (kLooked) {
+            uint32_t m[V * kBits / 32], any = 0;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                w[j] = s_word[i + j];
-                any |= w[j];
+            for (uint32_t j = 0; j < V * kBits / 32; ++j) {
+                m[j] = s_mark[i * kBits / 32 + j];
+                any |= m[j];
             }
             if (any != 0) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const uint32_t count = static_cast<uint32_t>((w[j] & (kPrompt - 1)) >> Word<W>::kEntryBits);
-                    const uint32_t entry = static_cast<uint32_t>(w[j] & (kOne - 1));
-                    if (w[j] >= kOne) l[j] = l[j] > 0.0f ? l[j] / by : l[j] * by;
-                    if (count > 0) l[j] -= fmaf(frequency, static_cast<float>(count), presence);
-                    if (entry > 0) l[j] += a.bias[r * a.bias_stride + entry - 1];
+                    const uint32_t w = MARKS == kMarks16 ? m[j / 2] >> (j % 2 * 16) & 0xFFFFu : m[j];
+                    l[j] = penalised(l[j], (w & ~kBiased) != 0, w & (kBiased - 1));
+                    if (w & kBiased) l[j] += bias_of(i + j);
                 }
+            }
+        }
+        if constexpr (MARKS == kMarks64) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const Word w = s_word[i + j];
+                if (w == 0) continue;
+                const uint32_t entry = static_cast<uint32_t>(w & (kOne - 1));
+                l[j] = penalised(l[j], w >= kOne, static_cast<uint32_t>((w & (kPrompt64 - 1)) >> 31));
+                if (entry > 0) l[j] += a.bias[r * a.bias_stride + entry - 1];
             }
         }
 #pragma unroll
@@ -174,36 +229,26 @@ __global__ __launch_bounds__(kAdjustBlock) void adjust_kernel(AdjustArgs a, uint
     }
 }
 
-template <class T, class O, class W, int HOLD>
+template <class T, class O, Marks MARKS, int HOLD>
 void launch_as(const AdjustArgs& a, hipStream_t stream) {
     constexpr uint32_t kSlice = kAdjustBlock * HOLD * kVec<T>;
     const uint32_t slices = (a.vocab + kSlice - 1) / kSlice;
-    adjust_kernel<T, O, W, HOLD><<<many_blocks(static_cast<uint64_t>(a.rows) * slices), kAdjustBlock, 0, stream>>>(a, slices);
+    adjust_kernel<T, O, MARKS, HOLD><<<many_blocks(static_cast<uint64_t>(a.rows) * slices), kAdjustBlock, 0, stream>>>(a, slices);
 }
 
-#ifndef HT
-#define HT 1024
-#endif
 template <class T, class O>
 hipError_t adjust_of(const AdjustArgs& a, hipStream_t stream) {
-    // the fields of a wide word only where the lists can be longer than a narrow one's
-    const bool wide = a.history_len >= (1u << Word<uint32_t>::kCountBits) || a.bias_len >= (1u << Word<uint32_t>::kEntryBits);
-    const bool lists = a.history || a.bias_ids;
-    // vectors a thread: as many as leave the chip enough blocks
+    const Marks marks = !a.history && !a.bias_ids ? kNoMarks : a.bias_len > kMaxLooked ? kMarks64
+                        : a.history_len >= kMaxHistory16 ? kMarks32 : kMarks16;
+    // two vectors a thread, where that leaves the chip 1024 blocks (four and eight leave a CU too few)
     const uint64_t vectors = static_cast<uint64_t>(a.rows) * ((a.vocab + kVec<T> - 1) / kVec<T>);
-    const int hold = vectors >= uint64_t{4} * HT * kAdjustBlock ? 4 : vectors >= uint64_t{2} * HT * kAdjustBlock ? 2 : 1;
+    const bool two = vectors >= uint64_t{2048} * kAdjustBlock;
     timing_before(stream, RS_KERNEL_ADJUST);
-    if (!lists) {
-        if (hold == 1) launch_as<T, O, NoWord, 1>(a, stream);
-        else if (hold == 2) launch_as<T, O, NoWord, 2>(a, stream);
-        else launch_as<T, O, NoWord, 4>(a, stream);
-    } else if (wide) {
-        if (hold == 1) launch_as<T, O, unsigned long long, 1>(a, stream);
-        else launch_as<T, O, unsigned long long, 2>(a, stream);
-    } else {
-        if (hold == 1) launch_as<T, O, uint32_t, 1>(a, stream);
-        else if (hold == 2) launch_as<T, O, uint32_t, 2>(a, stream);
-        else launch_as<T, O, uint32_t, 4>(a, stream);
+    switch (marks) {
+        case kNoMarks: two ? launch_as<T, O, kNoMarks, 2>(a, stream) : launch_as<T, O, kNoMarks, 1>(a, stream); break;
+        case kMarks16: two ? launch_as<T, O, kMarks16, 2>(a, stream) : launch_as<T, O, kMarks16, 1>(a, stream); break;
+        case kMarks32: two ? launch_as<T, O, kMarks32, 2>(a, stream) : launch_as<T, O, kMarks32, 1>(a, stream); break;
+        default: two ? launch_as<T, O, kMarks64, 2>(a, stream) : launch_as<T, O, kMarks64, 1>(a, stream); break;
     }
     const hipError_t e = hipGetLastError();
     timing_after(stream);

@@ -109,7 +109,22 @@ def test_extreme_values():
         close(call(x, r), *ref.adjust(values(x), **r), "extremes", dtype)
 
 
-@pytest.mark.parametrize("count", [32766, 32767, 32768, 65536, 70001])
+def test_extreme_penalties():
+    """Repetition penalties whose inverse is none, or no exact one, and infinite others."""
+    print("extreme penalties", flush=True)
+    by = np.array([1e-39, 2e-45, 1e-30, 2.0 ** -100, 2.0 ** -101, 1e30, 2.0 ** 100, 2.0 ** 127, 3e38, np.inf, 0.0, -2.0,
+                   np.nan, 1.0], np.float32)
+    rows, vocab = len(by), 400
+    x = np.tile(np.array([1e-37, 3e-39, 1.5, 3e38, -1.5, -3e-39, -3e38, 0.0, -0.0, np.inf, -np.inf, np.nan], np.float32), (rows, 40))
+    x = matrix(x[:, :vocab], "f32")
+    h = np.tile(np.arange(0, vocab, 2, dtype=np.int32), (rows, 1))
+    r = {"history": h, "prompts": np.full(rows, 1000, np.int32), "repetition": by}
+    close(call(x, r), *ref.adjust(values(x), **r), "penalties")
+    r = {"history": h, "presence": by, "frequency": by[::-1].copy()}
+    close(call(x, r), *ref.adjust(values(x), **r), "penalties behind the prompt")
+
+
+@pytest.mark.parametrize("count", [16383, 16384, 16385, 32766, 32767, 32768, 65536, 70001])
 def test_counts_of_one_token(count):
     """One token fills a history, behind and in the prompt: every occurrence counts."""
     print("one token", count, flush=True)
@@ -124,7 +139,7 @@ def test_counts_of_one_token(count):
     assert (got == 1).all()
 
 
-@pytest.mark.parametrize("entries", [1, 2, 65534, 65535, 65536, 70000])
+@pytest.mark.parametrize("entries", [1, 2, 511, 512, 513, 65534, 65535, 65536, 70000])
 def test_last_entry_of_a_token(entries):
     print("entries", entries, flush=True)
     ids = np.full((1, entries), 8500, np.int32)
@@ -133,6 +148,22 @@ def test_last_entry_of_a_token(entries):
     got = rs.adjust_logits(x, bias_ids=on(ids), bias=on(b))
     assert got[0, 8500] == entries - 1
     assert (got != 0).sum() == (entries > 1)
+
+
+@pytest.mark.parametrize("history", [0, 700, 20000])
+def test_biases_whose_tokens_share_low_bits(history):
+    """Entries of one token and of tokens a power of two apart, in any order."""
+    print("biases that collide", history, flush=True)
+    rng = np.random.default_rng(history)
+    rows, vocab, n = 3, 9000, 512
+    ids = (rng.integers(0, 4, (rows, n)) * 1024 + rng.integers(0, 40, (rows, n)) + rng.integers(0, 2, (rows, n)) * 4096).astype(np.int32)
+    ids[rng.random((rows, n)) < 0.1] = -1
+    r = rules(rng, rows, vocab, history)
+    if history:
+        r["history"][:, :100] = ids[:, :100]   # tokens with both
+    r.update(bias_ids=ids, bias=rng.standard_normal((rows, n)).astype(np.float32))
+    x = matrix(rng.standard_normal((rows, vocab)), "f32")
+    close(call(x, r), *ref.adjust(values(x), **r), "colliding biases")
 
 
 def test_strides_of_lists():
