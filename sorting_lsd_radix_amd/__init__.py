@@ -1219,14 +1219,16 @@ def embed_tokens_grad(dout, ids, vocab, scale=1.0, dtype=None, accumulate=False,
 
 
 def _lists(t, name, rows, cols, dtypes, index):
-    """(address, row stride) of a row's list of each row, whose elements are next to each other."""
-    if t.dtype not in dtypes or len(t.shape) != 2 or t.shape[0] != rows or \
-            (cols is not None and t.shape[1] != cols) or t.get_device() != index or \
-            (t.stride(1) != 1 and t.shape[1] > 1):
-        raise TypeError("%s must be a 2-D tensor of %d rows%s of %s on cuda:%d whose rows are contiguous"
-                        % (name, rows, "" if cols is None else " and %d columns" % cols,
-                           " or ".join(str(d) for d in dtypes), index))
-    return t.data_ptr(), t.stride(0)
+    """(address, row stride, columns) of a list of each row, its elements next to each other."""
+    shape = t.shape
+    if len(shape) == 2 and shape[0] == rows and (cols is None or shape[1] == cols) and \
+            t.dtype in dtypes and t.is_cuda and t.get_device() == index:
+        stride, step = t.stride()
+        if step == 1 or shape[1] <= 1:
+            return t.data_ptr(), stride, shape[1]
+    raise TypeError("%s must be a 2-D tensor of %d rows%s of %s on cuda:%d whose rows are contiguous"
+                    % (name, rows, "" if cols is None else " and %d columns" % cols,
+                       " or ".join(str(d) for d in dtypes), index))
 
 
 def adjust_logits(logits, history=None, lengths=None, prompt_lengths=None, repetition=None,
@@ -1253,16 +1255,14 @@ def adjust_logits(logits, history=None, lengths=None, prompt_lengths=None, repet
     at_history = at_ids = at_bias = at_mask = None
     hstride = hlen = istride = bstride = blen = mstride = 0
     if history is not None:
-        at_history, hstride = _lists(history, "history", rows, None, _INTS, index)
-        hlen = history.shape[1]
+        at_history, hstride, hlen = _lists(history, "history", rows, None, _INTS, index)
     if (bias_ids is None) != (bias is None):
         raise TypeError("bias_ids and bias must both be given")
     if bias is not None:
-        at_ids, istride = _lists(bias_ids, "bias_ids", rows, None, _INTS, index)
-        blen = bias_ids.shape[1]
-        at_bias, bstride = _lists(bias, "bias", rows, blen, f32, index)
+        at_ids, istride, blen = _lists(bias_ids, "bias_ids", rows, None, _INTS, index)
+        at_bias, bstride, _ = _lists(bias, "bias", rows, blen, f32, index)
     if mask is not None:
-        at_mask, mstride = _lists(mask, "mask", rows, (vocab + 31) // 32, _INTS, index)
+        at_mask, mstride, _ = _lists(mask, "mask", rows, (vocab + 31) // 32, _INTS, index)
     at_rows = [None if t is None else _check_like(t, name, (rows,), of, index)
                for t, name, of in ((lengths, "lengths", (torch.int32,)),
                                    (prompt_lengths, "prompt_lengths", (torch.int32,)),

@@ -199,3 +199,14 @@ def test_mask_words():
     allowed[0, [0, 33]] = True
     words = ref.mask_words(allowed)
     assert words.shape == (1, 2) and words[0, 0] == 1 and words[0, 1] & 0xFF == 2
+
+
+def test_wrappers_refuse_host_memory():
+    torch = pytest.importorskip("torch")
+    x, i = torch.zeros(4, 8), torch.zeros(4, dtype=torch.int32)
+    p, w = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    for call in (lambda: rs.gather_choices(x, i, p), lambda: rs.gather_choices_grad(x, x, p, w),
+                 lambda: rs.combine_choices(x, p), lambda: rs.combine_choices_grad(x, x, i, p, w),
+                 lambda: rs.embed_tokens(x, i), lambda: rs.embed_tokens_grad(x, i, 9), lambda: rs.adjust_logits(x)):
+        with pytest.raises(TypeError):
+            call()
