@@ -102,16 +102,16 @@ __global__ __launch_bounds__(kAdjustBlock) void adjust_kernel(AdjustArgs a, uint
         return l - (count > 0 ? fmaf(frequency, static_cast<float>(count), presence) : 0.0f);
     };
     if constexpr (MARKS != kNoMarks) {
-        const uint32_t length = a.history ? within(a.lengths, r, a.history_len, a.history_len) : 0u;
-        const uint32_t prompt = within(a.prompt_lengths, r, 0u, length);
         const uint32_t* history = a.history + r * a.history_stride;
         constexpr uint32_t kRound = kAdjustBlock * kTokens * kAhead;
         Tokens next[kAhead];
         auto load = [&](uint32_t i0) {
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) next[k] = load_tokens(history, i0 + (k * kAdjustBlock + tid) * kTokens, length);
+            for (int k = 0; k < kAhead; ++k) next[k] = load_tokens(history, i0 + (k * kAdjustBlock + tid) * kTokens, a.history_len);
         };
-        load(0);
+        load(0);   // before the length is known
+        const uint32_t length = a.history ? within(a.lengths, r, a.history_len, a.history_len) : 0u;
+        const uint32_t prompt = within(a.prompt_lengths, r, 0u, length);
         uint32_t token = ~0u;   // of this thread's bias entry
         float bias = 0.0f;
         if (kLooked && tid < a.bias_len) {
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(kAdjustBlock) void adjust_kernel(AdjustArgs a, uint
 #pragma unroll
                 for (int j = 0; j < kTokens; ++j) {
                     const uint32_t v = now[k][j] - lo;   // a token that is none lies behind every slice
-                    if (v >= size) continue;
+                    if (v >= size || i + j >= length) continue;
                     const bool before = i + j < prompt;
                     if constexpr (MARKS == kMarks64) {
                         if (before) atomicOr(&s_word[v], kPrompt64);
