@@ -575,7 +575,9 @@ rs_status rs_embed_tokens(rs_elem_type elem_type, const void *table, uint64_t ta
  * for all); dtable [vocab, width] of table_type, which is elem_type or
  * RS_ELEM_F32.  Without accumulate every element of dtable is written; with
  * it the rows that have no token are left as they are.
- * Temp with the query idiom; the size depends on elem_type, n, vocab and width.
+ * Temp with the query idiom; the size depends on elem_type, n, vocab and
+ * width.  Above 2^19 tokens the passes of rs_sort_pairs_u32 sort them, and
+ * their scheduling assumption holds.
  */
 rs_status rs_embed_tokens_grad(rs_elem_type elem_type, const void *dout, uint64_t dout_stride,
                                const uint32_t *ids, uint64_t n, uint32_t vocab, uint32_t width,

@@ -1,5 +1,21 @@
 // choices.hip -- a router's rows brought into the order of their experts, and
-// summed back by their weights, with the gradients of both.
+// summed back by their weights, with the gradients of both:
+//   y_i = w_c x_t (c = order_i, t = c / top_k), 0 without a choice;
+//   out_t = sum over j of w_tj y_(place_tj); products x_t y_(place_tj).
+//
+// The row of a token is read once: a wave takes a part of it and writes it to all
+// its choices' positions, or sums its choices' rows, eight in flight.  (A wave for
+// each position instead reads a row top_k times, from the caches: 333 us against 282
+// for 131072 choices of 4096 bf16.)  A choice's wave writes a position if order and
+// place name each other there, waves behind look for the other positions; so each is
+// written once, as order has it, whatever place holds.  Sums and products are f32
+// in the order of j, products by lanes and then waves: nothing depends on the order
+// in which blocks run.
+//
+// What bounds it is memory: 16384 rows with 8 choices in 163584 positions of 4096
+// bf16 take 280 us to gather (5.3 TB/s; writes scattered over 256 segments reach 5.6
+// without anything else), 203 to combine (5.8 TB/s); 8192 with 6 of 2048 f16 46 to combine
+// and 100 for the gradients (4.8 TB/s).
 #include "internal.hpp"
 #include "move_common.hpp"
 

@@ -13,9 +13,10 @@
 // tokens that occur, and the other rows are filled beside the sums (looking a row's
 // mark up costs a tenth of the filling's rate).
 //
-// What bounds it: 131072 rows of 2048 bf16 and 16384 tokens take 128 us, of which
-// the filling is some 95 (512 MB, 5.4 TB/s), the sums 20, the join 6; 32003 rows of
-// 1001 f32 and 50021 tokens 87: the sort 22, the sums and zeros 55 (5.0 TB/s), the join 8.
+// What bounds it: 131072 rows of 2048 bf16 and 16384 tokens take 131 us, of which
+// the sort's four launches with the filling are 101 (512 MB, 5.2 TB/s), the sums 23,
+// the join 7; 32003 rows of 1001 f32 and 50021 tokens 85: the sort 21, the sums and
+// zeros 60 (4.8 TB/s), the join 9.  Rows by token: 32768 of 5120 f16 94 us (4.8 TB/s).
 #include "internal.hpp"
 #include "move_common.hpp"
 
