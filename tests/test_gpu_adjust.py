@@ -78,6 +78,20 @@ def test_adjust(shape, dtype, to):
         assert torch.equal(x, got)
 
 
+@pytest.mark.parametrize("dtype,rows", [("f32", 40), ("bf16", 70)])
+@pytest.mark.parametrize("history,biases", [(0, 0), (600, 20), (17000, 20), (600, 600)])
+def test_many_rows(history, biases, dtype, rows):
+    """So many logits that a thread takes two vectors, with every kind of lists."""
+    print("many rows", history, biases, dtype, flush=True)
+    rng = np.random.default_rng(rows + history + biases)
+    vocab = 131072
+    x = matrix(rng.standard_normal((rows, vocab)), dtype)
+    r = rules(rng, rows, vocab, history, biases, 0.5)
+    got = call(x, r)
+    close(got, *ref.adjust(values(x), **r), "logits", dtype)
+    assert torch.equal(call(x, r, out=x), got)
+
+
 @pytest.mark.parametrize("only", ["history", "lengths", "prompts", "repetition", "presence", "frequency"])
 def test_each_rule_alone(only):
     """Whatever of the lists and penalties is given, the others have their neutral value."""

@@ -133,6 +133,27 @@ def test_gradients(shape, dtype):
     untouched()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("width", [1003, 530])
+def test_many_rows(width, dtype):
+    """So many that a wave takes several vectors of a row, with ends off their borders."""
+    print("many rows", width, dtype, flush=True)
+    rng = np.random.default_rng(width)
+    rows, k = 4200, 2
+    order, place = grouped(choices(rng, rows, k, 16), 16, 8)
+    o, p = order.cpu().numpy(), place.cpu().numpy()
+    x = matrix(rng.standard_normal((rows, width)), dtype, 1)
+    y = matrix(rng.standard_normal((len(o), width)), dtype)
+    w = weights_of(rng, rows, k)
+    for weights in (None, w):
+        given = None if weights is None else on(weights)
+        close(rs.gather_choices(x, order, place, weights=given), *ref.gather(values(x), o, k, weights), "y", dtype)
+        close(rs.combine_choices(y, place, weights=given), *ref.combine(values(y), p, weights), "out", dtype)
+    dy, dw = rs.combine_choices_grad(x, y, order, place, on(w))
+    close(dy, *ref.gather(values(x), o, k, w), "dy", dtype)
+    close(dw, *ref.dots(values(x), values(y), p), "dw")
+
+
 @pytest.mark.parametrize("width", [5, 300, 2100])
 @pytest.mark.parametrize("k", [1, 3, 8, 20])
 def test_any_order_and_place(width, k):

@@ -49,6 +49,17 @@ def test_embed(shape, scale, dtype):
     assert torch.equal(out, got) and (whole[:, width:] == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("scale", [1.0, 0.3])
+def test_embed_many(scale, dtype):
+    """So many rows that a wave takes several vectors of one, with an end off their borders."""
+    print("embed many", scale, dtype, flush=True)
+    rng = np.random.default_rng(7)
+    table = matrix(rng.standard_normal((200, 1003)), dtype, 2, 1)
+    ids = tokens(rng, 5000, 200)
+    close(rs.embed_tokens(table, on(ids), scale=scale), *ref.embed(values(table), ids, float(np.float32(scale))), "rows", dtype)
+
+
 @pytest.mark.parametrize("dtype,to", [("f32", "f32"), ("f16", "f16"), ("bf16", "bf16"), ("f16", "f32"), ("bf16", "f32")])
 @pytest.mark.parametrize("scale", [1.0, -3.7])
 @pytest.mark.parametrize("shape", SHAPES)
