@@ -143,10 +143,18 @@ struct Pass {
     const uint32_t* at;     // their positions, null in the first pass
     uint32_t* keys_out;
     uint32_t* at_out;
-    uint32_t* counts;       // [tiles][bins]
-    uint8_t* occurs;        // [vocab], or null
+    uint32_t* counts;       // [tiles][bins], or null: each tile counts the keys itself
+    uint8_t* occurs;        // [vocab]: a byte for each token that occurs
     uint32_t n, vocab, tiles, shift, bits;
+    bool clear, mark;       // whether this launch clears those bytes, and sets them
 };
+
+// Clears the bytes of the tokens, beside the tiles' other work.
+__device__ __forceinline__ void clear_occurs(const Pass& p) {
+    const uint32_t words = static_cast<uint32_t>((static_cast<uint64_t>(p.vocab) + 3) / 4);
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kSortBlock + threadIdx.x; i < words; i += static_cast<uint64_t>(gridDim.x) * kSortBlock)
+        reinterpret_cast<uint32_t*>(p.occurs)[i] = 0;
+}
 
 // A key: the token, `vocab` for one outside the table.
 __device__ __forceinline__ uint32_t key_of(const Pass& p, uint64_t i) {
@@ -155,14 +163,10 @@ __device__ __forceinline__ uint32_t key_of(const Pass& p, uint64_t i) {
 }
 
 template <class O, int ITEMS>
-__global__ __launch_bounds__(kSortBlock) void embed_count_kernel(Pass p, Zeros z, bool first) {
+__global__ __launch_bounds__(kSortBlock) void embed_count_kernel(Pass p, Zeros z) {
     __shared__ uint32_t s_count[1u << kMaxBits];
     const uint32_t tid = threadIdx.x;
-    if (first && p.occurs) {
-        const uint32_t words = static_cast<uint32_t>((static_cast<uint64_t>(p.vocab) + 3) / 4);
-        for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kSortBlock + tid; i < words; i += static_cast<uint64_t>(gridDim.x) * kSortBlock)
-            reinterpret_cast<uint32_t*>(p.occurs)[i] = 0;
-    }
+    if (p.clear) clear_occurs(p);
     if (blockIdx.x >= p.tiles) return zero_rows<O>(z, static_cast<uint64_t>(blockIdx.x - p.tiles) * kSortWaves + wave_id());
     const uint32_t base = blockIdx.x * (kSortBlock * ITEMS);
     s_count[tid] = 0;
@@ -189,6 +193,7 @@ __global__ __launch_bounds__(kSortBlock) void embed_place_kernel(Pass p, Zeros z
     const uint32_t tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
     const uint32_t tile = blockIdx.x;
     if (tile >= p.tiles) return zero_rows<O>(z, static_cast<uint64_t>(tile - p.tiles) * kSortWaves + wave_id());
+    if (p.clear) clear_occurs(p);
     const uint32_t bins = 1u << p.bits;
     const uint32_t base = tile * (kSortBlock * ITEMS) + wave * (kWave * ITEMS) + lane;
     uint32_t key[ITEMS], at[ITEMS], rank[ITEMS];
@@ -199,8 +204,33 @@ __global__ __launch_bounds__(kSortBlock) void embed_place_kernel(Pass p, Zeros z
         at[j] = i < p.n && p.at ? p.at[i] : i;
     }
     for (uint32_t x = lane; x < bins; x += kWave) s_count[wave][x] = 0;
-    // counts of the tiles: thread (slice q, bin) sums every slices-th tile
-    if (p.tiles > 1) {
+    if (p.tiles > 1 && p.counts == nullptr) {
+        // all keys, and those of earlier tiles; the digit of a wave's first lane, which may be
+        // every lane's, is counted once for all of them
+        s_part[0][tid] = s_part[1][tid] = 0;
+        __syncthreads();
+        const uint32_t here = tile * (kSortBlock * ITEMS);
+        for (uint32_t i0 = 0; i0 < p.n; i0 += kSortBlock * 4) {
+            uint32_t d[4];
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                const uint32_t i = i0 + j * kSortBlock + tid;
+                d[j] = i < p.n ? (key_of(p, i) >> p.shift) & (bins - 1) : ~0u;
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                const bool earlier = i0 + j * kSortBlock + tid < here;   // of a whole wave or none
+                const bool with_first = d[j] == __builtin_amdgcn_readfirstlane(d[j]);
+                const uint64_t same = ballot(with_first);
+                const uint32_t n = with_first ? __builtin_popcountll(same) : 1;
+                if (d[j] != ~0u && (!with_first || lane == 0)) {
+                    atomicAdd(&s_part[1][d[j]], n);
+                    if (earlier) atomicAdd(&s_part[0][d[j]], n);
+                }
+            }
+        }
+    } else if (p.tiles > 1) {
+        // counts of the tiles: thread (slice q, bin) sums every slices-th tile
         const uint32_t slices = kSortBlock >> p.bits;
         const uint32_t bin = tid & (bins - 1), q = tid >> p.bits;
         constexpr uint32_t kAhead = 8;   // loads in flight: of the last tile again behind the end
@@ -250,7 +280,7 @@ __global__ __launch_bounds__(kSortBlock) void embed_place_kernel(Pass p, Zeros z
         }
         if (p.tiles > 1) {
             total = 0;
-            for (uint32_t x = tid; x < kSortBlock; x += bins) {
+            for (uint32_t x = tid; x < (p.counts ? kSortBlock : bins); x += bins) {
                 before += s_part[0][x];
                 total += s_part[1][x];
             }
@@ -270,7 +300,7 @@ __global__ __launch_bounds__(kSortBlock) void embed_place_kernel(Pass p, Zeros z
         const uint32_t to = s_base[d] + s_count[wave][d] + rank[j];
         p.keys_out[to] = key[j];
         p.at_out[to] = at[j];
-        if (p.occurs && p.at == nullptr && key[j] < p.vocab) p.occurs[key[j]] = 1;   // from all that do, the same byte
+        if (p.mark && key[j] < p.vocab) p.occurs[key[j]] = 1;   // from all that do, the same byte
     }
 }
 
@@ -278,7 +308,7 @@ __global__ __launch_bounds__(kSortBlock) void embed_place_kernel(Pass p, Zeros z
 // kMaxTiles tiles of 4096 tokens.
 __global__ __launch_bounds__(kSortBlock) void embed_keys_kernel(Pass p) {
     const uint64_t i = static_cast<uint64_t>(block_id()) * kSortBlock + threadIdx.x;
-    if (p.occurs) {
+    if (p.clear) {
         const uint64_t step = static_cast<uint64_t>(gridDim.x) * gridDim.y * kSortBlock;
         const uint64_t words = (static_cast<uint64_t>(p.vocab) + 3) / 4;
         for (uint64_t w = i; w < words; w += step) reinterpret_cast<uint32_t*>(p.occurs)[w] = 0;
@@ -555,7 +585,12 @@ hipError_t sort_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&keys)[2
     const uint32_t each_bits = (bits + passes - 1) / passes;
     const uint32_t items = sort_items(a.n);
     p.tiles = static_cast<uint32_t>(up(a.n, uint64_t{kSortBlock} * items));
-    const bool counts = p.tiles > 1;
+    const bool marks = p.clear;
+    // With a launch for the tiles' counts, or, of few tiles, each counts all keys itself: 3 tiles 25.7 us
+    // for 28.2 in all, 10 tiles 34.5 for 32.4; beside the filling, which hides it, 16 tiles 125.7 for
+    // 127.5.  Where one pass has to clear the marks before several tiles set them, the launch is needed.
+    const bool counts = p.tiles > (fill ? 16u : 4u) || (p.tiles > 1 && passes == 1 && marks);
+    uint32_t* const tile_counts = p.counts;
     uint32_t launches = passes * (counts ? 2 : 1);
     // the next rows to be filled beside a launch: their blocks, and their end in z
     auto beside = [&] {
@@ -571,14 +606,19 @@ hipError_t sort_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&keys)[2
         p.at = k == 0 ? nullptr : at[(k - 1) & 1];
         p.keys_out = keys[k & 1];
         p.at_out = at[k & 1];
-        if (counts || (k == 0 && p.occurs)) {   // the latter clears the marks
+        p.counts = counts ? tile_counts : nullptr;
+        p.clear = marks && k == 0;
+        p.mark = false;
+        if (counts) {
             const uint32_t more = beside();
             timing_before(stream, RS_KERNEL_EMBED_SORT);
             const auto kernel = items == 1 ? embed_count_kernel<O, 1> : embed_count_kernel<O, 4>;
-            kernel<<<dim3(p.tiles + more), kSortBlock, 0, stream>>>(p, z, k == 0);
+            kernel<<<dim3(p.tiles + more), kSortBlock, 0, stream>>>(p, z);
             const hipError_t e = done(stream);
             if (e != hipSuccess) return e;
         }
+        if (counts) p.clear = false;
+        p.mark = marks && k == (counts ? 0 : passes - 1);
         const uint32_t more = beside();
         timing_before(stream, RS_KERNEL_EMBED_SORT);
         const auto kernel = items == 1 ? embed_place_kernel<O, 1> : embed_place_kernel<O, 4>;
@@ -600,7 +640,7 @@ hipError_t sort_many_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&ke
     embed_keys_kernel<<<grid, kSortBlock, 0, stream>>>(p);
     hipError_t e = done(stream);
     if (e != hipSuccess) return e;
-    if (p.occurs) {
+    if (p.clear) {
         p.keys = keys[0];
         timing_before(stream, RS_KERNEL_EMBED_SORT);
         embed_mark_kernel<<<grid, kSortBlock, 0, stream>>>(p);
@@ -650,7 +690,8 @@ hipError_t embed_grad_of(const EmbedGradArgs& a, void* temp, hipStream_t stream)
     p.vocab = a.vocab;
     p.counts = static_cast<uint32_t*>(sort);
     const bool fill = !a.accumulate && few_tokens(a.n, a.vocab);
-    p.occurs = a.accumulate || fill ? nullptr : occurs;
+    p.occurs = occurs;
+    p.clear = !a.accumulate && !fill;
     if (a.n > 0) {
         int last = 1;
         const hipError_t e = own_sort(a.n) ? sort_tokens<O>(a, p, keys, at, z, fill, &last, stream)
@@ -658,7 +699,7 @@ hipError_t embed_grad_of(const EmbedGradArgs& a, void* temp, hipStream_t stream)
         if (e != hipSuccess) return e;
         s.keys = keys[last];
         s.at = at[last];
-        z.occurs = p.occurs;
+        z.occurs = p.clear ? occurs : nullptr;
     }
     z.first = z.last;   // what the sort's launches did not fill
     z.last = a.accumulate ? z.first : a.vocab;   // nothing, where all of them were

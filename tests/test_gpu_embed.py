@@ -256,3 +256,21 @@ def test_rows_without_tokens(n, vocab, width):
     want = torch.zeros(vocab + 1, width, device=DEV)
     want.index_add_(0, on(np.where(ids < 0, vocab, ids)).long(), on(x))
     assert torch.equal(out, want[:vocab].bfloat16())
+
+
+@pytest.mark.parametrize("n", [1025, 2048, 7000, 16384, 16385])
+@pytest.mark.parametrize("vocab", [5, 1000, 1025, 3000])
+@pytest.mark.parametrize("skew", [0.0, 1.0, 100.0])
+def test_tiles_that_count_for_themselves(n, vocab, skew):
+    """Several tiles, one and two passes, tokens evenly spread, by a power law, and all the same but a few."""
+    print("tiles", n, vocab, skew, flush=True)
+    rng = np.random.default_rng(n + vocab)
+    law = np.arange(1, vocab + 1, dtype=np.float64) ** -skew
+    ids = rng.permutation(vocab)[rng.choice(vocab, n, p=law / law.sum())].astype(np.int32)
+    ids[rng.integers(0, n, 5)] = [-1, vocab, 0, vocab - 1, 2]
+    x = rng.integers(-8, 9, (n, 6)).astype(np.float32)
+    out = torch.full((vocab, 6), float("nan"), dtype=torch.float32, device=DEV)
+    rs.embed_tokens_grad(on(x).bfloat16(), on(ids), vocab, out=out)
+    want = np.zeros((vocab + 1, 6))
+    np.add.at(want, np.where((ids >= 0) & (ids < vocab), ids, vocab), x)
+    assert np.array_equal(out.cpu().numpy(), want[:vocab])
