@@ -13,10 +13,10 @@
 // tokens that occur, and the other rows are filled beside the sums (looking a row's
 // mark up costs a tenth of the filling's rate).
 //
-// What bounds it: 131072 rows of 2048 bf16 and 16384 tokens take 131 us, of which
-// the sort's four launches with the filling are 101 (512 MB, 5.2 TB/s), the sums 23,
+// What bounds it: 131072 rows of 2048 bf16 and 16384 tokens take 124 us, of which
+// the sort's two launches with the filling are 97 (512 MB, 5.5 TB/s), the sums 22,
 // the join 7; 32003 rows of 1001 f32 and 50021 tokens 85: the sort 21, the sums and
-// zeros 60 (4.8 TB/s), the join 9.  Rows by token: 32768 of 5120 f16 94 us (4.8 TB/s).
+// zeros 60 (4.8 TB/s), the join 9.  Rows by token: 32768 of 5120 f16 91 us (4.9 TB/s).
 #include "internal.hpp"
 #include "move_common.hpp"
 
@@ -107,10 +107,23 @@ struct Zeros {
     uint32_t first, last, width, each, lanes_log2;
 };
 
+// All rows first .. last of a table without gaps, a store for each lane: plain fills of
+// 1 GB reach 6.9 TB/s so and 6.0 with four stores a lane; beside the sort of 1000
+// tokens 512 MB take 103 us for 108.
+template <class O>
+__device__ __forceinline__ void zero_flat(const Zeros& z, uint64_t wave) {
+    constexpr int V = kVec<O>;
+    const uint64_t at = static_cast<uint64_t>(z.first) * z.width + (wave * kWave + lane_id()) * V;
+    const uint64_t end = static_cast<uint64_t>(z.last) * z.width;
+    const float zero[V] = {};
+    if (at < end) store_some<V>(static_cast<O*>(z.table) + at, end - at < V ? static_cast<uint32_t>(end - at) : V, zero);
+}
+
 template <class O>
 __device__ __forceinline__ void zero_rows(const Zeros& z, uint64_t wave) {
     constexpr int V = kVec<O>;
     const uint32_t lane = lane_id();
+    if (z.occurs == nullptr && z.stride == z.width) return zero_flat<O>(z, wave);
     const uint64_t row0 = z.first + wave * z.each;
     if (row0 >= z.last) return;
     const uint32_t n = z.last - row0 < z.each ? z.last - static_cast<uint32_t>(row0) : z.each;
@@ -124,6 +137,13 @@ __device__ __forceinline__ void zero_rows(const Zeros& z, uint64_t wave) {
         for (uint64_t c = (lane & ((1u << z.lanes_log2) - 1)) * V; c < z.width; c += static_cast<uint64_t>(V) << z.lanes_log2)
             store_some<V>(to + c, z.width - static_cast<uint32_t>(c), zero);
     }
+}
+
+// Waves for rows first .. last.
+template <class O>
+uint64_t zero_waves(const Zeros& z) {
+    const uint64_t rows = z.last - z.first;
+    return z.occurs == nullptr && z.stride == z.width ? up(rows * z.width, kWave * kVec<O>) : up(rows, z.each);
 }
 
 // ---- the sort -----------------------------------------------------------------------------
@@ -597,7 +617,7 @@ hipError_t sort_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&keys)[2
         z.first = z.last;
         const uint64_t rows = fill ? up(a.vocab - z.first, launches--) : 0;
         z.last += static_cast<uint32_t>(rows);
-        return static_cast<uint32_t>(up(up(rows, z.each), kSortWaves));
+        return static_cast<uint32_t>(up(zero_waves<O>(z), kSortWaves));
     };
     for (uint32_t k = 0; k < passes; ++k) {
         p.shift = k * each_bits;
@@ -656,7 +676,7 @@ template <class T, class O, int L>
 hipError_t sum_tokens(const EmbedGradArgs& a, Sorted s, const Zeros& z, hipStream_t stream) {
     const uint64_t pieces = up(a.n, s.piece);
     const uint32_t sums = static_cast<uint32_t>(up(pieces * s.chunks, kMoveBlock / L));
-    const uint32_t fill = static_cast<uint32_t>(up(up(z.last - z.first, z.each), kMoveWaves));
+    const uint32_t fill = static_cast<uint32_t>(up(zero_waves<O>(z), kMoveWaves));
     hipError_t e = hipSuccess;
     if (sums + fill > 0) {
         timing_before(stream, RS_KERNEL_EMBED_SUM);
