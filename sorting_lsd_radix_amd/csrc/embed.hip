@@ -83,7 +83,7 @@ template <class T, bool SCALED>
 hipError_t embed_of(const EmbedArgs& a, hipStream_t stream) {
     const uint32_t vectors = static_cast<uint32_t>(up(a.width, kVec<T>));
     timing_before(stream, RS_KERNEL_EMBED);
-    if (vectors <= 32) {
+    if (vectors <= 32) {   // 32768 rows of 32: 6.9 us, a wave each 7.9
         const uint32_t lanes = vectors <= 4 ? 4 : vectors <= 16 ? 16 : 32;
         const auto kernel = lanes == 4 ? embed_narrow_kernel<T, 4, SCALED> : lanes == 16 ? embed_narrow_kernel<T, 16, SCALED>
                                                                                          : embed_narrow_kernel<T, 32, SCALED>;

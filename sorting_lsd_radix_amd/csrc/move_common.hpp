@@ -116,7 +116,9 @@ __device__ __forceinline__ AnyVec<16>::V scaled(AnyVec<16>::V r, float w) {
 inline bool large(uint64_t bytes) { return bytes > (uint64_t{96} << 20); }
 
 // How rows are split among waves: vectors of a lane (1, 2 or 4, up to `most`, so
-// many that the parts still fill the chip), and parts of a row.
+// many that the parts still fill the chip), and parts of a row.  32768 rows of 640
+// vectors by token: 122 us with one, 92 with two, 96 with four; 3001 rows of 251 to 5
+// places each: 15.0 with one, 13.7 with two; 16384 of 512 to 8: 302, 297 and 285.
 struct Split {
     uint32_t unroll, parts;
 };
