@@ -145,6 +145,12 @@ uint64_t zero_waves(const Zeros& z) {
     const uint64_t rows = z.last - z.first;
     return z.occurs == nullptr && z.stride == z.width ? up(rows * z.width, kWave * kVec<O>) : up(rows, z.each);
 }
+// Rows whose zeros are at most `waves` waves' work.  A grid's 2^26 waves have 2^32
+// lanes and a row at most 2^28 vectors, so there are some.
+template <class O>
+uint64_t zero_rows_of(const Zeros& z, uint64_t waves) {
+    return z.occurs == nullptr && z.stride == z.width ? waves * (kWave * kVec<O>) / z.width : waves * z.each;
+}
 
 // ---- the sort -----------------------------------------------------------------------------
 //
@@ -157,6 +163,7 @@ constexpr int kSortBlock = 1024;
 constexpr int kSortWaves = kSortBlock / kWave;
 constexpr uint32_t kMaxBits = 10;
 constexpr uint32_t kMaxTiles = 128;   // each block sums the counts of all tiles
+constexpr uint32_t kMaxSortGrid = (1u << 22) - 1;   // blocks: a grid dimension holds less than 2^32 work items
 
 struct Pass {
     const uint32_t* keys;   // the tokens in the first pass
@@ -612,11 +619,14 @@ hipError_t sort_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&keys)[2
     const bool counts = p.tiles > (fill ? 16u : 4u) || (p.tiles > 1 && passes == 1 && marks);
     uint32_t* const tile_counts = p.counts;
     uint32_t launches = passes * (counts ? 2 : 1);
-    // the next rows to be filled beside a launch: their blocks, and their end in z
+    // the next rows to be filled beside a launch, no more than its grid holds: their
+    // blocks, and their end in z
     auto beside = [&] {
         z.first = z.last;
-        const uint64_t rows = fill ? up(a.vocab - z.first, launches--) : 0;
-        z.last += static_cast<uint32_t>(rows);
+        const uint64_t left = fill ? a.vocab - z.first : 0, share = launches > 1 ? up(left, launches) : left;
+        const uint64_t most = zero_rows_of<O>(z, uint64_t{kMaxSortGrid - kMaxTiles} * kSortWaves);
+        if (launches > 1) --launches;
+        z.last += static_cast<uint32_t>(share < most ? share : most);
         return static_cast<uint32_t>(up(zero_waves<O>(z), kSortWaves));
     };
     for (uint32_t k = 0; k < passes; ++k) {
@@ -646,6 +656,15 @@ hipError_t sort_tokens(const EmbedGradArgs& a, Pass p, uint32_t* const (&keys)[2
         const hipError_t e = done(stream);
         if (e != hipSuccess) return e;
         *last = k & 1;
+    }
+    // of a table past 64 GB a launch, the rest: by itself, since the sums write rows
+    p.tiles = 0;
+    while (fill && z.last < a.vocab) {
+        const uint32_t more = beside();
+        timing_before(stream, RS_KERNEL_EMBED_SORT);
+        embed_count_kernel<O, 1><<<dim3(more), kSortBlock, 0, stream>>>(p, z);
+        const hipError_t e = done(stream);
+        if (e != hipSuccess) return e;
     }
     return hipSuccess;
 }
