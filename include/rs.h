@@ -594,8 +594,9 @@ rs_status rs_embed_tokens_grad(rs_elem_type elem_type, const void *dout, uint64_
  *     presence[r]);
  *   if the row's bias lists v: l + its bias, of the last entry that names v;
  *   if the mask has v's bit clear: -inf, whatever l is.
- * out gets l rounded to out_type once.  (The quotient is a product with the
- * inverse, two roundings, where |repetition[r]| is within 2^-100 .. 2^100.)
+ * out gets l rounded to out_type once.  (The quotient, too, is rounded once,
+ * but for what is within 2^-22 of a step of the middle between two numbers; of
+ * l below 2^-100 it may be off by two steps.)
  *   history [rows, history_len] tokens of row r, the first lengths[r] of them
  *     (NULL: all; below 0 is 0, above history_len history_len), of which the
  *     first prompt_lengths[r] (NULL: none) are the prompt; tokens of `vocab` or

@@ -96,14 +96,21 @@ __global__ __launch_bounds__(kAdjustBlock) void adjust_kernel(AdjustArgs a, uint
     constexpr uint32_t kPrompt = 1u << (kBits % 64 - 1) % 32, kBiased = kPrompt >> 1;
     __shared__ uint32_t s_token[kLooked ? kSlots : 1], s_entry[kLooked ? kSlots : 1];
     __shared__ float s_bias[kLooked ? kSlots : 1];
-    // a division is a product with the inverse, two roundings for one, unless that may
-    // be inexact, infinite or 0 (`divide`)
+    // A division is a product with the inverse and what that leaves times the inverse
+    // again: off by half a step and 2^-22 of one at most, for logits from 2^-100 on (below,
+    // by two steps at most).  Where that is NaN, l is divided: for what is infinite, and for
+    // penalties whose inverse may be inexact, infinite or 0, which is NaN itself.  (The product
+    // alone, 1.5 steps: 256 rows of 131072 with histories up to 8192 41.6 us for 42.2.)
     float by = 1.0f, inverse = 1.0f, frequency = 0.0f, presence = 0.0f;
-    bool divide = false;
     // a logit of a token that the history holds `count` times behind the prompt
     auto penalised = [&](float l, bool seen, uint32_t count) {
-        const float scaled = l * (l > 0.0f ? inverse : by);
-        if (seen) l = divide && l > 0.0f ? l / by : scaled;
+        const bool up = l > 0.0f;
+        float scaled = l * (up ? inverse : by);
+        if (up) {
+            scaled = fmaf(fmaf(-scaled, by, l), inverse, scaled);
+            if (scaled != scaled) scaled = l / by;
+        }
+        if (seen) l = scaled;
         return l - (count > 0 ? fmaf(frequency, static_cast<float>(count), presence) : 0.0f);
     };
     if constexpr (MARKS != kNoMarks) {
@@ -127,8 +134,7 @@ __global__ __launch_bounds__(kAdjustBlock) void adjust_kernel(AdjustArgs a, uint
             if (a.repetition) by = a.repetition[r];
             if (a.frequency) frequency = a.frequency[r];
             if (a.presence) presence = a.presence[r];
-            inverse = 1.0f / by;
-            divide = !(fabsf(by) >= 0x1p-100f && fabsf(by) <= 0x1p100f);
+            inverse = fabsf(by) >= 0x1p-100f && fabsf(by) <= 0x1p100f ? 1.0f / by : __builtin_nanf("");
         }
         for (uint32_t i = tid; i < kVectors; i += kAdjustBlock) s_marks[i] = u32x4{0, 0, 0, 0};
         if constexpr (kLooked) {
@@ -213,6 +219,7 @@ __global__ __launch_bounds__(kAdjustBlock) void adjust_kernel(AdjustArgs a, uint
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const uint32_t w = MARKS == kMarks16 ? m[j / 2] >> (j % 2 * 16) & 0xFFFFu : m[j];
+                    if (w == 0) continue;   // of all lanes: 256 rows of 131072, histories up to 500, 25.6 us for 27.8
                     l[j] = penalised(l[j], (w & ~kBiased) != 0, w & (kBiased - 1));
                     if (w & kBiased) l[j] += bias_of(i + j);
                 }
