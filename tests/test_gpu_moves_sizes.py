@@ -1,11 +1,12 @@
 """The calls that move rows by index at sizes where their launches or forms change."""
 import gc
 
+import numpy as np
 import pytest
 import torch
 
 import sorting_lsd_radix_amd as rs
-from rows_helpers import DEV
+from rows_helpers import DEV, DTYPES
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +31,51 @@ def test_table_past_one_grid():
     del out, x
     gc.collect()
     torch.cuda.empty_cache()
+
+
+def some_tokens(kind, n, vocab, seed):
+    """"law": by a power law; "one": three quarters of them the same; "runs": each some hundred times.  All with a
+    twentieth outside the table."""
+    rng = np.random.default_rng(seed)
+    ids = np.minimum(rng.zipf(1.3, n) - 1, vocab - 1) if kind == "law" else rng.integers(0, max(1, min(vocab, n // 300)), n)
+    if kind == "one":
+        ids = np.where(rng.random(n) < 0.75, vocab - 1, rng.integers(0, vocab, n))
+    ids = rng.permutation(vocab)[ids].astype(np.int32)
+    out = rng.random(n) < 0.05
+    ids[out] = rng.choice([-1, vocab, 2 ** 31 - 1], out.sum())
+    return torch.from_numpy(ids).to(DEV)
+
+
+# tokens, rows, width, dtype, elements between rows; a wave takes 64 vectors of 16 bytes of 8, 16, 32 or 64 positions
+WIDE = [
+    (3001, 900, 1031, "bf16", 1), (6000, 70, 515, "f32", 0), (16400, 5000, 2051, "f16", 0), (20003, 100000, 2048, "bf16", 8),
+    (16400, 300, 4099, "bf16", 0), (40000, 32003, 1001, "f32", 0), (50021, 3000, 1501, "f32", 3), (140000, 20000, 1040, "f16", 0),
+    (524290, 4000, 522, "bf16", 2),
+]
+
+
+@pytest.mark.parametrize("kind", ["law", "one", "runs"])
+@pytest.mark.parametrize("shape", WIDE)
+def test_wide_rows_of_tokens_in_many_pieces(shape, kind):
+    """Whole numbers, whose sums are exact in f32, in rows of several waves: tokens of one piece and of
+    hundreds, pieces of every length, every size of the sort; into both types, given and added to."""
+    print("wide rows", shape, kind, flush=True)
+    n, vocab, width, dtype, pad = shape
+    ids = some_tokens(kind, n, vocab, n + vocab)
+    g = torch.Generator(device=DEV).manual_seed(n)
+    x = torch.randint(-4, 5, (n, width + pad), generator=g, device=DEV, dtype=torch.int8).to(DTYPES[dtype])[:, :width]
+    inside = (ids >= 0) & (ids < vocab)
+    want = torch.zeros(vocab + 1, width, device=DEV)
+    want.index_add_(0, torch.where(inside, ids, vocab).long(), x.float())
+    want = want[:vocab] * -2
+    assert float(want.abs().max()) < 2 ** 23
+    for to in {DTYPES[dtype], torch.float32}:
+        whole = torch.full((vocab, width + pad), float("nan"), dtype=to, device=DEV)
+        out = whole[:, :width]
+        rs.embed_tokens_grad(x, ids, vocab, scale=-2.0, out=out)
+        assert torch.equal(out, want.to(to)), to
+        old = torch.randint(-100, 101, (vocab, width), generator=g, device=DEV, dtype=torch.int8).to(to)
+        out.copy_(old)
+        rs.embed_tokens_grad(x, ids, vocab, scale=-2.0, out=out, accumulate=True)
+        assert torch.equal(out, (old.float() + want).to(to)), to
+        assert whole[:, width:].isnan().all()
