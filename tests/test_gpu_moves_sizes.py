@@ -79,3 +79,23 @@ def test_wide_rows_of_tokens_in_many_pieces(shape, kind):
         rs.embed_tokens_grad(x, ids, vocab, scale=-2.0, out=out, accumulate=True)
         assert torch.equal(out, (old.float() + want).to(to)), to
         assert whole[:, width:].isnan().all()
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("rows,top_k,width,dtype", [(8400, 3, 2051, "bf16"), (9000, 12, 520, "f16"), (5100, 5, 1001, "f32")])
+def test_combining_past_the_caches(rows, top_k, width, dtype, weighted):
+    """So many rows that they are read around the caches; whole numbers times powers of two, whose sums are exact."""
+    print("combine past the caches", rows, top_k, width, dtype, weighted, flush=True)
+    assert rows * top_k * width * (4 if dtype == "f32" else 2) > 96 << 20
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    ids = torch.randint(-1, 40, (rows, top_k), generator=g, device=DEV).int()
+    order, place, _, _ = rs.group_choices(ids, 40, align=16)
+    y = torch.randint(-4, 5, (order.numel(), width), generator=g, device=DEV, dtype=torch.int8).to(DTYPES[dtype])
+    w = 2.0 ** torch.randint(-2, 3, (rows, top_k), generator=g, device=DEV).float() if weighted else None
+    y[order < 0] = float("nan")   # padding: not read
+    want = torch.zeros(rows, width, device=DEV)
+    for j in range(top_k):
+        p = place[:, j].long()
+        part = torch.where((p >= 0)[:, None], y[p.clamp(min=0)].float(), 0.0)
+        want += part if w is None else part * w[:, j:j + 1]
+    assert torch.equal(rs.combine_choices(y, place, weights=w), want.to(DTYPES[dtype]))
