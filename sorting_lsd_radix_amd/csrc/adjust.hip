@@ -42,7 +42,6 @@ __device__ __forceinline__ uint32_t within(const int32_t* n, uint32_t r, uint32_
 }
 
 constexpr int kTokens = 4;   // of a vector load
-constexpr int kAhead = 1;    // vectors of history in flight while one is marked
 typedef uint32_t Tokens __attribute__((ext_vector_type(kTokens), aligned(4)));
 
 // Tokens i .. i + 4 of `length`; what is behind them is no token.
@@ -115,13 +114,9 @@ __global__ __launch_bounds__(kAdjustBlock) void adjust_kernel(AdjustArgs a, uint
     };
     if constexpr (MARKS != kNoMarks) {
         const uint32_t* history = a.history + r * a.history_stride;
-        constexpr uint32_t kRound = kAdjustBlock * kTokens * kAhead;
-        Tokens next[kAhead];
-        auto load = [&](uint32_t i0) {
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) next[k] = load_tokens(history, i0 + (k * kAdjustBlock + tid) * kTokens, a.history_len);
-        };
-        load(0);   // before the length is known
+        constexpr uint32_t kRound = kAdjustBlock * kTokens;
+        // a round ahead, the first before the length is known
+        Tokens next = load_tokens(history, tid * kTokens, a.history_len);
         const uint32_t length = a.history ? within(a.lengths, r, a.history_len, a.history_len) : 0u;
         const uint32_t prompt = within(a.prompt_lengths, r, 0u, length);
         uint32_t token = ~0u;   // of this thread's bias entry
@@ -169,27 +164,22 @@ __global__ __launch_bounds__(kAdjustBlock) void adjust_kernel(AdjustArgs a, uint
             __syncthreads();   // nothing is above the entries yet
         }
         for (uint32_t i0 = 0; i0 < length; i0 += kRound) {
-            Tokens now[kAhead];
+            const Tokens now = next;
+            const uint32_t i = i0 + tid * kTokens;
+            if (i0 + kRound < length) next = load_tokens(history, i + kRound, a.history_len);
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) now[k] = next[k];
-            if (i0 + kRound < length) load(i0 + kRound);
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const uint32_t i = i0 + (k * kAdjustBlock + tid) * kTokens;
-#pragma unroll
-                for (int j = 0; j < kTokens; ++j) {
-                    const uint32_t v = now[k][j] - lo;   // a token that is none lies behind every slice
-                    if (v >= size || i + j >= length) continue;
-                    const bool before = i + j < prompt;
-                    if constexpr (MARKS == kMarks64) {
-                        if (before) atomicOr(&s_word[v], kPrompt64);
-                        else atomicAdd(&s_word[v], kOne);
-                    } else {
-                        uint32_t* mark = &s_mark[MARKS == kMarks16 ? v / 2 : v];
-                        const uint32_t shift = MARKS == kMarks16 ? v % 2 * 16 : 0;
-                        if (before) atomicOr(mark, kPrompt << shift);
-                        else atomicAdd(mark, 1u << shift);
-                    }
+            for (int j = 0; j < kTokens; ++j) {
+                const uint32_t v = now[j] - lo;   // a token that is none lies behind every slice
+                if (v >= size || i + j >= length) continue;
+                const bool before = i + j < prompt;
+                if constexpr (MARKS == kMarks64) {
+                    if (before) atomicOr(&s_word[v], kPrompt64);
+                    else atomicAdd(&s_word[v], kOne);
+                } else {
+                    uint32_t* mark = &s_mark[MARKS == kMarks16 ? v / 2 : v];
+                    const uint32_t shift = MARKS == kMarks16 ? v % 2 * 16 : 0;
+                    if (before) atomicOr(mark, kPrompt << shift);
+                    else atomicAdd(mark, 1u << shift);
                 }
             }
         }

@@ -350,8 +350,6 @@ void pick(bool whether, Call call) {
     else call(std::false_type{});
 }
 
-uint64_t up(uint64_t n, uint64_t d) { return (n + d - 1) / d; }
-
 // Positions that a wave fills: few where there is padding, which is all that it
 // writes, many where there is none and it only looks.  131072 choices in 163584
 // positions of 4096 bf16 elements: 295 us with 4, 305 with 16; without padding, 15005

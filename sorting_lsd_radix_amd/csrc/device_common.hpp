@@ -85,6 +85,23 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// The rank of this lane's digit d, of `bits` bits, among the equal ones of the wave's
+// real lanes: those of earlier calls, counted at `count` by digit, and the lower
+// lanes', found by a ballot for each bit.  Counts these.
+__device__ __forceinline__ uint32_t rank_among(uint16_t* count, bool real, uint32_t d, uint32_t bits) {
+    uint64_t peers = ballot(real);
+    for (uint32_t b = 0; b < bits; ++b) {
+        const uint64_t ones = ballot((d >> b) & 1u);
+        peers &= ((d >> b) & 1u) ? ones : ~ones;
+    }
+    const uint32_t below = count_below(peers);
+    const uint32_t rank = real ? count[d] + below : 0u;
+    wave_fence();   // all peers have read before the last of them writes
+    if (real && below + 1 == static_cast<uint32_t>(__builtin_popcountll(peers))) count[d] = static_cast<uint16_t>(rank + 1);
+    wave_fence();
+    return rank;
+}
+
 // The value of lane ^ M: DPP quad permutes for 1 and 2, a row rotate for 8,
 // swizzles for 4 and 16, a lane permute for 32.
 template <int M>

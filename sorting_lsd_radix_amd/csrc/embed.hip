@@ -24,14 +24,11 @@ namespace rs {
 
 namespace {
 
-
 hipError_t done(hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     timing_after(stream);
     return e;
 }
-
-uint64_t up(uint64_t n, uint64_t d) { return (n + d - 1) / d; }
 
 // ---- rows by token ------------------------------------------------------------------
 
@@ -156,8 +153,7 @@ uint64_t zero_rows_of(const Zeros& z, uint64_t waves) {
 //
 // A stable counting sort by digits of up to 10 bits, lowest first.  A block
 // ranks a tile of keys as group.hip does: wave w holds the w-th run of 64 ITEMS
-// keys, 64 a row, and a key's rank among its digit's in the wave is the count
-// of earlier rows plus the peers in lower lanes, found by a ballot for each bit.
+// keys, 64 a row, which it ranks row by row.
 
 constexpr int kSortBlock = 1024;
 constexpr int kSortWaves = kSortBlock / kWave;
@@ -284,17 +280,7 @@ __global__ __launch_bounds__(kSortBlock) void embed_place_kernel(Pass p, Zeros z
     for (int j = 0; j < ITEMS; ++j) {
         const bool real = key[j] != ~0u;
         const uint32_t d = (key[j] >> p.shift) & (bins - 1);
-        uint64_t peers = ballot(real);
-        for (uint32_t b = 0; b < p.bits; ++b) {
-            const uint64_t ones = ballot((d >> b) & 1u);
-            peers &= ((d >> b) & 1u) ? ones : ~ones;
-        }
-        const uint32_t below = count_below(peers);
-        rank[j] = real ? s_count[wave][d] + below : 0u;
-        wave_fence();   // all peers have read before the last of them writes
-        if (real && below + 1 == static_cast<uint32_t>(__builtin_popcountll(peers)))
-            s_count[wave][d] = static_cast<uint16_t>(rank[j] + 1);
-        wave_fence();
+        rank[j] = rank_among(s_count[wave], real, d, p.bits);
     }
     __syncthreads();
     uint32_t before = 0, total = 0;

@@ -3,10 +3,9 @@
 //
 // A block ranks a tile of choices: wave w holds the w-th run of 64 ITEMS
 // choices in registers, 64 a row, so that (wave, row, lane) is input order.  A
-// choice's rank among its expert's in the wave is the wave's count of earlier
-// rows plus the peers in lower lanes, found by a ballot for each bit of the
-// expert's number; sums over waves, tiles and experts give its place.  Nothing
-// depends on the order in which blocks or atomics run.
+// choice's rank among its expert's in the wave, found row by row, and sums over
+// waves, tiles and experts give its place.  Nothing depends on the order in
+// which blocks or atomics run.
 //
 //  * One tile: one launch does it all.
 //  * Up to kShortSum counts (tiles * experts): two launches.  Every tile
@@ -179,17 +178,7 @@ __global__ __launch_bounds__(kGroupBlock) void group_place_kernel(GroupArgs a, u
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
         const bool real = e[j] < a.experts;
-        uint64_t peers = ballot(real);
-        for (uint32_t b = 0; b < bits; ++b) {
-            const uint64_t ones = ballot((e[j] >> b) & 1u);
-            peers &= ((e[j] >> b) & 1u) ? ones : ~ones;
-        }
-        const uint32_t below = count_below(peers);
-        rank[j] = real ? s_count[e[j]] + below : 0u;
-        wave_fence();   // all peers have read before the last of them writes
-        if (real && below + 1 == static_cast<uint32_t>(__builtin_popcountll(peers)))
-            s_count[e[j]] = static_cast<uint16_t>(rank[j] + 1);
-        wave_fence();
+        rank[j] = rank_among(s_count, real, e[j], bits);
     }
     __syncthreads();
     uint32_t before = 0, total = 0;

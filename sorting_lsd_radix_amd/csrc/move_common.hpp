@@ -64,15 +64,10 @@ struct RowPart {
             r[u] = ONCE ? __builtin_nontemporal_load(from) : *from;
         }
     }
-    template <bool ONCE = false>
     __device__ __forceinline__ void store(T* row, const Vec (&r)[U]) const {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (!real[u]) continue;
-            Vec* to = reinterpret_cast<Vec*>(row + at[u]);
-            if (ONCE) __builtin_nontemporal_store(r[u], to);
-            else *to = r[u];
-        }
+        for (int u = 0; u < U; ++u)
+            if (real[u]) *reinterpret_cast<Vec*>(row + at[u]) = r[u];
     }
 };
 
@@ -107,6 +102,8 @@ __device__ __forceinline__ AnyVec<16>::V scaled(AnyVec<16>::V r, float w) {
     for (int j = 0; j < kVec<T>; ++j) x[j] *= w;
     return narrow<T>(x);
 }
+
+inline uint64_t up(uint64_t n, uint64_t d) { return (n + d - 1) / d; }
 
 // Whether rows that are read once are read past the caches, which hold 256 MB on
 // the package: combining a router's rows, others in between, takes at 64 MB 12.7 us
