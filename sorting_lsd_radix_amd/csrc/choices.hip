@@ -351,11 +351,15 @@ void pick(bool whether, Call call) {
 }
 
 // Positions that a wave fills: few where there is padding, which is all that it
-// writes, many where there is none and it only looks.  131072 choices in 163584
-// positions of 4096 bf16 elements: 295 us with 4, 305 with 16; without padding, 15005
-// positions of 1001 f32: 16.8 us with 4, 15.8 with 16; 2176 positions, most of them
-// padding: 5.5 us with 4, 6.7 with 16.
-uint32_t fill_each(uint64_t room, uint64_t choices) { return room > choices + choices / 16 ? 4 : 16; }
+// writes, many where there is none and it only looks.  Gathering, whose filling is
+// behind the rows: with padding, 131072 choices in 163584 positions of 4096 bf16 281 us with
+// 4 and 284 with 16, 16384 in 16504 of 1024 f16 10.8 and 13.4, 2000 in 2112 of 2048 bf16 4.3 and 6.1;
+// without, 15005 of 1001 f32 13.5 and 13.0, 24000 of 1024 f16 13.3 and 12.9.
+uint32_t fill_each(uint64_t room, uint64_t choices) { return room > choices ? 4 : 16; }
+// In front of the products, few only where much is padding: 80000 choices in 80448
+// positions of 512 bf16 58.7 us with 4 and 56.2 with 16 (with the combining), 16384 in 16504 of 1024 f16
+// 25.4 and 26.0, 49152 in 53184 of 2048 f16 140.8 and 139.3.
+uint32_t fill_each_in_front(uint64_t room, uint64_t choices) { return fill_each(room, choices + choices / 16); }
 
 // call(lanes a row) of a narrow row.
 template <class Call>
@@ -417,7 +421,7 @@ hipError_t products_of(const CombineArgs& a, const GatherArgs& g, hipStream_t st
         });
     const uint32_t waves = vectors <= kWave ? 1 : vectors <= 2 * kWave ? 2 : 4;   // of a row; 8192 rows of 256 vectors: 146 us with 4, 160 with 1
     const uint32_t parts = static_cast<uint32_t>(up(vectors, 4 * kWave));
-    const uint32_t each = fill_each(g.room, static_cast<uint64_t>(a.rows) * a.top_k);
+    const uint32_t each = fill_each_in_front(g.room, static_cast<uint64_t>(a.rows) * a.top_k);
     const uint32_t fill = SUM ? 0 : static_cast<uint32_t>(up(up(g.room, each) * parts, kMoveWaves));
     return timed(RS_KERNEL_COMBINE, stream, [&] {
         pick(a.top_k > kBatch, [&](auto many) {
