@@ -9,8 +9,8 @@
 // maxima, so the order of the atomics does not matter.  Every block of a row reads
 // the row's whole lists, from the caches.
 //
-// What bounds it: 256 rows of 131072 bf16 take 25 us without lists (5.3 TB/s), 28 with
-// histories of up to 500 tokens, 41 with up to 8192 and 300 biases, where the marking's
+// What bounds it: 256 rows of 131072 bf16 take 25 us without lists (5.3 TB/s), 26 with
+// histories of up to 500 tokens, 42 with up to 8192 and 300 biases, where the marking's
 // instructions and atomics keep the VALU two thirds busy.
 #include <type_traits>
 

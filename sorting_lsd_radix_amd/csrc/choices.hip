@@ -5,17 +5,17 @@
 //
 // The row of a token is read once: a wave takes a part of it and writes it to all
 // its choices' positions, or sums its choices' rows, eight in flight.  (A wave for
-// each position instead reads a row top_k times, from the caches: 333 us against 282
-// for 131072 choices of 4096 bf16.)  A choice's wave writes a position if order and
-// place name each other there, waves behind look for the other positions; so each is
-// written once, as order has it, whatever place holds.  Sums and products are f32
-// in the order of j, products by lanes and then waves: nothing depends on the order
-// in which blocks run.
+// each position instead reads a row top_k times, from the caches: 333 us for 131072
+// choices of 4096 bf16, where a wave each row in an earlier form took 300.)  A choice's
+// wave writes a position if order and place name each other there, waves behind look
+// for the other positions; so each is written once, as order has it, whatever place
+// holds.  Sums and products are f32 in the order of j, products by lanes and then
+// waves: nothing depends on the order in which blocks run.
 //
 // What bounds it is memory: 16384 rows with 8 choices in 163584 positions of 4096
 // bf16 take 280 us to gather (5.3 TB/s; writes scattered over 256 segments reach 5.6
 // without anything else), 203 to combine (5.8 TB/s); 8192 with 6 of 2048 f16 46 to combine
-// and 100 for the gradients (4.8 TB/s).
+// and 100 for the gradients (4.5 TB/s).
 #include "internal.hpp"
 #include "move_common.hpp"
 
@@ -66,7 +66,7 @@ __device__ __forceinline__ bool owns(const uint32_t* order, uint32_t room, uint3
 
 // A wave for each part of a row, which it reads once and writes to all its
 // choices' positions; the waves behind write the other positions, `each` a wave (in
-// front of the rows' waves they took 131072 choices in 163584 positions of 4096 bf16 from 282 us to 297).
+// front of the rows' waves 131072 choices in 163584 positions of 4096 bf16 took 297 us for 282).
 template <class T, int U, bool WEIGHTS>
 __global__ __launch_bounds__(kMoveBlock) void gather_kernel(GatherArgs a, uint32_t parts, uint32_t each) {
     const uint32_t unit = block_id() * kMoveWaves + wave_id();
@@ -356,9 +356,10 @@ void pick(bool whether, Call call) {
 // 4 and 284 with 16, 16384 in 16504 of 1024 f16 10.8 and 13.4, 2000 in 2112 of 2048 bf16 4.3 and 6.1;
 // without, 15005 of 1001 f32 13.5 and 13.0, 24000 of 1024 f16 13.3 and 12.9.
 uint32_t fill_each(uint64_t room, uint64_t choices) { return room > choices ? 4 : 16; }
-// In front of the products, few only where much is padding: 80000 choices in 80448
-// positions of 512 bf16 58.7 us with 4 and 56.2 with 16 (with the combining), 16384 in 16504 of 1024 f16
-// 25.4 and 26.0, 49152 in 53184 of 2048 f16 140.8 and 139.3.
+// In front of the products (and with the combining, which is the same), few only where
+// much is padding: 80000 choices in 80448 positions of 512 bf16 58.7 us with 4 and 56.2 with 16,
+// 24000 in 24120 of 1024 41.7 and 40.8; 2000 in 6032 of 2048 12.1 and 14.1, 16000 in 22336 of
+// 1001 f32 54.3 and 54.2, 65536 in 98048 of 2048 bf16 207 and 205.
 uint32_t fill_each_in_front(uint64_t room, uint64_t choices) { return fill_each(room, choices + choices / 16); }
 
 // call(lanes a row) of a narrow row.

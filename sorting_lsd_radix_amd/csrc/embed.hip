@@ -13,10 +13,11 @@
 // tokens that occur, and the other rows are filled beside the sums (looking a row's
 // mark up costs a tenth of the filling's rate).
 //
-// What bounds it: 131072 rows of 2048 bf16 and 16384 tokens take 124 us, of which
-// the sort's two launches with the filling are 97 (512 MB, 5.5 TB/s), the sums 22,
-// the join 7; 32003 rows of 1001 f32 and 50021 tokens 85: the sort 21, the sums and
-// zeros 60 (4.8 TB/s), the join 9.  Rows by token: 32768 of 5120 f16 91 us (4.9 TB/s).
+// What bounds it: 131072 rows of 2048 bf16 and 16384 tokens take 125 us.  A trace, under
+// which launches take some 4 % longer, has 101 for the sort's two launches with the filling (512 MB, 5.3
+// TB/s), 23 for the sums, 7 for the join.  32003 rows of 1001 f32 and 50021 tokens take 85; the
+// trace has 21 for the sort, 61 for the sums and zeros (318 MB, 5.2 TB/s), 8 for the join.  Rows by
+// token: 32768 of 5120 f16 91 us (4.9 TB/s).
 #include "internal.hpp"
 #include "move_common.hpp"
 
@@ -550,8 +551,11 @@ __global__ __launch_bounds__(kJoinBlock) void embed_join_kernel(EmbedGradArgs a,
 
 uint32_t sort_items(uint64_t n) { return n <= kMaxTiles * kSortBlock ? 1 : 4; }
 bool own_sort(uint64_t n) { return n <= uint64_t{kMaxTiles} * kSortBlock * 4; }
-// Whether all rows are filled beside the sort.  131072 rows of 2048 bf16: with 32768
-// tokens 146 us, 156 filled by what occurs; with 65536 tokens 194 and 193.
+// Whether all rows are filled beside the sort, or beside the sums those that have no
+// token.  With a quarter as many tokens as rows, 131072 rows of 2048 bf16 take 149 us and 159, 32000
+// of 1001 f32 42.3 and 48.5, 8000 of 8192 bf16 40.8 and 43.3, 50000 of 512 f32 44.4 and 44.4,
+// 262144 of 64 f16 51.4 and 51.3; with half as many 186 and 192, 58.8 and 57.8, 53.6 and 54.9,
+// 52.5 and 51.0, 66.6 and 67.8: by then either may be ahead.
 bool few_tokens(uint64_t n, uint32_t vocab) { return own_sort(n) && n > 0 && n <= vocab / 4; }
 // Lanes that take a row's vectors of T, 64 for one of several chunks, and the chunks.
 struct Lanes {

@@ -113,9 +113,10 @@ inline uint64_t up(uint64_t n, uint64_t d) { return (n + d - 1) / d; }
 inline bool large(uint64_t bytes) { return bytes > (uint64_t{96} << 20); }
 
 // How rows are split among waves: vectors of a lane (1, 2 or 4, up to `most`, so
-// many that the parts still fill the chip), and parts of a row.  32768 rows of 640
-// vectors by token: 122 us with one, 92 with two, 96 with four; 3001 rows of 251 to 5
-// places each: 15.0 with one, 13.7 with two; 16384 of 512 to 8: 302, 297 and 285.
+// many that the parts still fill the chip), and parts of a row.  By token, at most two:
+// 32768 rows of 640 vectors 119 us with one, 91 with two, 95 with four; 100000 of 75 54.0, 41.5 and
+// 41.3; 8192 of 512 17.4, 18.0 and 19.3.  To places, at most four: 16384 rows of 512 to 8 places each 303, 291
+// and 281; 5000 of 1024 to 6 185, 165 and 166; 3001 of 251 to 5 13.1 each way.
 struct Split {
     uint32_t unroll, parts;
 };

@@ -32,9 +32,10 @@ def combine(y, place, w=None):
 
 
 def dots(x, y, place):
-    """(products of the rows of x with the rows of y at their choices, bound).  At least 8 lanes
-    share a row and at most 64 elements' distance of a lane's own follow each other in its sum: a
-    lane adds at most width / 64 + 16 products, the lanes and waves add up in at most 16 steps more."""
+    """(products of the rows of x with the rows of y at their choices, bound).  A wave or more shares a
+    row of more than 32 vectors of at most 8 elements, whose lanes add width / 64 + 8 products each at
+    most; 4 to 32 lanes share a shorter one, a vector each: 8 products.  The lanes and waves add up in at
+    most 16 steps more."""
     rows, k = place.shape
     out = np.zeros((rows, k))
     size = np.zeros_like(out)
