@@ -99,3 +99,35 @@ def test_combining_past_the_caches(rows, top_k, width, dtype, weighted):
         part = torch.where((p >= 0)[:, None], y[p.clamp(min=0)].float(), 0.0)
         want += part if w is None else part * w[:, j:j + 1]
     assert torch.equal(rs.combine_choices(y, place, weights=w), want.to(DTYPES[dtype]))
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,vocab,width", [(600000, 3000, 24), (20000, 200000, 520)])
+def test_replays_of_each_sort(n, vocab, width, accumulate):
+    """The gradient of more tokens than its own sort takes, and of few for a large table, in a graph that is
+    replayed with other work between: whole numbers, exact."""
+    print("replays", n, vocab, width, accumulate, flush=True)
+    x = torch.zeros(n, width, dtype=torch.bfloat16, device=DEV)
+    ids = torch.zeros(n, dtype=torch.int32, device=DEV)
+    out = torch.zeros(vocab, width, device=DEV)
+    size = rs.rs_embed_tokens_grad(rs.RS_ELEM_BF16, None, 0, None, n, vocab, width, 1.0, 0, rs.RS_ELEM_F32, None, 0, None, 0)
+    temp = torch.empty(size, dtype=torch.uint8, device=DEV)
+
+    def call():
+        rs.embed_tokens_grad(x, ids, vocab, out=out, accumulate=accumulate, temp=temp)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for i in range(4):
+        x.copy_(torch.randint(-8, 9, (n, width), device=DEV))
+        ids.copy_(torch.randint(-1, vocab, (n,), device=DEV))
+        temp.fill_(255 - i)
+        out.fill_(3.0)
+        want = torch.full((vocab + 1, width), 3.0 if accumulate else 0.0, device=DEV)
+        want.index_add_(0, torch.where(ids < 0, vocab, ids).long(), x.float())
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[:vocab]), i
